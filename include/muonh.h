@@ -81,7 +81,7 @@ enum {
   MUONH_EWORKSPACE = -3, /* workspace missing, too small or misaligned */
   MUONH_EHIP = -4,       /* a HIP runtime call failed (see muonh_last_error) */
   MUONH_ENOMEM = -5,     /* host allocation failed */
-  MUONH_EALIAS = -6      /* two of the W, G, M matrices overlap in memory */
+  MUONH_EALIAS = -6      /* two of the W, G, M matrices (or an fp8 call's arrays) overlap */
 };
 
 /* Newton-Schulz plan flags (at most one). Default: operands in bf16, bf16
@@ -321,6 +321,113 @@ int muonh_step_status(const muonh_plan* plan, const void* workspace, size_t work
  */
 int muonh_check_disjoint(const muonh_plan* plan, const void* const* W, const void* const* G,
                          const void* const* M);
+
+/*
+ * Block-scaled 8-bit matrices: the operands of the linear layers that a
+ * MuonH-trained model runs in E4M3 with a scale per block of 128 (model card
+ * "Puro", section "Training"; report page, part 6/7, section 4.3 "Cost
+ * Estimation", blockwise FP8: linear-layer products in FP8, master weights
+ * and optimizer state in FP32 or BF16). The pages give neither the rounding
+ * nor the scales' type; the readings here:
+ *   - codes: OCP e4m3 (sign, 4 exponent, 3 mantissa bits; largest 448,
+ *     smallest normal 2^-6, smallest 2^-9; NaN, no infinity);
+ *   - scales: E8M0, the byte b stands for 2^(b - 127). A block's scale is the
+ *     smallest power of two 2^e, e >= -126, with max|x| <= 448 * 2^e over the
+ *     block's finite entries (-126 where all are zero or none is finite), so
+ *     no entry overflows. x * 2^-e is exact, so a code is x / 2^e rounded
+ *     once, to the nearest e4m3 value, ties to even. NaN and infinities
+ *     become NaN codes and do not count for the maximum;
+ *   - blocks: MUONH_FP8_ROWS: 128 consecutive columns of one row (the last
+ *     one of a row may be shorter); MUONH_FP8_TILES: 128 x 128 entries (edge
+ *     tiles smaller).
+ * Storage of a rows x cols matrix: codes, row-major, row pitch
+ * muonh_fp8_ld(cols) = cols rounded up to 128 bytes, zeros in the columns
+ * past cols; scales, row-major, one row per matrix row (ROWS) or per 128
+ * matrix rows (TILES), muonh_fp8_scale_ld(cols) = ceil(cols/128) rounded up
+ * to a multiple of 4 bytes per row, zeros past ceil(cols/128). codes 16-byte,
+ * scales 4-byte aligned. Matrices without rows or columns are allowed.
+ */
+enum { MUONH_FP8_ROWS = 0, MUONH_FP8_TILES = 1 };
+enum { MUONH_DT_FP32 = 0, MUONH_DT_BF16 = 1 };
+#define MUONH_MAX_FP8_DIM (1 << 24) /* rows and cols of a block-scaled matrix */
+
+typedef struct {
+  const void* codes;  /* DEVICE, rows x muonh_fp8_ld(cols) bytes */
+  const void* scales; /* DEVICE, rows or ceil(rows/128) x muonh_fp8_scale_ld(cols) bytes */
+  int64_t rows, cols; /* in [0, MUONH_MAX_FP8_DIM] */
+  int32_t block;      /* MUONH_FP8_ROWS or MUONH_FP8_TILES */
+} muonh_fp8_matrix;
+
+/* Row pitches in bytes (0 for cols out of [0, MUONH_MAX_FP8_DIM]) and the
+ * number of scale rows. Host-only. */
+int64_t muonh_fp8_ld(int64_t cols);
+int64_t muonh_fp8_scale_ld(int64_t cols);
+int64_t muonh_fp8_scale_rows(int64_t rows, int32_t block);
+
+/*
+ * Quantize src (DEVICE, rows x cols of `dtype`, element (r, c) at
+ * r*src_ld + c, src_ld >= cols) into codes and scales, its own orientation,
+ * and/or codes_t and scales_t, the same for its transpose (cols x rows). Each
+ * pair is given whole or NULL, at least one of them given. With MUONH_FP8_ROWS
+ * the two forms group differently (along src's columns, and along its rows:
+ * a forward product contracts over features, a weight gradient over
+ * tokens); with MUONH_FP8_TILES they hold the same values. One pass over
+ * src. Deterministic; asynchronous on `stream`, capturable.
+ * Errors: MUONH_EINVAL (NULL or half-given pair, bad dtype or block, src_ld <
+ * cols or above 2^36, misaligned output), MUONH_ESHAPE (a dim out of range, or 2^24 tiles
+ * of 128 x 128 or more), MUONH_EALIAS (an output overlaps src or another
+ * output), MUONH_EHIP.
+ */
+int muonh_fp8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t src_ld,
+                       int32_t block, void* codes, void* scales, void* codes_t, void* scales_t,
+                       void* stream);
+
+/*
+ * Quantize every weight of a plan with MUONH_FP8_TILES, in grouped launches:
+ * what the forward product (codes, scales) and the data gradient (codes_t,
+ * scales_t, the transposed form) read after a step. W: DEVICE array of
+ * n_matrices DEVICE pointers, as for muonh_step; the others: DEVICE arrays of
+ * n_matrices DEVICE pointers to outputs in the storage above. codes_t and
+ * scales_t may both be NULL. No output may overlap another or W (not
+ * checked: the arrays live in device memory). Deterministic; asynchronous
+ * on `stream`, capturable.
+ * Errors: MUONH_EINVAL (NULL argument, half-given pair), MUONH_ESHAPE (2^24
+ * tiles or more in one launch of up to 16 groups), MUONH_EHIP.
+ */
+int muonh_fp8_weights(const muonh_plan* plan, const float* const* W, void* const* codes,
+                      void* const* scales, void* const* codes_t, void* const* scales_t,
+                      void* stream);
+
+/*
+ * out[i][j] = sum_k a[i][k] * b[j][k] over the values that a (m x k) and b
+ * (n x k) stand for, plus out's old value if `accumulate`; out: DEVICE, m x n
+ * of out_dtype, element (i, j) at i*out_ld + j, out_ld >= n. The products of
+ * a linear layer Y = X W^T:
+ *   Y  = matmul(X, W)           X rows; W tiles (n x k)
+ *   dX = matmul(dY, W^T)        dY rows; W's transposed tiles
+ *   dW = matmul(dY^T, X^T)      transposed rows forms (grouped along tokens);
+ *                               fp32 or bf16 G with accumulate: micro-batches
+ * k = 0 gives zeros (or leaves out as it is). Sums are fp32; the result is
+ * rounded once to out_dtype. bf16 results use the 8-bit matrix instructions,
+ * which drop product bits below 2^-13 of the largest of a few products they
+ * add at once: about 2e-5 relative error, far below bf16's 2^-9. fp32 results
+ * use bf16 matrix instructions on the widened codes, exact up to the fp32
+ * sums (about 1e-6; entries under 2^-117 in magnitude may lose bits), at
+ * half the rate. NaN codes give NaN in their row or column of out.
+ * The result does not depend on out_ld or alignment, and is deterministic.
+ * workspace: DEVICE, 256-byte aligned, of at least
+ * muonh_fp8_matmul_workspace_bytes(m, n, k, out_dtype) bytes (NULL if that is
+ * 0): partial sums of products with few output tiles. Calls in flight at once
+ * need workspaces of their own. Asynchronous on `stream`, capturable.
+ * Errors: MUONH_EINVAL (NULL argument, bad block or dtype, misaligned codes or
+ * scales, out_ld < n), MUONH_ESHAPE (a dim out of range, a and b of different
+ * cols, or 2^22 output tiles of 128 x 128 or more), MUONH_EWORKSPACE, MUONH_EALIAS (out or
+ * the workspace overlaps an operand or each other), MUONH_EHIP.
+ */
+size_t muonh_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t out_dtype);
+int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* out,
+                     int32_t out_dtype, int64_t out_ld, int32_t accumulate, void* workspace,
+                     size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* muonh_status_string(int status);

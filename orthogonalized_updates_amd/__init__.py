@@ -17,6 +17,11 @@ MuonH(shapes, precision=..., grad_dtype=..., mom_dtype=...) runs the step
 weight decay (step_muon_wd); AdamW(numels) updates the parameters outside
 the matrix group. Gradients and momenta may be float32 or bfloat16 tensors
 (grad_dtype / mom_dtype); weights are float32.
+
+fp8_quantize and fp8_matmul run the linear layers beside the step in e4m3
+with a scale per block of 128 (model card "Puro", section "Training"; the
+report page, part 6/7, section 4.3 "Cost Estimation": blockwise FP8), and
+step(..., fp8=set) leaves the updated weights quantized for them.
 """
 from __future__ import annotations
 
@@ -43,6 +48,11 @@ MUONH_GRAD_BF16 = 4
 MUONH_MOM_BF16 = 8
 MUONH_NONFINITE_MOMENTUM = 1
 MUONH_NONFINITE_UPDATE = 2
+MUONH_FP8_ROWS = 0
+MUONH_FP8_TILES = 1
+MUONH_DT_FP32 = 0
+MUONH_DT_BF16 = 1
+MUONH_MAX_FP8_DIM = 1 << 24
 # Bytes of muonh_step_noalloc's fixed per-GPU workspace (include/muonh.h).
 MUONH_NOALLOC_WORKSPACE_BYTES = 128 << 20
 
@@ -74,6 +84,12 @@ class MuonHAliasError(MuonHError, ValueError):
 # a training loop that cycles through a few gradient buffers uploads each
 # array once.
 PTR_CACHE_ENTRIES = 64
+
+
+class Fp8Desc(ctypes.Structure):
+    """muonh_fp8_matrix."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("block", ctypes.c_int32)]
 
 
 class GroupDesc(ctypes.Structure):
@@ -109,6 +125,14 @@ def _load_library() -> ctypes.CDLL:
                                             i32, vp]),
         "muonh_step_status": (ctypes.c_int, [vp, vp, sz, vp, ctypes.POINTER(ctypes.c_uint32)]),
         "muonh_check_disjoint": (ctypes.c_int, [vp, vp, vp, vp]),
+        "muonh_fp8_ld": (i64, [i64]),
+        "muonh_fp8_scale_ld": (i64, [i64]),
+        "muonh_fp8_scale_rows": (i64, [i64, i32]),
+        "muonh_fp8_quantize": (ctypes.c_int, [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp]),
+        "muonh_fp8_weights": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp]),
+        "muonh_fp8_matmul_workspace_bytes": (sz, [i64, i64, i64, i32]),
+        "muonh_fp8_matmul": (ctypes.c_int, [ctypes.POINTER(Fp8Desc), ctypes.POINTER(Fp8Desc), vp,
+                                            i32, i64, i32, vp, sz, vp]),
         "muonh_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "muonh_last_error": (ctypes.c_char_p, []),
     }
@@ -345,15 +369,22 @@ class MuonH:
         inv = self.torch.tensor(self.plan_order, dtype=self.torch.int64, device=self.device)
         self._R_plan = r.index_select(0, inv)
 
-    def step(self, weights, grads, moms, lr: float, beta: float = 0.95, ns_iters: int = 5) -> None:
-        """One MuonH step: moms and weights are updated in place."""
+    def step(self, weights, grads, moms, lr: float, beta: float = 0.95, ns_iters: int = 5,
+             fp8: "Optional[Fp8Weights]" = None) -> None:
+        """One MuonH step: moms and weights are updated in place. With `fp8`
+        (a set from fp8_weights()), the updated weights are then quantized
+        into it, as quantize_weights() does."""
         self._check_state(weights, grads, moms)
         if not hasattr(self, "_R_plan"):
             raise RuntimeError("call init() (or set_radius()) before step()")
+        if fp8 is not None:
+            self._check_fp8(fp8, weights, grads, moms)
         check(get_lib().muonh_step(self.plan.handle, self._ptr_array("W", weights),
                              self._ptr_array("G", grads), self._ptr_array("M", moms),
                              self._R_plan.data_ptr(), float(lr), float(beta), int(ns_iters),
                              self.workspace.data_ptr(), self.workspace.numel(), self._stream()))
+        if fp8 is not None:
+            self._quantize(weights, fp8)
 
     def step_noalloc(self, weights, grads, moms, lr: float, beta: float = 0.95,
                      ns_iters: int = 5) -> None:
@@ -386,11 +417,15 @@ class MuonH:
                                    self._stream(), arr, len(events)))
 
     def step_muon_wd(self, weights, grads, moms, lr: float, beta: float = 0.95,
-                     weight_decay: float = 0.1, ns_iters: int = 5, events=None) -> None:
+                     weight_decay: float = 0.1, ns_iters: int = 5, events=None,
+                     fp8: "Optional[Fp8Weights]" = None) -> None:
         """The baseline MuonH is measured against: Muon with decoupled weight
         decay, W <- (1 - lr*wd) W - lr O (no projection, no radius). With
-        `events` (as for step_timed), records the phase boundaries."""
+        `events` (as for step_timed), records the phase boundaries; `fp8` as
+        for step() (after the last event)."""
         self._check_state(weights, grads, moms)
+        if fp8 is not None:
+            self._check_fp8(fp8, weights, grads, moms)
         args = [self.plan.handle, self._ptr_array("W", weights), self._ptr_array("G", grads),
                 self._ptr_array("M", moms), float(lr), float(beta), float(weight_decay),
                 int(ns_iters), self.workspace.data_ptr(), self.workspace.numel(), self._stream()]
@@ -399,6 +434,43 @@ class MuonH:
         else:
             arr = (ctypes.c_void_p * len(events))(*[int(e.cuda_event) for e in events])
             check(get_lib().muonh_step_muon_wd_timed(*args, arr, len(events)))
+        if fp8 is not None:
+            self._quantize(weights, fp8)
+
+    # -- 8-bit weights ------------------------------------------------------
+    def fp8_weights(self, transposed: bool = True) -> "Fp8Weights":
+        """Storage for this optimizer's weights in e4m3 with 128 x 128 scales:
+        .weights[i] is matrix i as the forward product reads it,
+        .transposed[i] its transpose (for the data gradient). Contents are
+        undefined until a quantize_weights() or a step(..., fp8=set)."""
+        return Fp8Weights(self.shapes, self.device, transposed)
+
+    def quantize_weights(self, weights, out: "Fp8Weights") -> "Fp8Weights":
+        """Quantize the weights into `out` (a set from fp8_weights()), in
+        grouped launches (muonh_fp8_weights)."""
+        self._check(weights, "weights")
+        self._check_fp8(out, weights)
+        self._quantize(weights, out)
+        return out
+
+    def _check_fp8(self, out, *lists) -> None:
+        if not isinstance(out, Fp8Weights):
+            raise TypeError("expected an Fp8Weights set (see fp8_weights())")
+        if out.shapes != self.shapes or out.device != self.device:
+            raise ValueError("the Fp8Weights set has other shapes or another device")
+        lo, hi = out.span
+        for ts in lists:
+            for t in ts:
+                p = t.data_ptr()
+                if p < hi and lo < p + t.numel() * t.element_size():
+                    raise MuonHAliasError("a tensor of the call overlaps the Fp8Weights set")
+
+    def _quantize(self, weights, out) -> None:
+        arrs = [self._ptr_array("W", weights)]
+        for ms in (out.weights, out.transposed):
+            for field in ("codes", "scales"):
+                arrs.append(self._ptr_array(field, [getattr(m, field) for m in ms]) if ms else None)
+        check(get_lib().muonh_fp8_weights(self.plan.handle, *arrs, self._stream()))
 
     def read_update(self, index: int):
         """The update O of matrix `index` from the last step (fp32, rows x cols)."""
@@ -425,7 +497,9 @@ __all__ = ["MuonH", "Plan", "MuonHError", "GroupDesc", "get_lib", "check", "LIB_
            "MUONH_EHIP", "MUONH_ENOMEM", "MUONH_EALIAS", "MuonHAliasError", "MUONH_NS_FP32", "MUONH_NS_SPLIT_BF16", "MUONH_GRAD_BF16",
            "MUONH_MOM_BF16", "MUONH_NONFINITE_MOMENTUM", "MUONH_NONFINITE_UPDATE",
            "MUONH_NOALLOC_WORKSPACE_BYTES", "AdamW",
-           "PTR_CACHE_ENTRIES"]
+           "PTR_CACHE_ENTRIES", "Fp8Matrix", "Fp8Weights", "fp8_quantize", "fp8_matmul",
+           "MUONH_FP8_ROWS", "MUONH_FP8_TILES", "MUONH_DT_FP32", "MUONH_DT_BF16",
+           "MUONH_MAX_FP8_DIM"]
 
 
 class AdamW:
@@ -482,3 +556,210 @@ class AdamW:
             self._ptr_array("M", exp_avg), self._ptr_array("V", exp_avg_sq),
             float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
             stream))
+
+
+# -- block-scaled 8-bit matrices ---------------------------------------------
+# Entries per scale along a row, and per tile edge (include/muonh.h).
+FP8_BLOCK = 128
+FP8_BLOCKS = {"rows": MUONH_FP8_ROWS, "tiles": MUONH_FP8_TILES}
+FP8_FORMS = ("plain", "transposed", "both")
+
+
+def _up(v: int, m: int) -> int:
+    return -(-v // m) * m
+
+
+def _fp8_layout(rows: int, cols: int, block: str):
+    """(codes shape, scales shape) of a rows x cols matrix."""
+    if block not in FP8_BLOCKS:
+        raise ValueError(f"block must be one of {sorted(FP8_BLOCKS)}, got {block!r}")
+    if not (0 <= rows <= MUONH_MAX_FP8_DIM and 0 <= cols <= MUONH_MAX_FP8_DIM):
+        raise ValueError(f"shape {(rows, cols)} out of [0, {MUONH_MAX_FP8_DIM}]")
+    srows = rows if block == "rows" else -(-rows // FP8_BLOCK)
+    return (rows, _up(cols, FP8_BLOCK)), (srows, _up(-(-cols // FP8_BLOCK), 4))
+
+
+class Fp8Matrix:
+    """A rows x cols matrix held as e4m3 codes with a power-of-two scale per
+    block (muonh_fp8_matrix): per 128 columns of a row (block="rows") or per
+    128 x 128 entries ("tiles").
+
+    codes: torch.float8_e4m3fn, rows x (cols rounded up to 128), zeros past
+    cols; scales: torch.float8_e8m0fnu, (rows, or rows/128 rounded up) x
+    (cols/128 rounded up, then to a multiple of 4). Both contiguous, on one
+    GPU. shape: (rows, cols).
+    """
+    __slots__ = ("codes", "scales", "shape", "block", "device", "desc")
+
+    def __init__(self, codes, scales, shape: Tuple[int, int], block: str = "rows"):
+        import torch
+        rows, cols = int(shape[0]), int(shape[1])
+        for name, t, dt, want in zip(("codes", "scales"), (codes, scales),
+                                     (torch.float8_e4m3fn, torch.float8_e8m0fnu),
+                                     _fp8_layout(rows, cols, block)):
+            if not isinstance(t, torch.Tensor) or t.dtype != dt:
+                raise TypeError(f"{name} must be a {dt} torch tensor")
+            if tuple(t.shape) != want or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {want} tensor")
+        if codes.device != scales.device or codes.device.type != "cuda":
+            raise ValueError("codes and scales must be on one ROCm GPU")
+        self.codes, self.scales, self.shape, self.block = codes, scales, (rows, cols), block
+        self.device = codes.device
+        self.desc = Fp8Desc(codes.data_ptr(), scales.data_ptr(), rows, cols, FP8_BLOCKS[block])
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, block: str = "rows", device=None) -> "Fp8Matrix":
+        """Storage with undefined contents."""
+        import torch
+        c, s = _fp8_layout(rows, cols, block)
+        dev = device if device is not None else "cuda"
+        return cls(torch.empty(c, dtype=torch.float8_e4m3fn, device=dev),
+                   torch.empty(s, dtype=torch.float8_e8m0fnu, device=dev), (rows, cols), block)
+
+    def dequantize(self):
+        """The values it stands for, fp32 (torch operations; for inspection)."""
+        rows, cols = self.shape
+        s = self.scales[:, :-(-cols // FP8_BLOCK)].float()
+        if self.block == "tiles":
+            s = s.repeat_interleave(FP8_BLOCK, 0)[:rows]
+        return self.codes[:, :cols].float() * s.repeat_interleave(FP8_BLOCK, 1)[:, :cols]
+
+
+class Fp8Weights:
+    """The weights of a MuonH optimizer in 8 bits (MuonH.fp8_weights): lists
+    of Fp8Matrix with block "tiles" in the caller's order, `weights` and
+    `transposed` (empty without transposed forms), in one allocation."""
+
+    def __init__(self, shapes, device, transposed: bool = True):
+        import torch
+        self.shapes = list(shapes)
+        self.device = device
+        self.weights: List[Fp8Matrix] = []
+        self.transposed: List[Fp8Matrix] = []
+        places, total = [], 0
+        for r, c in self.shapes:
+            for shape, to in ((r, c), self.weights), ((c, r), self.transposed):
+                if to is self.transposed and not transposed:
+                    continue
+                at = []
+                for h, w in _fp8_layout(*shape, "tiles"):
+                    at.append((total, h, w))
+                    total = _up(total + h * w, 256)
+                places.append((shape, to, at))
+        self.storage = torch.empty(total, dtype=torch.uint8, device=device)
+        for shape, to, at in places:
+            parts = [self.storage[o:o + h * w].view(dt).view(h, w)
+                     for (o, h, w), dt in zip(at, (torch.float8_e4m3fn, torch.float8_e8m0fnu))]
+            to.append(Fp8Matrix(*parts, shape, "tiles"))
+
+    @property
+    def span(self) -> Tuple[int, int]:
+        p = int(self.storage.data_ptr())
+        return p, p + self.storage.numel()
+
+
+def _fp8_dt(torch, dtype) -> int:
+    if dtype == torch.float32:
+        return MUONH_DT_FP32
+    if dtype == torch.bfloat16:
+        return MUONH_DT_BF16
+    raise TypeError(f"expected torch.float32 or torch.bfloat16, got {dtype}")
+
+
+def _row_pitch(t, name: str) -> int:
+    """Elements between the rows of a 2-d tensor whose rows are contiguous."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous (stride 1 along columns)")
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return ld
+
+
+def fp8_quantize(x, block: str = "rows", forms: str = "plain",
+                 out: Optional[Fp8Matrix] = None, out_t: Optional[Fp8Matrix] = None):
+    """Quantize x (a 2-d fp32 or bf16 tensor on the GPU whose rows are
+    contiguous, any row stride) to block-scaled e4m3 (muonh_fp8_quantize).
+
+    forms: "plain" (x itself), "transposed" (its transpose: with block "rows",
+    grouped along x's rows) or "both", in one pass. Returns (q, q_t), None in
+    the place of a form that was not asked for. out / out_t: matrices to
+    write into instead of new ones. Runs on the current stream of x's device.
+    """
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch tensor")
+    dt = _fp8_dt(torch, x.dtype)
+    dev = x.device
+    if x.dim() != 2 or dev.type != "cuda":
+        raise ValueError("x must be a 2-d tensor on a ROCm GPU")
+    if forms not in FP8_FORMS:
+        raise ValueError(f"forms must be one of {FP8_FORMS}, got {forms!r}")
+    rows, cols = x.shape
+    ld = _row_pitch(x, "x")
+    got = []
+    for name, o, want, shape in (("out", out, forms != "transposed", (rows, cols)),
+                                 ("out_t", out_t, forms != "plain", (cols, rows))):
+        if not want:
+            if o is not None:
+                raise ValueError(f"{name} given, but forms={forms!r}")
+        elif o is None:
+            o = Fp8Matrix.empty(*shape, block, dev)
+        elif not isinstance(o, Fp8Matrix):
+            raise TypeError(f"{name} must be an Fp8Matrix")
+        elif o.shape != shape or o.block != block or o.device != dev:
+            raise ValueError(f"{name} must be a {shape} Fp8Matrix of block {block!r} on {dev}")
+        got.append(o)
+    ptr = [v for o in got for v in ((o.desc.codes, o.desc.scales) if o is not None else (None, None))]
+    with torch.cuda.device(dev):
+        check(get_lib().muonh_fp8_quantize(x.data_ptr(), dt, rows, cols, ld, FP8_BLOCKS[block], *ptr,
+                                           int(torch.cuda.current_stream(dev).cuda_stream)))
+    return tuple(got)
+
+
+def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate: bool = False):
+    """out[i][j] = sum_k a[i][k] * b[j][k] (muonh_fp8_matmul), plus out's old
+    values with accumulate=True.
+
+    out: a 2-d fp32 or bf16 tensor (a rows x b rows) whose rows are
+    contiguous; otherwise a new one of out_dtype (default bfloat16). The
+    products of a linear layer Y = X W^T: matmul(X, W); dX = matmul(dY, W_t);
+    G += matmul(dY_t, X_t) into the gradient the optimizer step reads. Runs on
+    the current stream of the operands' device.
+    """
+    import torch
+    for name, m in (("a", a), ("b", b)):
+        if not isinstance(m, Fp8Matrix):
+            raise TypeError(f"{name} must be an Fp8Matrix")
+    dev = a.device
+    if dev != b.device:
+        raise ValueError(f"a is on {dev}, b on {b.device}")
+    if a.shape[1] != b.shape[1]:
+        raise ValueError(f"a has {a.shape[1]} columns, b {b.shape[1]}")
+    m, n = shape = (a.shape[0], b.shape[0])
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs out")
+        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        dt = _fp8_dt(torch, out_dtype)
+        out = torch.empty(shape, device=dev, dtype=out_dtype)
+    else:
+        if not isinstance(out, torch.Tensor):
+            raise TypeError("out must be a torch tensor")
+        dt = _fp8_dt(torch, out.dtype)
+        if out_dtype is not None and out_dtype != out.dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        if tuple(out.shape) != shape or out.device != dev:
+            raise ValueError(f"out must be a {shape} tensor on {dev}")
+    ld = _row_pitch(out, "out")
+    lib = get_lib()
+    with torch.cuda.device(dev):
+        nbytes = lib.muonh_fp8_matmul_workspace_bytes(m, n, a.shape[1], dt)
+        # from torch's allocator on the current stream: calls on other streams
+        # and captured graphs get memory of their own
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        check(lib.muonh_fp8_matmul(ctypes.byref(a.desc), ctypes.byref(b.desc), out.data_ptr(), dt, ld,
+                                   int(bool(accumulate)), ws.data_ptr() if nbytes else None, nbytes,
+                                   int(torch.cuda.current_stream(dev).cuda_stream)))
+    return out

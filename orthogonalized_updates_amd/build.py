@@ -14,7 +14,8 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libmuonh.so"
-SOURCES = ["muonh_abi.hip", "ns_gemm.hip", "elementwise.hip", "adamw.hip"]
+SOURCES = ["muonh_abi.hip", "ns_gemm.hip", "elementwise.hip", "adamw.hip", "fp8_quantize.hip",
+           "fp8_matmul.hip"]
 ARCH = "gfx950"
 
 

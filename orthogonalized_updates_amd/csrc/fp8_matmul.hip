@@ -1,0 +1,498 @@
+// Products of block-scaled e4m3 matrices on gfx950 (formats and contract:
+// include/muonh.h): out[i][j] = sum_k a[i][k] b[j][k], both operands read
+// along their rows.
+//
+// One v_mfma_scale_f32_16x16x128_f8f6f4 covers exactly one scale block of 128
+// along k and applies one E8M0 scale per operand row itself, so scales cost
+// no vector arithmetic on the accumulators. Lane l of a fragment holds row
+// l%16 and 32 of the 128 codes: 16-byte chunks l/16 and l/16 + 4 of the row
+// (any assignment of k to lanes is right as long as both operands use the
+// same one; this one reads LDS without bank conflicts, see frag_off).
+//
+// bf16 results take that path. Within one instruction the 8-bit products are
+// added in groups whose terms keep no bits below 2^-13 of the largest
+// (measured: 1.4-1.6e-5 relative error on normal data, 5e-5 on codes spread
+// over the whole format, independent of k). fp32 results must not carry
+// that, so they widen the codes to bf16 with their scale applied (exact) and
+// use v_mfma_f32_16x16x32_bf16, whose sums are accurate to fp32 (measured 1e-7
+// at k = 8192), at half the matrix rate.
+#include <algorithm>
+
+#include "fp8_internal.h"
+
+namespace muonh {
+namespace fp8 {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+struct Operand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows, ld;  // ld: bytes per row of codes
+  int64_t sld;       // bytes per row of scales
+  int sshift;        // scale row of matrix row r: r >> sshift
+};
+
+struct MatArgs {
+  Operand a, b;      // m x k, n x k
+  int64_t m, n;
+  int nkb;           // 128-blocks of k
+  void* out;
+  int64_t ldo;
+  int accumulate;
+  int vec;           // out's address and pitch allow 16-byte accesses
+  float* part;       // partial sums [split][m][pld], or nullptr
+  int64_t pld;
+  int splits, per;   // k blocks per split
+  int tm, tn;        // tile grid
+};
+
+// 8 codes (two dwords) widened to bf16 times a power of two: exact.
+__device__ __forceinline__ bf16x8 widen8(int lo, int hi, float s) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// 2^(byte - 127) for bytes 1 .. 254.
+__device__ __forceinline__ float scale_of(int byte) { return __int_as_float(byte << 23); }
+
+// acc[x][y] += X_x Y_y^T for one block of k: NX x NY products of 16 x 16.
+// sx, sy: scale bytes of the fragments' rows (in the low 8 bits).
+// WIDE: through bf16.
+template <bool WIDE, int NX, int NY>
+__device__ __forceinline__ void mma_block(const i32x8 (&x)[NX], const i32x8 (&y)[NY],
+                                          const int (&sx)[NX], const int (&sy)[NY],
+                                          f32x4 (&acc)[NX][NY]) {
+  if constexpr (!WIDE) {
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+#pragma unroll
+      for (int j = 0; j < NY; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[i], y[j], acc[i][j], 0, 0, 0,
+                                                                     sx[i], 0, sy[j]);
+  } else {
+    float fx[NX], fy[NY];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) fx[i] = scale_of(sx[i] & 255);
+#pragma unroll
+    for (int j = 0; j < NY; ++j) fy[j] = scale_of(sy[j] & 255);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      bf16x8 wx[NX], wy[NY];
+#pragma unroll
+      for (int i = 0; i < NX; ++i) wx[i] = widen8(x[i][2 * q], x[i][2 * q + 1], fx[i]);
+#pragma unroll
+      for (int j = 0; j < NY; ++j) wy[j] = widen8(y[j][2 * q], y[j][2 * q + 1], fy[j]);
+#pragma unroll
+      for (int i = 0; i < NX; ++i)
+#pragma unroll
+        for (int j = 0; j < NY; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wx[i], wy[j], acc[i][j], 0, 0, 0);
+    }
+  }
+}
+
+// ---- output ------------------------------------------------------------------
+// v: CNT consecutive results of row i from column j (16 bytes or a part of
+// them). Guards the column end; the caller guards the row.
+template <typename T, int CNT>
+__device__ __forceinline__ void put(const MatArgs& a, int64_t i, int64_t j, const float (&v)[CNT]) {
+  T* p = static_cast<T*>(a.out) + i * a.ldo + j;
+  typedef T vecT __attribute__((ext_vector_type(CNT)));
+  if (a.vec && j + CNT <= a.n) {
+    vecT w;
+    if (a.accumulate) {
+      const vecT o = *reinterpret_cast<const vecT*>(p);
+#pragma unroll
+      for (int q = 0; q < CNT; ++q) w[q] = (T)((float)o[q] + v[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < CNT; ++q) w[q] = (T)v[q];
+    }
+    *reinterpret_cast<vecT*>(p) = w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < CNT; ++q)
+      if (j + q < a.n) p[q] = (T)((a.accumulate ? (float)p[q] : 0.f) + v[q]);
+  }
+}
+
+// Waits until at most VM of this wave's memory operations are outstanding and
+// its LDS reads have retired, then the workgroup's barrier; neither memory
+// accesses nor MFMAs move across.
+template <int VM>
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((VM & 0xF) | ((VM >> 4) << 14) | (0x7 << 4));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// LDS DMA: lane l's 16 (4) bytes at g go to LDS bytes m0 + 16 l (4 l). No
+// register results; waits and barriers are the caller's.
+__device__ __forceinline__ void dma16(const void* g, uint32_t m0) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "{m0}"(m0) : "memory");
+}
+__device__ __forceinline__ void dma4(const void* g, uint32_t m0) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "{m0}"(m0) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// 128 x 128 tiles, 4 waves of 64 x 64, two LDS stages of one k block (2 x 32
+// KB): the DMA of block t + 1 runs under the MFMAs of block t.
+//
+// An LDS row holds the 128 codes of one operand row; 16-byte chunk c of row r
+// sits at position c ^ (r & 7), which spreads the 16 rows x 4 chunks of a
+// fragment read over the banks (measured: 510 GB/s per CU against 290 with
+// chunk pairs 2g, 2g + 1). The DMA writes LDS linearly, so the lane's source
+// chunk is permuted instead. Rows past the matrix reload its last row; their
+// results are not stored.
+//
+// The b operand is the MFMA's first one, so a lane's 4 accumulators are 4
+// consecutive columns of one row of out. For 2-byte results b's rows are
+// also dealt to the fragments so that a lane holds 8 consecutive columns in
+// two neighbouring fragments: 16-byte stores, whole 64-byte runs per row.
+// ---------------------------------------------------------------------------
+constexpr int kT = 128;
+constexpr int kOpStage = kT * kBlock;     // 16 KB
+constexpr int kStageBytes = 2 * kOpStage;
+constexpr int kScaleBytes = 2 * kT * 4;   // 4 k blocks of both operands' rows
+
+// Tile row (0 .. 63 of a wave's 64 columns) held by fragment f, fragment row r.
+template <bool PAIR>
+__device__ __forceinline__ int b_row(int f, int r) {
+  return PAIR ? 32 * (f >> 1) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3) : 16 * f + r;
+}
+
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(256, 2) void k_matmul_tile(MatArgs a) {
+  constexpr bool kPair = sizeof(T) == 2;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes + 2 * kScaleBytes];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tile = blockIdx.x, split = blockIdx.y;
+  const int ti = tile % a.tm, tj = tile / a.tm;
+  const int kb0 = split * a.per, kb1 = min(kb0 + a.per, a.nkb);
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
+
+  // DMA of one stage: waves 0, 1 fill a's 128 rows, waves 2, 3 b's; 8
+  // instructions of 8 rows each. Lane l: row l / 8, position l % 8.
+  const Operand& op = wave < 2 ? a.a : a.b;
+  const int64_t row0 = (int64_t)(wave < 2 ? ti : tj) * kT;
+  const uint8_t* src[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int lr = 64 * (wave & 1) + 8 * q + (lane >> 3);  // LDS row
+    const int mr = wave < 2 ? lr : 64 * (lr >> 6) + b_row<kPair>((lr & 63) >> 4, lr & 15);
+    const int64_t r = min(row0 + mr, op.rows - 1);
+    src[q] = op.codes + r * op.ld + (((lane & 7) ^ (lr & 7)) << 4);
+  }
+  const uint32_t dst = base + (wave < 2 ? 0 : kOpStage) + (wave & 1) * 64 * kBlock;
+  // Scales: every 4 k blocks each wave fetches 4 bytes of 64 rows.
+  const uint8_t* ssrc;
+  {
+    const int lr = 64 * (wave & 1) + lane;
+    const int mr = wave < 2 ? lr : 64 * (lr >> 6) + b_row<kPair>((lr & 63) >> 4, lr & 15);
+    ssrc = op.scales + (min(row0 + mr, op.rows - 1) >> op.sshift) * op.sld;
+  }
+  const uint32_t sdst = base + 2 * kStageBytes + (wave < 2 ? 0 : kT * 4) + (wave & 1) * 64 * 4;
+  auto issue = [&](int kb) {
+    const int buf = (kb - kb0) & 1;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dma16(src[q] + (int64_t)kb * kBlock, dst + buf * kStageBytes + q * 1024);
+    if (kb == kb0 || (kb & 3) == 0) dma4(ssrc + (kb & ~3), sdst + ((kb >> 2) & 1) * kScaleBytes);
+  };
+
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r16 = lane & 15, g = lane >> 4;
+  const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);  // fragment rows start at multiples of 16
+  f32x4 acc[4][4];  // [b fragment][a fragment]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+
+  if (kb0 < kb1) issue(kb0);
+  for (int kb = kb0; kb < kb1; ++kb) {
+    stage_barrier<0>();  // block kb has landed for all waves; the other stage is free
+    if (kb + 1 < kb1) issue(kb + 1);
+    const char* st = lds + ((kb - kb0) & 1) * kStageBytes;
+    const char* ss = lds + 2 * kStageBytes + ((kb >> 2) & 1) * kScaleBytes;
+    auto frag = [&](const char* p) {
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(p + foff);
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (foff ^ 64));
+      return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    i32x8 fa[4], fb[4];
+    int sa[4], sb[4];
+    const int sh = (kb & 3) * 8;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      fa[f] = frag(st + (64 * wm + 16 * f) * kBlock);
+      fb[f] = frag(st + kOpStage + (64 * wn + 16 * f) * kBlock);
+      sa[f] = *reinterpret_cast<const int*>(ss + (64 * wm + 16 * f + r16) * 4) >> sh;
+      sb[f] = *reinterpret_cast<const int*>(ss + kT * 4 + (64 * wn + 16 * f + r16) * 4) >> sh;
+    }
+    mma_block<WIDE, 4, 4>(fb, fa, sb, sa, acc);
+  }
+
+  // lane: row 16 f + l%16 of the wave's rows; columns by b_row
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int64_t i = (int64_t)ti * kT + 64 * wm + 16 * f + r16;
+    if (i >= a.m) continue;
+    const int64_t j0 = (int64_t)tj * kT + 64 * wn;
+    if (a.part) {
+      float* p = a.part + ((int64_t)split * a.m + i) * a.pld;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t j = j0 + b_row<kPair>(q, 4 * g);
+        if (j < a.pld) *reinterpret_cast<f32x4*>(p + j) = acc[q][f];  // pld: a multiple of 4
+      }
+    } else if constexpr (kPair) {
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[q][f][e];
+          v[4 + e] = acc[q + 1][f][e];
+        }
+        put<T, 8>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {acc[q][f][0], acc[q][f][1], acc[q][f][2], acc[q][f][3]};
+        put<T, 4>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
+      }
+    }
+  }
+}
+
+// out (+)= the partial sums, split by split in order; 4 columns per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_matmul_join(MatArgs a) {
+  const int64_t q4 = a.pld >> 2;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= a.m * q4) return;
+  const int64_t i = e / q4, j = (e - i * q4) * 4;
+  f32x4 s = {};
+  for (int p = 0; p < a.splits; ++p)
+    s += *reinterpret_cast<const f32x4*>(a.part + ((int64_t)p * a.m + i) * a.pld + j);
+  const float v[4] = {s[0], s[1], s[2], s[3]};
+  put<T, 4>(a, i, j, v);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of a (m <= 16 NA): one workgroup per 16 columns of out; its waves
+// take the k blocks in turn, straight from global memory (every code of b is
+// read once, by one wave), and join their sums through LDS.
+// ---------------------------------------------------------------------------
+constexpr int kSkinnyWaves = 8;
+
+template <typename T, bool WIDE, int NA>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void k_matmul_skinny(MatArgs a) {
+  __shared__ __attribute__((aligned(16))) f32x4 red[kSkinnyWaves][NA][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r16 = lane & 15, g = lane >> 4;
+  const int64_t j0 = (int64_t)blockIdx.x * 16;
+  auto row_of = [&](const Operand& o, int64_t r, const uint8_t*& codes, const uint8_t*& scales) {
+    r = min(r, o.rows - 1);
+    codes = o.codes + r * o.ld + 16 * g;
+    scales = o.scales + (r >> o.sshift) * o.sld;
+  };
+  const uint8_t *bc, *bs, *ac[NA], *as[NA];
+  row_of(a.b, j0 + r16, bc, bs);
+#pragma unroll
+  for (int f = 0; f < NA; ++f) row_of(a.a, 16 * f + r16, ac[f], as[f]);
+  auto frag = [](const uint8_t* p) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(p), hi = *reinterpret_cast<const i32x4*>(p + 64);
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  f32x4 acc[1][NA];
+#pragma unroll
+  for (int f = 0; f < NA; ++f) acc[0][f] = f32x4{};
+#pragma unroll 2
+  for (int kb = wave; kb < a.nkb; kb += kSkinnyWaves) {
+    i32x8 fb[1] = {frag(bc + (int64_t)kb * kBlock)}, fa[NA];
+    int sb[1] = {bs[kb]}, sa[NA];
+#pragma unroll
+    for (int f = 0; f < NA; ++f) {
+      fa[f] = frag(ac[f] + (int64_t)kb * kBlock);
+      sa[f] = as[f][kb];
+    }
+    mma_block<WIDE, 1, NA>(fb, fa, sb, sa, acc);
+  }
+#pragma unroll
+  for (int f = 0; f < NA; ++f) red[wave][f][lane] = acc[0][f];
+  __syncthreads();
+  for (int e = tid; e < NA * 64; e += 64 * kSkinnyWaves) {
+    const int f = e >> 6, l = e & 63;
+    f32x4 s = red[0][f][l];
+#pragma unroll
+    for (int w = 1; w < kSkinnyWaves; ++w) s += red[w][f][l];
+    const int64_t i = 16 * f + (l & 15);
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    if (i < a.m) put<T, 4>(a, i, j0 + 4 * (l >> 4), v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int64_t kCUs = 256;
+constexpr int64_t kMaxTiles = (1 << 22) - 1;
+
+enum Kind { kSkinny = 0, kTile = 1 };
+struct Choice {
+  Kind kind;
+  int splits, per;
+  size_t ws_bytes;
+};
+
+Choice choose(int64_t m, int64_t n, int64_t k) {
+  Choice c{kTile, 1, (int)ceil_div(k, kBlock), 0};
+  const int64_t nkb = ceil_div(k, kBlock);
+  if (m <= 64) {
+    c.kind = kSkinny;
+    return c;
+  }
+  // Two workgroups fit a CU. Fewer tiles than that leave CUs idle: the k
+  // blocks are split over up to 16 workgroups per tile, 4 blocks each at least.
+  const int64_t tiles = ceil_div(m, kT) * ceil_div(n, kT);
+  int64_t s = std::min<int64_t>({2 * kCUs / std::max<int64_t>(tiles, 1), nkb / 4, 16});
+  if (s > 1) {
+    c.per = (int)ceil_div(nkb, s);
+    c.splits = (int)ceil_div(nkb, c.per);
+    c.ws_bytes = (size_t)c.splits * m * (ceil_div(n, 4) * 4) * sizeof(float);
+  }
+  return c;
+}
+
+template <typename T, bool WIDE>
+int launch(const MatArgs& a, const Choice& c, hipStream_t s) {
+  if (c.kind == kSkinny) {
+    const dim3 grid((unsigned)ceil_div(a.n, 16)), thr(64 * kSkinnyWaves);
+    if (a.m <= 16)
+      hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 1>), grid, thr, 0, s, a);
+    else if (a.m <= 32)
+      hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 2>), grid, thr, 0, s, a);
+    else
+      hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 4>), grid, thr, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_matmul_tile<T, WIDE>), dim3((unsigned)(a.tm * a.tn), (unsigned)a.splits),
+                       dim3(256), 0, s, a);
+    if (a.part)
+      hipLaunchKernelGGL((k_matmul_join<T>), dim3((unsigned)ceil_div(a.m * (a.pld >> 2), 256)),
+                         dim3(256), 0, s, a);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(MUONH_EHIP, "fp8 matmul: %s (%d)", hipGetErrorString(e), (int)e);
+  return MUONH_OK;
+}
+
+int check_operand(const char* name, const muonh_fp8_matrix* x) {
+  if (!x) return fail(MUONH_EINVAL, "%s is NULL", name);
+  if (bad_dim(x->rows) || bad_dim(x->cols))
+    return fail(MUONH_ESHAPE, "%s: shape %lld x %lld out of [0, %d]", name, (long long)x->rows,
+                (long long)x->cols, MUONH_MAX_FP8_DIM);
+  if (x->block != MUONH_FP8_ROWS && x->block != MUONH_FP8_TILES)
+    return fail(MUONH_EINVAL, "%s: block=%d is neither MUONH_FP8_ROWS nor MUONH_FP8_TILES", name, x->block);
+  if (x->rows == 0 || x->cols == 0) return MUONH_OK;
+  if (!x->codes || !x->scales) return fail(MUONH_EINVAL, "%s: codes and scales must not be NULL", name);
+  if (reinterpret_cast<uintptr_t>(x->codes) & 15u || reinterpret_cast<uintptr_t>(x->scales) & 3u)
+    return fail(MUONH_EINVAL, "%s: codes must be 16-byte and scales 4-byte aligned", name);
+  return MUONH_OK;
+}
+
+Operand operand(const muonh_fp8_matrix* x) {
+  return Operand{static_cast<const uint8_t*>(x->codes), static_cast<const uint8_t*>(x->scales), x->rows,
+                 code_ld(x->cols), scale_ld(x->cols), x->block == MUONH_FP8_TILES ? 7 : 0};
+}
+
+}  // namespace
+}  // namespace fp8
+}  // namespace muonh
+
+extern "C" {
+
+size_t muonh_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
+  using namespace muonh::fp8;
+  (void)out_dtype;
+  if (bad_dim(m) || bad_dim(n) || bad_dim(k) || m == 0 || n == 0) return 0;
+  return choose(m, n, k).ws_bytes;
+}
+
+int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* out,
+                     int32_t out_dtype, int64_t out_ld, int32_t accumulate, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  using namespace muonh;
+  using namespace muonh::fp8;
+  if (const int err = check_operand("a", a)) return err;
+  if (const int err = check_operand("b", b)) return err;
+  if (a->cols != b->cols)
+    return fail(MUONH_ESHAPE, "a has %lld columns, b %lld", (long long)a->cols, (long long)b->cols);
+  if (out_dtype != MUONH_DT_FP32 && out_dtype != MUONH_DT_BF16)
+    return fail(MUONH_EINVAL, "out_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", out_dtype);
+  const int64_t m = a->rows, n = b->rows, k = a->cols;
+  if (out_ld < n || out_ld > (1LL << 36))
+    return fail(MUONH_EINVAL, "out_ld=%lld out of [n=%lld, 2^36]", (long long)out_ld, (long long)n);
+  if (m == 0 || n == 0) return MUONH_OK;
+  if (!out) return fail(MUONH_EINVAL, "out is NULL");
+  const int esize = out_dtype == MUONH_DT_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(out) & (uintptr_t)(esize - 1))
+    return fail(MUONH_EINVAL, "out is not aligned to its type");
+  const int64_t tm = ceil_div(m, kT), tn = ceil_div(n, kT);
+  if (tm * tn > kMaxTiles) return fail(MUONH_ESHAPE, "2^22 output tiles of 128 x 128 or more");
+  const Choice c = choose(m, n, k);
+  if (c.ws_bytes) {
+    if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the product needs %zu bytes", c.ws_bytes);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+      return fail(MUONH_EWORKSPACE, "workspace must be 256-byte aligned");
+    if (workspace_bytes < c.ws_bytes)
+      return fail(MUONH_EWORKSPACE, "workspace has %zu bytes, the product needs %zu", workspace_bytes, c.ws_bytes);
+  }
+  const Span written[2] = {span("out", out, ((m - 1) * out_ld + n) * esize),
+                           span("workspace", c.ws_bytes ? workspace : nullptr, (int64_t)c.ws_bytes)};
+  const Span read[4] = {span("a's codes", a->codes, m * code_ld(k)),
+                        span("a's scales", a->scales, scale_rows(m, a->block) * scale_ld(k)),
+                        span("b's codes", b->codes, n * code_ld(k)),
+                        span("b's scales", b->scales, scale_rows(n, b->block) * scale_ld(k))};
+  if (overlap(written[0], written[1])) return fail(MUONH_EALIAS, "out overlaps the workspace");
+  for (const Span& w : written)
+    for (const Span& r : read)
+      if (overlap(w, r)) return fail(MUONH_EALIAS, "%s overlaps %s", w.name, r.name);
+
+  MatArgs x{};
+  x.a = operand(a);
+  x.b = operand(b);
+  x.m = m;
+  x.n = n;
+  x.nkb = (int)ceil_div(k, kBlock);
+  x.out = out;
+  x.ldo = out_ld;
+  x.accumulate = accumulate != 0;
+  x.vec = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(out_ld * esize)) & 15u) == 0;
+  x.splits = c.splits;
+  x.per = c.per;
+  x.pld = ceil_div(n, 4) * 4;
+  x.part = c.ws_bytes ? static_cast<float*>(workspace) : nullptr;
+  x.tm = (int)tm;
+  x.tn = (int)tn;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return out_dtype == MUONH_DT_BF16 ? launch<__bf16, false>(x, c, s) : launch<float, true>(x, c, s);
+}
+
+}  // extern "C"

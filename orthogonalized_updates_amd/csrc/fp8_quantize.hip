@@ -1,0 +1,375 @@
+// Quantization to block-scaled e4m3 on gfx950 (formats: include/muonh.h; the
+// report page, part 6/7, section 4.3 "Cost Estimation", names blockwise FP8
+// linear layers, without a rounding or a scale type).
+//
+// One workgroup takes one 128 x 128 tile of the source, which holds whole
+// blocks of every kind: 128 row groups, 128 column groups (the transposed
+// form's row groups) or one tile. It reads the tile once into registers (16 x 16
+// threads, each an 8 x 8 patch), takes the
+// maxima by lane exchanges and LDS, and writes one or both forms: 4 (fp32) or
+// 2 (bf16) bytes read and 1 or 2 written per entry, HBM-bound.
+//
+// A scale is a power of two, so x * 2^-e is exact and the conversion
+// instruction's rounding (nearest, ties to even) is the only one. The
+// exponent comes from the bits of the maximum a = 1.f * 2^E: 448 = 1.75 * 2^8,
+// so e = E - 8 where 1.f <= 1.75, else E - 7.
+#include "fp8_internal.h"
+
+namespace muonh {
+namespace fp8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxGroups = 16;
+// Blocks of one launch: a launch has fewer than 2^32 threads.
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+
+// Bits of max |x| over finite entries -> scale byte e + 127, e >= -126.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  const int b = (int)((amax_bits + 0x1fffffu) >> 23) - 8;
+  return (uint32_t)(b < 1 ? 1 : b);
+}
+// 2^-e = 2^(127 - byte): byte in [1, 247], so the result is a normal number.
+__device__ __forceinline__ float inv_scale(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+// |x|'s bits, 0 for NaN and infinities (as integers they order like values).
+__device__ __forceinline__ uint32_t mag(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// 4 values to 4 codes, the first in the low byte. |v| <= 448 where finite.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+struct Group {
+  int64_t rows, cols, src_ld;
+  uint32_t first, tiles_c;  // first matrix (grouped launches); tiles per tile row
+  uint32_t tiles, begin;    // tiles per matrix; first block of the group
+};
+struct Args {
+  Group g[kMaxGroups];
+  int ngroups;
+  // one matrix (ptrs == 0), or device arrays of pointers indexed by matrix
+  int ptrs;
+  const void* src;
+  void *codes, *scales, *codes_t, *scales_t;
+};
+
+template <bool BF>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  if (BF) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+  return static_cast<const float*>(p)[i];
+}
+// 8 consecutive entries from i; the address is 16-byte aligned.
+template <bool BF>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+  if (BF) {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+// The scale byte of block column kb of one scale row; the block of the last
+// column also writes the row's zero padding.
+__device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, int64_t cols,
+                                          uint32_t byte) {
+  const int64_t ld = scale_ld(cols), nb = ceil_div(cols, kBlock);
+  uint8_t* p = s + row * ld;
+  p[kb] = (uint8_t)byte;
+  if (kb == nb - 1)
+    for (int64_t j = nb; j < ld; ++j) p[j] = 0;
+}
+
+// Thread (ty, tx) = (tid / 16, tid % 16) holds rows 8 ty .. +7, columns
+// 8 tx .. +7 of the tile. PLAIN, TRANS: the forms written; TILES: one scale.
+template <bool BF, bool TILES, bool PLAIN, bool TRANS>
+__global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
+  __shared__ uint32_t red[4][kBlock];                                  // maxima by wave
+  __shared__ __attribute__((aligned(16))) uint8_t stage[kBlock * kBlock];  // transposed codes
+  int gi = 0;
+  for (int i = 1; i < a.ngroups; ++i)
+    if (blockIdx.x >= a.g[i].begin) gi = i;
+  const Group& g = a.g[gi];
+  const uint32_t local = blockIdx.x - g.begin;
+  const uint32_t m = local / g.tiles, t = local - m * g.tiles;
+  const int64_t tr = t / g.tiles_c, tc = t - (uint32_t)tr * g.tiles_c;
+  const int64_t mat = g.first + m;
+  const void* src = a.ptrs ? static_cast<const void* const*>(a.src)[mat] : a.src;
+  auto pick = [&](void* p) {
+    return static_cast<uint8_t*>(a.ptrs ? static_cast<void* const*>(p)[mat] : p);
+  };
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tx = tid & 15, ty = tid >> 4;
+  const int64_t r0 = tr * kBlock + 8 * ty, c0 = tc * kBlock + 8 * tx;
+  const int64_t rows = g.rows, cols = g.cols;
+
+  float v[8][8];
+  const bool vec = ((reinterpret_cast<uintptr_t>(src) | (uintptr_t)(g.src_ld * (BF ? 2 : 4))) & 15u) == 0;
+  if (vec && c0 + 8 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // rows past the end reload the last one, so that no load waits in a branch
+      const int64_t r = r0 + i < rows ? r0 + i : rows - 1;
+      load8<BF>(src, r * g.src_ld + c0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i >= rows)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[i][j] = r0 + i < rows && c0 + j < cols ? load1<BF>(src, (r0 + i) * g.src_ld + c0 + j) : 0.f;
+  }
+
+  uint32_t tile_byte = 0;
+  if (TILES) {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mx = umax(mx, mag(v[i][j]));
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
+    if (lane == 0) red[0][wave] = mx;
+    __syncthreads();
+    tile_byte = scale_byte(umax(umax(red[0][0], red[0][1]), umax(red[0][2], red[0][3])));
+    const float inv = inv_scale(tile_byte);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+    if (tid == 0) {
+      if (PLAIN) put_scale(pick(a.scales), tr, tc, cols, tile_byte);
+      if (TRANS) put_scale(pick(a.scales_t), tc, tr, rows, tile_byte);
+    }
+  }
+
+  if (PLAIN) {
+    uint8_t* codes = pick(a.codes);
+    const int64_t ld = code_ld(cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float s = 1.f;
+      if (!TILES) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = umax(mx, mag(v[i][j]));
+        // the 16 threads of a row are 16 consecutive lanes
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
+        const uint32_t byte = scale_byte(mx);
+        s = inv_scale(byte);
+        if (tx == 0 && r0 + i < rows) put_scale(pick(a.scales), r0 + i, tc, cols, byte);
+      }
+      if (r0 + i < rows) {
+        uint2 q;
+        q.x = codes4(v[i][0] * s, v[i][1] * s, v[i][2] * s, v[i][3] * s);
+        q.y = codes4(v[i][4] * s, v[i][5] * s, v[i][6] * s, v[i][7] * s);
+        *reinterpret_cast<uint2*>(codes + (r0 + i) * ld + c0) = q;
+      }
+    }
+  }
+
+  if (TRANS) {
+    float s[8];
+    if (!TILES) {
+      uint32_t mx[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mx[j] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[j] = umax(mx[j], mag(v[i][j]));
+        // the wave's 4 thread rows, then the 4 waves through LDS
+        mx[j] = umax(mx[j], (uint32_t)__shfl_xor((int)mx[j], 16, 64));
+        mx[j] = umax(mx[j], (uint32_t)__shfl_xor((int)mx[j], 32, 64));
+      }
+      if (lane < 16)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) red[wave][8 * tx + j] = mx[j];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = 8 * tx + j;
+        const uint32_t byte = scale_byte(umax(umax(red[0][c], red[1][c]), umax(red[2][c], red[3][c])));
+        s[j] = inv_scale(byte);
+        if (ty == 0 && c0 + j < cols) put_scale(pick(a.scales_t), c0 + j, tr, rows, byte);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = 1.f;
+    }
+    // Row c of the staged tile: 16 pieces of 8 codes (piece = thread row),
+    // piece p at position p ^ (c / 8), so that the 16 thread columns of a
+    // store fall on different banks.
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint2 q;
+      q.x = codes4(v[0][j] * s[j], v[1][j] * s[j], v[2][j] * s[j], v[3][j] * s[j]);
+      q.y = codes4(v[4][j] * s[j], v[5][j] * s[j], v[6][j] * s[j], v[7][j] * s[j]);
+      *reinterpret_cast<uint2*>(stage + (8 * tx + j) * kBlock + ((ty ^ tx) << 3)) = q;
+    }
+    __syncthreads();
+    uint8_t* out = pick(a.codes_t);
+    const int64_t ld = code_ld(rows);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = (tid >> 3) + 32 * k, u = tid & 7;  // 16 bytes: pieces 2u, 2u + 1
+      const uint2 lo = *reinterpret_cast<const uint2*>(stage + c * kBlock + (((2 * u) ^ (c >> 3)) << 3));
+      const uint2 hi = *reinterpret_cast<const uint2*>(stage + c * kBlock + (((2 * u + 1) ^ (c >> 3)) << 3));
+      if (tc * kBlock + c < cols)
+        *reinterpret_cast<uint4*>(out + (tc * kBlock + c) * ld + tr * kBlock + 16 * u) =
+            make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  }
+}
+
+template <bool BF, bool TILES>
+void launch_forms(const Args& a, int64_t blocks, bool plain, bool trans, hipStream_t s) {
+  const dim3 grid((unsigned)blocks), thr(kThreads);
+  if (plain && trans)
+    hipLaunchKernelGGL((k_quantize<BF, TILES, true, true>), grid, thr, 0, s, a);
+  else if (plain)
+    hipLaunchKernelGGL((k_quantize<BF, TILES, true, false>), grid, thr, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_quantize<BF, TILES, false, true>), grid, thr, 0, s, a);
+}
+
+int launched(const char* what) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(MUONH_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
+  return MUONH_OK;
+}
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+}  // namespace
+}  // namespace fp8
+}  // namespace muonh
+
+extern "C" {
+
+int64_t muonh_fp8_ld(int64_t cols) {
+  return muonh::fp8::bad_dim(cols) ? 0 : muonh::fp8::code_ld(cols);
+}
+
+int64_t muonh_fp8_scale_ld(int64_t cols) {
+  return muonh::fp8::bad_dim(cols) ? 0 : muonh::fp8::scale_ld(cols);
+}
+
+int64_t muonh_fp8_scale_rows(int64_t rows, int32_t block) {
+  if (muonh::fp8::bad_dim(rows) || (block != MUONH_FP8_ROWS && block != MUONH_FP8_TILES)) return 0;
+  return muonh::fp8::scale_rows(rows, block);
+}
+
+int muonh_fp8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t src_ld,
+                       int32_t block, void* codes, void* scales, void* codes_t, void* scales_t,
+                       void* stream) {
+  using namespace muonh;
+  using namespace muonh::fp8;
+  if (dtype != MUONH_DT_FP32 && dtype != MUONH_DT_BF16)
+    return fail(MUONH_EINVAL, "dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", dtype);
+  if (block != MUONH_FP8_ROWS && block != MUONH_FP8_TILES)
+    return fail(MUONH_EINVAL, "block=%d is neither MUONH_FP8_ROWS nor MUONH_FP8_TILES", block);
+  if (bad_dim(rows) || bad_dim(cols))
+    return fail(MUONH_ESHAPE, "shape %lld x %lld out of [0, %d]", (long long)rows, (long long)cols,
+                MUONH_MAX_FP8_DIM);
+  if (src_ld < cols || src_ld > (1LL << 36))
+    return fail(MUONH_EINVAL, "src_ld=%lld out of [cols=%lld, 2^36]", (long long)src_ld, (long long)cols);
+  if (rows == 0 || cols == 0) return MUONH_OK;
+  if (!src) return fail(MUONH_EINVAL, "src is NULL");
+  if (!codes != !scales || !codes_t != !scales_t)
+    return fail(MUONH_EINVAL, "codes and scales (codes_t and scales_t) go together");
+  if (!codes && !codes_t) return fail(MUONH_EINVAL, "no output given");
+  const int esize = dtype == MUONH_DT_BF16 ? 2 : 4;
+  if (misaligned(src, esize)) return fail(MUONH_EINVAL, "src is not aligned to its type");
+  if (misaligned(codes, 16) || misaligned(codes_t, 16) || misaligned(scales, 4) || misaligned(scales_t, 4))
+    return fail(MUONH_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
+  const int64_t tr = ceil_div(rows, kBlock), tc = ceil_div(cols, kBlock);
+  if (tr * tc > kMaxBlocks) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more");
+  const Span spans[5] = {
+      span("src", src, ((rows - 1) * src_ld + cols) * esize),
+      span("codes", codes, rows * code_ld(cols)),
+      span("scales", scales, scale_rows(rows, block) * scale_ld(cols)),
+      span("codes_t", codes_t, cols * code_ld(rows)),
+      span("scales_t", scales_t, scale_rows(cols, block) * scale_ld(rows))};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(spans[i], spans[j]))
+        return fail(MUONH_EALIAS, "%s overlaps %s", spans[j].name, spans[i].name);
+
+  Args a{};
+  a.ngroups = 1;
+  a.g[0] = Group{rows, cols, src_ld, 0, (uint32_t)tc, (uint32_t)(tr * tc), 0};
+  a.src = src;
+  a.codes = codes;
+  a.scales = scales;
+  a.codes_t = codes_t;
+  a.scales_t = scales_t;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const bool plain = codes != nullptr, trans = codes_t != nullptr;
+  if (dtype == MUONH_DT_BF16) {
+    if (block == MUONH_FP8_TILES) launch_forms<true, true>(a, tr * tc, plain, trans, s);
+    else launch_forms<true, false>(a, tr * tc, plain, trans, s);
+  } else {
+    if (block == MUONH_FP8_TILES) launch_forms<false, true>(a, tr * tc, plain, trans, s);
+    else launch_forms<false, false>(a, tr * tc, plain, trans, s);
+  }
+  return launched("fp8 quantize");
+}
+
+int muonh_fp8_weights(const muonh_plan* plan, const float* const* W, void* const* codes,
+                      void* const* scales, void* const* codes_t, void* const* scales_t,
+                      void* stream) {
+  using namespace muonh;
+  using namespace muonh::fp8;
+  if (!plan) return fail(MUONH_EINVAL, "plan is NULL");
+  if (!W || !codes || !scales) return fail(MUONH_EINVAL, "W, codes and scales must be device arrays");
+  if (!codes_t != !scales_t) return fail(MUONH_EINVAL, "codes_t and scales_t go together");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int ng = plan_num_groups(plan);
+  // both passes walk the same launches: the first one only counts blocks
+  for (int pass = 0; pass < 2; ++pass)
+    for (int g0 = 0; g0 < ng; g0 += kMaxGroups) {
+      Args a{};
+      a.ptrs = 1;
+      a.src = W;
+      a.codes = const_cast<void**>(codes);
+      a.scales = const_cast<void**>(scales);
+      a.codes_t = const_cast<void**>(codes_t);
+      a.scales_t = const_cast<void**>(scales_t);
+      int64_t blocks = 0;
+      for (int i = g0; i < ng && i < g0 + kMaxGroups; ++i) {
+        const PlanGroup p = plan_group(plan, i);
+        const int64_t tr = ceil_div(p.rows, kBlock), tc = ceil_div(p.cols, kBlock);
+        a.g[a.ngroups++] = Group{p.rows, p.cols, p.cols, (uint32_t)p.first, (uint32_t)tc,
+                                 (uint32_t)(tr * tc), (uint32_t)blocks};
+        blocks += tr * tc * p.count;
+        if (blocks > kMaxBlocks) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more in one launch");
+      }
+      if (pass == 0) continue;
+      launch_forms<false, true>(a, blocks, true, codes_t != nullptr, s);
+      if (const int err = launched("fp8 weights")) return err;
+    }
+  return MUONH_OK;
+}
+
+}  // extern "C"

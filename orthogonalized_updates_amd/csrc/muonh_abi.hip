@@ -830,3 +830,10 @@ int muonh_read_update(const muonh_plan* plan, int64_t index, float* dst, const v
 }
 
 }  // extern "C"
+
+int muonh::plan_num_groups(const muonh_plan* p) { return (int)p->groups.size(); }
+
+muonh::PlanGroup muonh::plan_group(const muonh_plan* p, int i) {
+  const GroupPlan& g = p->groups[i];
+  return PlanGroup{g.rows, g.cols, g.count, g.first};
+}

@@ -200,3 +200,13 @@ hipError_t launch_gemm(GemmMode mode, NsPrec prec, const GemmArgs& a, hipStream_
 hipError_t launch_zero_i32(int* p, int n, hipStream_t s);
 
 }  // namespace muonh
+
+// Shape groups of a plan, for the sources that do not see its definition.
+struct muonh_plan;
+namespace muonh {
+struct PlanGroup {
+  int rows, cols, count, first;
+};
+int plan_num_groups(const muonh_plan* p);
+PlanGroup plan_group(const muonh_plan* p, int i);
+}  // namespace muonh
