@@ -17,6 +17,7 @@
 // use v_mfma_f32_16x16x32_bf16, whose sums are accurate to fp32 (measured 1e-7
 // at k = 8192), at half the matrix rate.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8_internal.h"
 
@@ -126,6 +127,70 @@ __device__ __forceinline__ void put(const MatArgs& a, int64_t i, int64_t j, cons
   }
 }
 
+// Fragment row r of b's fragment f within a wave's 64 columns -> column. For
+// 2-byte results (PAIR) neighbouring fragments hold 8 consecutive columns.
+template <bool PAIR>
+__device__ __forceinline__ int b_row(int f, int r) {
+  return PAIR ? 32 * (f >> 1) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3) : 16 * f + r;
+}
+
+// Stores a wave's 16 NA rows x 64 columns from row i0, column j0: acc[q][f],
+// b's fragment q, a's fragment f; lane l holds row 16 f + l%16 and columns
+// b_row(q, 4 (l/16) ..+3).
+template <typename T, int NA>
+__device__ __forceinline__ void store_wave(const MatArgs& a, int split, int64_t i0, int64_t j0, int lane,
+                                           const f32x4 (&acc)[4][NA]) {
+  constexpr bool kPair = sizeof(T) == 2;
+  const int r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int f = 0; f < NA; ++f) {
+    const int64_t i = i0 + 16 * f + r16;
+    if (i >= a.m) continue;
+    if (a.part) {
+      float* p = a.part + ((int64_t)split * a.m + i) * a.pld;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t j = j0 + b_row<kPair>(q, 4 * g);
+        if (j < a.pld) *reinterpret_cast<f32x4*>(p + j) = acc[q][f];  // pld: a multiple of 4
+      }
+    } else if constexpr (kPair) {
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[q][f][e];
+          v[4 + e] = acc[q + 1][f][e];
+        }
+        put<T, 8>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {acc[q][f][0], acc[q][f][1], acc[q][f][2], acc[q][f][3]};
+        put<T, 4>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
+      }
+    }
+  }
+}
+
+// Block -> tile. Blocks are dealt to the 8 XCDs in turn; each XCD takes a
+// contiguous eighth of the tile list, so the tiles resident on it share
+// operand rows in its L2. The list runs in bands of 8 tile rows, down each
+// tile column of the band. False: the block has no tile.
+__device__ __forceinline__ bool map_tile(const MatArgs& a, int b, int& ti, int& tj) {
+  const int64_t tot = (int64_t)a.tm * a.tn;
+  const int x = b & 7, lo = (int)((x * tot) >> 3), hi = (int)(((x + 1) * tot) >> 3);
+  const int t = lo + (b >> 3);
+  if (t >= hi) return false;
+  const int per_band = 8 * a.tn, band = t / per_band, rr = t - band * per_band;
+  const int h = min(8, a.tm - 8 * band);
+  ti = 8 * band + rr % h;
+  tj = rr / h;
+  return true;
+}
+int map_grid(int64_t tiles) { return (int)(8 * ceil_div(tiles, 8)); }
+
 // Waits until at most VM of this wave's memory operations are outstanding and
 // its LDS reads have retired, then the workgroup's barrier; neither memory
 // accesses nor MFMAs move across.
@@ -169,20 +234,15 @@ constexpr int kOpStage = kT * kBlock;     // 16 KB
 constexpr int kStageBytes = 2 * kOpStage;
 constexpr int kScaleBytes = 2 * kT * 4;   // 4 k blocks of both operands' rows
 
-// Tile row (0 .. 63 of a wave's 64 columns) held by fragment f, fragment row r.
-template <bool PAIR>
-__device__ __forceinline__ int b_row(int f, int r) {
-  return PAIR ? 32 * (f >> 1) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3) : 16 * f + r;
-}
-
 template <typename T, bool WIDE>
 __global__ __launch_bounds__(256, 2) void k_matmul_tile(MatArgs a) {
   constexpr bool kPair = sizeof(T) == 2;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes + 2 * kScaleBytes];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tile = blockIdx.x, split = blockIdx.y;
-  const int ti = tile % a.tm, tj = tile / a.tm;
+  const int split = blockIdx.y;
+  int ti, tj;
+  if (!map_tile(a, blockIdx.x, ti, tj)) return;
   const int kb0 = split * a.per, kb1 = min(kb0 + a.per, a.nkb);
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
 
@@ -247,38 +307,200 @@ __global__ __launch_bounds__(256, 2) void k_matmul_tile(MatArgs a) {
     mma_block<WIDE, 4, 4>(fb, fa, sb, sa, acc);
   }
 
-  // lane: row 16 f + l%16 of the wave's rows; columns by b_row
+  store_wave<T, 4>(a, split, (int64_t)ti * kT + 64 * wm, (int64_t)tj * kT + 64 * wn, lane, acc);
+}
+
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles, 8 waves (2 x 4, wave tile 128 x 64), two LDS stages of one
+// k block (2 x 64 KB): 8-bit products with enough tiles for the chip.
+//
+// The waves form two groups of 4, one wave of each per SIMD, that take turns
+// phase by phase: one group's 16 MFMAs run while the other reads LDS and
+// issues DMA, so the matrix cores see no gap and MFMA waves issue no memory
+// instruction. A wave's block of k takes two turns, 64 of its 128 rows each
+// (A0, A1), which keeps the fragments at 64 registers beside 128
+// accumulators. Phases of block s, group 0 | group 1:
+//   4s    read B, A0         | multiply A1 of s-1
+//   4s+1  multiply A0        | read B, A0
+//   4s+2  read A1            | multiply A0
+//   4s+3  multiply A1        | read A1
+// A stage is refilled part by part as it falls free, each part at least
+// three phases before block s+2 needs it:
+//   4s+2  group 0: B and b's scales (last read in 4s+1)
+//   4s+3  group 1: A rows 0-191 (group 0's half, last read in 4s+2, and group
+//         1's A0, last read in 4s+1)
+//   4s+4  group 0: A rows 192-255 (group 1's A1, last read in 4s+3) and a's
+//         scales (read with each half): refill_tail
+// and waited for at the end of 4s+7. Every phase ends in a barrier that
+// retires the wave's LDS reads.
+// ---------------------------------------------------------------------------
+constexpr int kB = 256;
+constexpr int kBigOp = kB * kBlock;            // 32 KB
+constexpr int kBigStage = 2 * kBigOp;          // A, then B
+constexpr int kBigScales = 2 * kB * 4;         // a's rows, then b's: 4 k blocks each
+// 32-bit offsets from a tile's first row: 256 rows of less than 2^23 bytes
+constexpr int64_t kBigMaxLd = 1 << 23;
+
+// As dma16 / dma4, the source at a scalar base plus the lane's 32-bit offset.
+__device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
+}
+__device__ __forceinline__ void dma4s(const uint8_t* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
+}
+
+template <typename T, int G>
+__device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint32_t base, const uint8_t* pa,
+                                         const uint8_t* pb, const uint8_t* sca, const uint8_t* scb,
+                                         const uint32_t (&off)[10], uint32_t soa, uint32_t sob, int kb0, int nk, int wave, int lane,
+                                         f32x4 (&acc)[4][8]) {
+  const int w4 = wave & 3, r16 = lane & 15, g = lane >> 4;
+  const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);
+  i32x8 fa[4], fb[4];
+  int sa[4], sb[4];
+  auto frag = [&](const char* p) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(p + foff);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (foff ^ 64));
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  // scale byte (in the low 8 bits) of the lane's row of a fragment; rows of b
+  // follow a's 256
+  auto scale = [&](int s, int row) {
+    const char* q = lds + 2 * kBigStage + (s & 1) * kBigScales;
+    return *reinterpret_cast<const int*>(q + (row + r16) * 4) >> (((kb0 + s) & 3) * 8);
+  };
+  auto load_a = [&](int s, int half) {
+    const char* p = lds + (s & 1) * kBigStage + (128 * G + 64 * half) * kBlock;
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const int64_t i = (int64_t)ti * kT + 64 * wm + 16 * f + r16;
-    if (i >= a.m) continue;
-    const int64_t j0 = (int64_t)tj * kT + 64 * wn;
-    if (a.part) {
-      float* p = a.part + ((int64_t)split * a.m + i) * a.pld;
+    for (int f = 0; f < 4; ++f) {
+      fa[f] = frag(p + 16 * f * kBlock);
+      sa[f] = scale(s, 128 * G + 64 * half + 16 * f);
+    }
+  };
+  auto load_b = [&](int s) {
+    const char* p = lds + (s & 1) * kBigStage + kBigOp + 64 * w4 * kBlock;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t j = j0 + b_row<kPair>(q, 4 * g);
-        if (j < a.pld) *reinterpret_cast<f32x4*>(p + j) = acc[q][f];  // pld: a multiple of 4
-      }
-    } else if constexpr (kPair) {
+    for (int f = 0; f < 4; ++f) {
+      fb[f] = frag(p + 16 * f * kBlock);
+      sb[f] = scale(s, kB + 64 * w4 + 16 * f);
+    }
+  };
+  auto mul = [&](int half) {
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        float v[8];
+    for (int f = 0; f < 4; ++f)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[q][f][e];
-          v[4 + e] = acc[q + 1][f][e];
-        }
-        put<T, 8>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
-      }
+      for (int q = 0; q < 4; ++q)
+        acc[q][4 * half + f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            fb[q], fa[f], acc[q][4 * half + f], 0, 0, 0, sb[q], 0, sa[f]);
+  };
+  // this group's part of a refill of block s (see the table above)
+  auto refill = [&](int s) {
+    const uint32_t st = base + (s & 1) * kBigStage;
+    const int64_t k = (int64_t)(kb0 + s) * kBlock;
+    if (G == 0) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) dma16s(pb + k, off[q], st + kBigOp + (8 * w4 + q) * 1024);
+      dma4s(scb + ((kb0 + s) & ~3), sob, base + 2 * kBigStage + (s & 1) * kBigScales + kB * 4 + w4 * 256);
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v[4] = {acc[q][f][0], acc[q][f][1], acc[q][f][2], acc[q][f][3]};
-        put<T, 4>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
-      }
+      for (int q = 0; q < 6; ++q) dma16s(pa + k, off[q], st + (6 * w4 + q) * 1024);
     }
+  };
+  auto refill_tail = [&](int s) {  // group 0
+    const uint32_t st = base + (s & 1) * kBigStage;
+    const int64_t k = (int64_t)(kb0 + s) * kBlock;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) dma16s(pa + k, off[8 + q], st + (24 + 2 * w4 + q) * 1024);
+    dma4s(sca + ((kb0 + s) & ~3), soa, base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 256);
+  };
+  constexpr int kPart = G == 0 ? 9 : 6;  // memory operations of refill()
+
+  refill(0);
+  if (G == 0) refill_tail(0);
+  if (nk > 1) {
+    refill(1);
+    stage_barrier<kPart>();
+  } else {
+    stage_barrier<0>();
   }
+  if (G == 1) stage_barrier<63>();  // phase 0
+  // One block of k; LEFT: how many more blocks follow (2: at least two). The
+  // loop body has no branch: the compiler moves MFMAs across barriers into
+  // later basic blocks, and then keeps two sets of fragments alive.
+  auto block = [&](int s, auto left) {
+    constexpr int kLeft = decltype(left)::value;
+    load_b(s);
+    load_a(s, 0);
+    if constexpr (G == 0 && kLeft >= 1) refill_tail(s + 1);
+    stage_barrier<63>();
+    mul(0);
+    stage_barrier<63>();
+    load_a(s, 1);
+    if constexpr (kLeft >= 2) refill(s + 2);
+    // the end of phase 4s+3: block s+1 has landed; what was just issued for
+    // block s+2 may be in flight
+    constexpr int kLand = kLeft >= 2 ? kPart : 0;
+    stage_barrier<(G == 1 ? kLand : 63)>();
+    mul(1);
+    stage_barrier<(G == 0 ? kLand : 63)>();
+  };
+  int s = 0;
+  for (; s + 2 < nk; ++s) block(s, std::integral_constant<int, 2>{});
+  if (s + 1 < nk) block(s++, std::integral_constant<int, 1>{});
+  block(s, std::integral_constant<int, 0>{});
+  if (G == 0) stage_barrier<63>();  // group 1's last phase
+}
+
+template <typename T>
+__global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
+  constexpr bool kPair = sizeof(T) == 2;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kBigStage + 2 * kBigScales];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = blockIdx.y;
+  int ti, tj;
+  if (!map_tile(a, blockIdx.x, ti, tj)) return;
+  const int kb0 = split * a.per, nk = min(a.per, a.nkb - kb0);
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
+  // Tile bases, and this lane's source offsets for each DMA instruction: LDS
+  // rows 8 i .. +7 of an operand, lane l: row l / 8, position l % 8.
+  const int64_t ra = (int64_t)ti * kB, rb = (int64_t)tj * kB;
+  const uint8_t* pa = a.a.codes + ra * a.a.ld;
+  const uint8_t* pb = a.b.codes + rb * a.b.ld;
+  const int w4 = wave & 3;
+  auto off_a = [&](int i) {
+    const int lr = 8 * i + (lane >> 3);
+    return (uint32_t)(min(ra + lr, a.m - 1) - ra) * (uint32_t)a.a.ld + (uint32_t)(((lane & 7) ^ (lr & 7)) << 4);
+  };
+  auto off_b = [&](int i) {
+    const int lr = 8 * i + (lane >> 3);
+    const int r = 64 * (lr >> 6) + b_row<kPair>((lr & 63) >> 4, lr & 15);
+    return (uint32_t)(min(rb + r, a.n - 1) - rb) * (uint32_t)a.b.ld + (uint32_t)(((lane & 7) ^ (lr & 7)) << 4);
+  };
+  f32x4 acc[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{};
+  uint32_t off[10];
+  if (wave < 4) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) off[q] = off_b(8 * w4 + q);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) off[8 + q] = off_a(24 + 2 * w4 + q);
+    const int64_t r = min(ra + 64 * w4 + lane, a.m - 1);
+    const int64_t c = min(rb + 64 * w4 + b_row<kPair>(lane >> 4, lane & 15), a.n - 1);
+    const int64_t a0 = ra >> a.a.sshift, b0 = rb >> a.b.sshift;
+    const uint32_t soa = (uint32_t)((r >> a.a.sshift) - a0) * (uint32_t)a.a.sld;
+    const uint32_t sob = (uint32_t)((c >> a.b.sshift) - b0) * (uint32_t)a.b.sld;
+    big_loop<T, 0>(a, lds, base, pa, pb, a.a.scales + a0 * a.a.sld, a.b.scales + b0 * a.b.sld, off, soa, sob,
+                   kb0, nk, wave, lane, acc);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 6; ++q) off[q] = off_a(6 * w4 + q);
+    big_loop<T, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, kb0, nk, wave, lane, acc);
+  }
+  store_wave<T, 8>(a, split, ra + 128 * (wave >> 2), rb + 64 * w4, lane, acc);
 }
 
 // out (+)= the partial sums, split by split in order; 4 columns per thread.
@@ -355,18 +577,23 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_matmul_skinny(MatArgs a) 
 constexpr int64_t kCUs = 256;
 constexpr int64_t kMaxTiles = (1 << 22) - 1;
 
-enum Kind { kSkinny = 0, kTile = 1 };
+enum Kind { kSkinny = 0, kTile = 1, kBig = 2 };
 struct Choice {
   Kind kind;
   int splits, per;
   size_t ws_bytes;
 };
 
-Choice choose(int64_t m, int64_t n, int64_t k) {
+Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
   Choice c{kTile, 1, (int)ceil_div(k, kBlock), 0};
   const int64_t nkb = ceil_div(k, kBlock);
   if (m <= 64) {
     c.kind = kSkinny;
+    return c;
+  }
+  if (out_dtype == MUONH_DT_BF16 && k > 0 && code_ld(k) < kBigMaxLd &&
+      ceil_div(m, kB) * ceil_div(n, kB) >= kCUs / 2) {
+    c.kind = kBig;
     return c;
   }
   // Two workgroups fit a CU. Fewer tiles than that leave CUs idle: the k
@@ -391,9 +618,12 @@ int launch(const MatArgs& a, const Choice& c, hipStream_t s) {
       hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 2>), grid, thr, 0, s, a);
     else
       hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 4>), grid, thr, 0, s, a);
+  } else if (c.kind == kBig) {
+    if constexpr (!WIDE)
+      hipLaunchKernelGGL((k_matmul_big<T>), dim3((unsigned)map_grid((int64_t)a.tm * a.tn)), dim3(512), 0, s, a);
   } else {
-    hipLaunchKernelGGL((k_matmul_tile<T, WIDE>), dim3((unsigned)(a.tm * a.tn), (unsigned)a.splits),
-                       dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_matmul_tile<T, WIDE>),
+                       dim3((unsigned)map_grid((int64_t)a.tm * a.tn), (unsigned)a.splits), dim3(256), 0, s, a);
     if (a.part)
       hipLaunchKernelGGL((k_matmul_join<T>), dim3((unsigned)ceil_div(a.m * (a.pld >> 2), 256)),
                          dim3(256), 0, s, a);
@@ -430,9 +660,8 @@ extern "C" {
 
 size_t muonh_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
   using namespace muonh::fp8;
-  (void)out_dtype;
   if (bad_dim(m) || bad_dim(n) || bad_dim(k) || m == 0 || n == 0) return 0;
-  return choose(m, n, k).ws_bytes;
+  return choose(m, n, k, out_dtype).ws_bytes;
 }
 
 int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* out,
@@ -454,9 +683,9 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   const int esize = out_dtype == MUONH_DT_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(out) & (uintptr_t)(esize - 1))
     return fail(MUONH_EINVAL, "out is not aligned to its type");
-  const int64_t tm = ceil_div(m, kT), tn = ceil_div(n, kT);
-  if (tm * tn > kMaxTiles) return fail(MUONH_ESHAPE, "2^22 output tiles of 128 x 128 or more");
-  const Choice c = choose(m, n, k);
+  if (ceil_div(m, kT) * ceil_div(n, kT) > kMaxTiles)
+    return fail(MUONH_ESHAPE, "2^22 output tiles of 128 x 128 or more");
+  const Choice c = choose(m, n, k, out_dtype);
   if (c.ws_bytes) {
     if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the product needs %zu bytes", c.ws_bytes);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -489,8 +718,9 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   x.per = c.per;
   x.pld = ceil_div(n, 4) * 4;
   x.part = c.ws_bytes ? static_cast<float*>(workspace) : nullptr;
-  x.tm = (int)tm;
-  x.tn = (int)tn;
+  const int edge = c.kind == kBig ? kB : kT;
+  x.tm = (int)ceil_div(m, edge);
+  x.tn = (int)ceil_div(n, edge);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return out_dtype == MUONH_DT_BF16 ? launch<__bf16, false>(x, c, s) : launch<float, true>(x, c, s);
 }

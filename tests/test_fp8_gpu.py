@@ -175,7 +175,8 @@ def check_product(out, va, vb, dtype, old=None):
 
 SIZES = [(1, 1, 1), (1, 6144, 2048), (2, 17, 129), (16, 512, 2048), (17, 130, 1000), (33, 64, 128), (64, 300, 4096),
          (65, 15, 64), (128, 128, 128), (129, 257, 385), (300, 1, 700), (777, 1003, 501), (1024, 512, 256),
-         (200, 300, 8192), (513, 2050, 640), (2100, 1100, 192)]
+         (200, 300, 8192), (513, 2050, 640), (2100, 1100, 192), (2900, 2900, 100), (2817, 3000, 1301),
+         (4096, 2048, 384), (1536, 5400, 2560)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
