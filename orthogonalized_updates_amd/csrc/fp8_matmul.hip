@@ -349,7 +349,7 @@ __device__ __forceinline__ void dma4s(const uint8_t* base, uint32_t off, uint32_
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
 }
 
-template <typename T, int G>
+template <typename T, bool WIDE, int G>
 __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint32_t base, const uint8_t* pa,
                                          const uint8_t* pb, const uint8_t* sca, const uint8_t* scb,
                                          const uint32_t (&off)[10], uint32_t soa, uint32_t sob, int kb0, int nk, int wave, int lane,
@@ -386,12 +386,28 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
     }
   };
   auto mul = [&](int half) {
+    if constexpr (!WIDE) {
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+      for (int f = 0; f < 4; ++f)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        acc[q][4 * half + f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            fb[q], fa[f], acc[q][4 * half + f], 0, 0, 0, sb[q], 0, sa[f]);
+        for (int q = 0; q < 4; ++q)
+          acc[q][4 * half + f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fb[q], fa[f], acc[q][4 * half + f], 0, 0, 0, sb[q], 0, sa[f]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        bf16x8 wb[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) wb[q] = widen8(fb[q][2 * k], fb[q][2 * k + 1], scale_of(sb[q] & 255));
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const bf16x8 wa = widen8(fa[f][2 * k], fa[f][2 * k + 1], scale_of(sa[f] & 255));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[q][4 * half + f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], wa, acc[q][4 * half + f], 0, 0, 0);
+        }
+      }
+    }
   };
   // this group's part of a refill of block s (see the table above)
   auto refill = [&](int s) {
@@ -451,7 +467,7 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
   if (G == 0) stage_barrier<63>();  // group 1's last phase
 }
 
-template <typename T>
+template <typename T, bool WIDE>
 __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
   constexpr bool kPair = sizeof(T) == 2;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kBigStage + 2 * kBigScales];
@@ -493,12 +509,12 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
     const int64_t a0 = ra >> a.a.sshift, b0 = rb >> a.b.sshift;
     const uint32_t soa = (uint32_t)((r >> a.a.sshift) - a0) * (uint32_t)a.a.sld;
     const uint32_t sob = (uint32_t)((c >> a.b.sshift) - b0) * (uint32_t)a.b.sld;
-    big_loop<T, 0>(a, lds, base, pa, pb, a.a.scales + a0 * a.a.sld, a.b.scales + b0 * a.b.sld, off, soa, sob,
+    big_loop<T, WIDE, 0>(a, lds, base, pa, pb, a.a.scales + a0 * a.a.sld, a.b.scales + b0 * a.b.sld, off, soa, sob,
                    kb0, nk, wave, lane, acc);
   } else {
 #pragma unroll
     for (int q = 0; q < 6; ++q) off[q] = off_a(6 * w4 + q);
-    big_loop<T, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, kb0, nk, wave, lane, acc);
+    big_loop<T, WIDE, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, kb0, nk, wave, lane, acc);
   }
   store_wave<T, 8>(a, split, ra + 128 * (wave >> 2), rb + 64 * w4, lane, acc);
 }
@@ -591,7 +607,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
     c.kind = kSkinny;
     return c;
   }
-  if (out_dtype == MUONH_DT_BF16 && k > 0 && code_ld(k) < kBigMaxLd &&
+  if (k > 0 && code_ld(k) < kBigMaxLd &&
       ceil_div(m, kB) * ceil_div(n, kB) >= kCUs / 2) {
     c.kind = kBig;
     return c;
@@ -619,8 +635,7 @@ int launch(const MatArgs& a, const Choice& c, hipStream_t s) {
     else
       hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 4>), grid, thr, 0, s, a);
   } else if (c.kind == kBig) {
-    if constexpr (!WIDE)
-      hipLaunchKernelGGL((k_matmul_big<T>), dim3((unsigned)map_grid((int64_t)a.tm * a.tn)), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((k_matmul_big<T, WIDE>), dim3((unsigned)map_grid((int64_t)a.tm * a.tn)), dim3(512), 0, s, a);
   } else {
     hipLaunchKernelGGL((k_matmul_tile<T, WIDE>),
                        dim3((unsigned)map_grid((int64_t)a.tm * a.tn), (unsigned)a.splits), dim3(256), 0, s, a);
