@@ -22,7 +22,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 16;
 // Blocks of one launch: a launch has fewer than 2^32 threads.
-constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+constexpr int64_t kMaxBlocks = (1 << 24) - 8;
 
 // Bits of max |x| over finite entries -> scale byte e + 127, e >= -126.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
@@ -54,6 +54,7 @@ struct Group {
 struct Args {
   Group g[kMaxGroups];
   int ngroups;
+  uint32_t tiles;  // of all groups
   // one matrix (ptrs == 0), or device arrays of pointers indexed by matrix
   int ptrs;
   const void* src;
@@ -65,22 +66,27 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
   if (BF) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
   return static_cast<const float*>(p)[i];
 }
-// 8 consecutive entries from i; the address is 16-byte aligned.
+// 8 consecutive entries from i, at any multiple of the entry's size (gfx950
+// takes vector accesses at any address).
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 template <bool BF>
 __device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
   if (BF) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const u32x4_a2 w = *reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[2 * k] = __uint_as_float(w[k] << 16);
       v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
   } else {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const f32x4_a4* q = reinterpret_cast<const f32x4_a4*>(static_cast<const float*>(p) + i);
+    const f32x4_a4 a = q[0], b = q[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = a[k];
+      v[4 + k] = b[k];
+    }
   }
 }
 
@@ -97,15 +103,23 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, i
 
 // Thread (ty, tx) = (tid / 16, tid % 16) holds rows 8 ty .. +7, columns
 // 8 tx .. +7 of the tile. PLAIN, TRANS: the forms written; TILES: one scale.
+//
+// Blocks are dealt to the 8 XCDs in turn; each XCD takes a contiguous eighth
+// of the tiles, so that the scale bytes of neighbouring tiles, which share
+// cache lines in both forms, meet in one L2.
 template <bool BF, bool TILES, bool PLAIN, bool TRANS>
-__global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
+__global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   __shared__ uint32_t red[4][kBlock];                                  // maxima by wave
-  __shared__ __attribute__((aligned(16))) uint8_t stage[kBlock * kBlock];  // transposed codes
+  __shared__ uint8_t byte_of[2][kBlock];                               // scale bytes of rows, columns
+  __shared__ __attribute__((aligned(16))) uint8_t stage[TRANS ? kBlock * kBlock : 16];  // transposed codes
+  const uint32_t x = blockIdx.x & 7;
+  const uint32_t index = (uint32_t)(((uint64_t)x * a.tiles) >> 3) + (blockIdx.x >> 3);
+  if (index >= (uint32_t)(((uint64_t)(x + 1) * a.tiles) >> 3)) return;
   int gi = 0;
   for (int i = 1; i < a.ngroups; ++i)
-    if (blockIdx.x >= a.g[i].begin) gi = i;
+    if (index >= a.g[i].begin) gi = i;
   const Group& g = a.g[gi];
-  const uint32_t local = blockIdx.x - g.begin;
+  const uint32_t local = index - g.begin;
   const uint32_t m = local / g.tiles, t = local - m * g.tiles;
   const int64_t tr = t / g.tiles_c, tc = t - (uint32_t)tr * g.tiles_c;
   const int64_t mat = g.first + m;
@@ -119,8 +133,7 @@ __global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
   const int64_t rows = g.rows, cols = g.cols;
 
   float v[8][8];
-  const bool vec = ((reinterpret_cast<uintptr_t>(src) | (uintptr_t)(g.src_ld * (BF ? 2 : 4))) & 15u) == 0;
-  if (vec && c0 + 8 <= cols) {
+  if (c0 + 8 <= cols) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // rows past the end reload the last one, so that no load waits in a branch
@@ -178,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
         for (int off = 8; off > 0; off >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
         const uint32_t byte = scale_byte(mx);
         s = inv_scale(byte);
-        if (tx == 0 && r0 + i < rows) put_scale(pick(a.scales), r0 + i, tc, cols, byte);
+        if (tx == 0) byte_of[0][8 * ty + i] = (uint8_t)byte;
       }
       if (r0 + i < rows) {
         uint2 q;
@@ -189,6 +202,14 @@ __global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
     }
   }
 
+  if (PLAIN && TRANS && !TILES) {
+    // the second form takes its magnitudes anew: kept from the first one
+    // they would take 64 more registers
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(v[i][j]));
+  }
   if (TRANS) {
     float s[8];
     if (!TILES) {
@@ -211,7 +232,7 @@ __global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
         const int c = 8 * tx + j;
         const uint32_t byte = scale_byte(umax(umax(red[0][c], red[1][c]), umax(red[2][c], red[3][c])));
         s[j] = inv_scale(byte);
-        if (ty == 0 && c0 + j < cols) put_scale(pick(a.scales_t), c0 + j, tr, rows, byte);
+        if (ty == 0) byte_of[1][c] = (uint8_t)byte;
       }
     } else {
 #pragma unroll
@@ -227,7 +248,16 @@ __global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
       q.y = codes4(v[4][j] * s[j], v[5][j] * s[j], v[6][j] * s[j], v[7][j] * s[j]);
       *reinterpret_cast<uint2*>(stage + (8 * tx + j) * kBlock + ((ty ^ tx) << 3)) = q;
     }
-    __syncthreads();
+  }
+  if (TRANS || !TILES) __syncthreads();
+  if (!TILES) {
+    if (PLAIN && tid < kBlock && tr * kBlock + tid < rows)
+      put_scale(pick(a.scales), tr * kBlock + tid, tc, cols, byte_of[0][tid]);
+    const int c = tid - (kThreads - kBlock);
+    if (TRANS && c >= 0 && tc * kBlock + c < cols)
+      put_scale(pick(a.scales_t), tc * kBlock + c, tr, rows, byte_of[1][c]);
+  }
+  if (TRANS) {
     uint8_t* out = pick(a.codes_t);
     const int64_t ld = code_ld(rows);
 #pragma unroll
@@ -243,8 +273,8 @@ __global__ __launch_bounds__(kThreads) void k_quantize(Args a) {
 }
 
 template <bool BF, bool TILES>
-void launch_forms(const Args& a, int64_t blocks, bool plain, bool trans, hipStream_t s) {
-  const dim3 grid((unsigned)blocks), thr(kThreads);
+void launch_forms(const Args& a, bool plain, bool trans, hipStream_t s) {
+  const dim3 grid((unsigned)(8 * ceil_div(a.tiles, 8))), thr(kThreads);
   if (plain && trans)
     hipLaunchKernelGGL((k_quantize<BF, TILES, true, true>), grid, thr, 0, s, a);
   else if (plain)
@@ -319,6 +349,7 @@ int muonh_fp8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t col
   Args a{};
   a.ngroups = 1;
   a.g[0] = Group{rows, cols, src_ld, 0, (uint32_t)tc, (uint32_t)(tr * tc), 0};
+  a.tiles = (uint32_t)(tr * tc);
   a.src = src;
   a.codes = codes;
   a.scales = scales;
@@ -327,11 +358,11 @@ int muonh_fp8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t col
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool plain = codes != nullptr, trans = codes_t != nullptr;
   if (dtype == MUONH_DT_BF16) {
-    if (block == MUONH_FP8_TILES) launch_forms<true, true>(a, tr * tc, plain, trans, s);
-    else launch_forms<true, false>(a, tr * tc, plain, trans, s);
+    if (block == MUONH_FP8_TILES) launch_forms<true, true>(a, plain, trans, s);
+    else launch_forms<true, false>(a, plain, trans, s);
   } else {
-    if (block == MUONH_FP8_TILES) launch_forms<false, true>(a, tr * tc, plain, trans, s);
-    else launch_forms<false, false>(a, tr * tc, plain, trans, s);
+    if (block == MUONH_FP8_TILES) launch_forms<false, true>(a, plain, trans, s);
+    else launch_forms<false, false>(a, plain, trans, s);
   }
   return launched("fp8 quantize");
 }
@@ -366,7 +397,8 @@ int muonh_fp8_weights(const muonh_plan* plan, const float* const* W, void* const
         if (blocks > kMaxBlocks) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more in one launch");
       }
       if (pass == 0) continue;
-      launch_forms<false, true>(a, blocks, true, codes_t != nullptr, s);
+      a.tiles = (uint32_t)blocks;
+      launch_forms<false, true>(a, true, codes_t != nullptr, s);
       if (const int err = launched("fp8 weights")) return err;
     }
   return MUONH_OK;
