@@ -9,8 +9,8 @@
 // maxima by lane exchanges and LDS, and writes one or both forms: 4 (fp32) or
 // 2 (bf16) bytes read and 1 or 2 written per entry, HBM-bound.
 //
-// A scale is a power of two, so x * 2^-e is exact and the conversion
-// instruction's rounding (nearest, ties to even) is the only one. The
+// A scale is a power of two, so the conversion instruction, which divides by
+// it, rounds once (to nearest, ties to even). The
 // exponent comes from the bits of the maximum a = 1.f * 2^E: 448 = 1.75 * 2^8,
 // so e = E - 8 where 1.f <= 1.75, else E - 7.
 #include "fp8_internal.h"
@@ -29,21 +29,52 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   const int b = (int)((amax_bits + 0x1fffffu) >> 23) - 8;
   return (uint32_t)(b < 1 ? 1 : b);
 }
-// 2^-e = 2^(127 - byte): byte in [1, 247], so the result is a normal number.
-__device__ __forceinline__ float inv_scale(uint32_t byte) {
-  return __uint_as_float((254u - byte) << 23);
-}
-// |x|'s bits, 0 for NaN and infinities (as integers they order like values).
-__device__ __forceinline__ uint32_t mag(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
-}
+// The scale itself, 2^e: byte in [1, 247], a normal number.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// 4 values to 4 codes, the first in the low byte. |v| <= 448 where finite.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+// Bits of max |x| over the finite ones of 8 values (they order like the
+// values). One v_max3_f32 takes two of them, magnitudes included; only where
+// that meets an infinity or a NaN are the finite ones picked one by one.
+__device__ __forceinline__ float max3(float m, float a, float b) {
+  float r;
+  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(m), "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t amax8(float a, float b, float c, float d, float e, float f, float g,
+                                          float h) {
+  uint32_t m = __float_as_uint(max3(max3(max3(max3(0.f, a, b), c, d), e, f), g, h));
+  if (m >= 0x7f800000u) {
+    const float v[8] = {a, b, c, d, e, f, g, h};
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+      if (u < 0x7f800000u) m = umax(m, u);
+    }
+  }
+  return m;
+}
+
+// Maximum over the 16 lanes of a DPP row, in all of them.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  return umax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t max_row16(uint32_t v) {
+  v = max_dpp<0xB1>(v);   // quad [1,0,3,2]
+  v = max_dpp<0x4E>(v);   // quad [2,3,0,1]
+  v = max_dpp<0x141>(v);  // mirrored halves: the other quad of 8
+  return max_dpp<0x140>(v);  // mirrored row: the other 8
+}
+
+// 4 values over a scale 2^e (exact) to 4 codes, the first in the low byte.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s) {
+  s16x2 v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(s16x2{0, 0}, a, b, s, false);
+  v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, s, true);
+  return __builtin_bit_cast(uint32_t, v);
 }
 
 struct Group {
@@ -109,7 +140,7 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, i
 // cache lines in both forms, meet in one L2.
 template <bool BF, bool TILES, bool PLAIN, bool TRANS>
 __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
-  __shared__ uint32_t red[4][kBlock];                                  // maxima by wave
+  __shared__ __attribute__((aligned(16))) uint32_t red[4][kBlock];                                  // maxima by wave
   __shared__ uint8_t byte_of[2][kBlock];                               // scale bytes of rows, columns
   __shared__ __attribute__((aligned(16))) uint8_t stage[TRANS ? kBlock * kBlock : 16];  // transposed codes
   const uint32_t x = blockIdx.x & 7;
@@ -153,26 +184,22 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
         v[i][j] = r0 + i < rows && c0 + j < cols ? load1<BF>(src, (r0 + i) * g.src_ld + c0 + j) : 0.f;
   }
 
-  uint32_t tile_byte = 0;
+  float scale = 1.f;  // of the tile
   if (TILES) {
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = umax(mx, mag(v[i][j]));
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
+      mx = umax(mx, amax8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7]));
+    mx = max_row16(mx);
+    mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
+    mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
     if (lane == 0) red[0][wave] = mx;
     __syncthreads();
-    tile_byte = scale_byte(umax(umax(red[0][0], red[0][1]), umax(red[0][2], red[0][3])));
-    const float inv = inv_scale(tile_byte);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+    const uint32_t byte = scale_byte(umax(umax(red[0][0], red[0][1]), umax(red[0][2], red[0][3])));
+    scale = scale_of(byte);
     if (tid == 0) {
-      if (PLAIN) put_scale(pick(a.scales), tr, tc, cols, tile_byte);
-      if (TRANS) put_scale(pick(a.scales_t), tc, tr, rows, tile_byte);
+      if (PLAIN) put_scale(pick(a.scales), tr, tc, cols, byte);
+      if (TRANS) put_scale(pick(a.scales_t), tc, tr, rows, byte);
     }
   }
 
@@ -181,62 +208,58 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
     const int64_t ld = code_ld(cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float s = 1.f;
+      float s = scale;
       if (!TILES) {
-        uint32_t mx = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mx = umax(mx, mag(v[i][j]));
-        // the 16 threads of a row are 16 consecutive lanes
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
-        const uint32_t byte = scale_byte(mx);
-        s = inv_scale(byte);
+        // the 16 threads of a row are the lanes of a DPP row
+        const uint32_t byte = scale_byte(
+            max_row16(amax8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7])));
+        s = scale_of(byte);
         if (tx == 0) byte_of[0][8 * ty + i] = (uint8_t)byte;
       }
       if (r0 + i < rows) {
         uint2 q;
-        q.x = codes4(v[i][0] * s, v[i][1] * s, v[i][2] * s, v[i][3] * s);
-        q.y = codes4(v[i][4] * s, v[i][5] * s, v[i][6] * s, v[i][7] * s);
+        q.x = codes4(v[i][0], v[i][1], v[i][2], v[i][3], s);
+        q.y = codes4(v[i][4], v[i][5], v[i][6], v[i][7], s);
         *reinterpret_cast<uint2*>(codes + (r0 + i) * ld + c0) = q;
       }
     }
   }
 
-  if (PLAIN && TRANS && !TILES) {
-    // the second form takes its magnitudes anew: kept from the first one
-    // they would take 64 more registers
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(v[i][j]));
-  }
   if (TRANS) {
     float s[8];
     if (!TILES) {
       uint32_t mx[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mx[j] = 0;
+      for (int j = 0; j < 8; ++j)
+        mx[j] = amax8(v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]);
+      // The wave's 4 thread rows: a swap of lane halves brings both halves'
+      // maxima of one column together, of column j in the lower lanes and of
+      // j + 4 in the upper ones; then the same with rows of 16 lanes.
+      uint32_t h[4], w[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx[j] = umax(mx[j], mag(v[i][j]));
-        // the wave's 4 thread rows, then the 4 waves through LDS
-        mx[j] = umax(mx[j], (uint32_t)__shfl_xor((int)mx[j], 16, 64));
-        mx[j] = umax(mx[j], (uint32_t)__shfl_xor((int)mx[j], 32, 64));
+      for (int j = 0; j < 4; ++j) {
+        const auto p = __builtin_amdgcn_permlane32_swap(mx[j], mx[j + 4], false, false);
+        h[j] = umax(p[0], p[1]);
       }
-      if (lane < 16)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) red[wave][8 * tx + j] = mx[j];
+      for (int j = 0; j < 2; ++j) {
+        const auto p = __builtin_amdgcn_permlane16_swap(h[j], h[j + 2], false, false);
+        w[j] = umax(p[0], p[1]);
+      }
+      // lane 16 g + tx: columns 8 tx + 4 (g / 2) + 2 (g % 2) + {0, 1}
+      const int g = lane >> 4;
+      *reinterpret_cast<uint2*>(&red[wave][8 * tx + 4 * (g >> 1) + 2 * (g & 1)]) = make_uint2(w[0], w[1]);
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = 8 * tx + j;
         const uint32_t byte = scale_byte(umax(umax(red[0][c], red[1][c]), umax(red[2][c], red[3][c])));
-        s[j] = inv_scale(byte);
+        s[j] = scale_of(byte);
         if (ty == 0) byte_of[1][c] = (uint8_t)byte;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = 1.f;
+      for (int j = 0; j < 8; ++j) s[j] = scale;
     }
     // Row c of the staged tile: 16 pieces of 8 codes (piece = thread row),
     // piece p at position p ^ (c / 8), so that the 16 thread columns of a
@@ -244,8 +267,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       uint2 q;
-      q.x = codes4(v[0][j] * s[j], v[1][j] * s[j], v[2][j] * s[j], v[3][j] * s[j]);
-      q.y = codes4(v[4][j] * s[j], v[5][j] * s[j], v[6][j] * s[j], v[7][j] * s[j]);
+      q.x = codes4(v[0][j], v[1][j], v[2][j], v[3][j], s[j]);
+      q.y = codes4(v[4][j], v[5][j], v[6][j], v[7][j], s[j]);
       *reinterpret_cast<uint2*>(stage + (8 * tx + j) * kBlock + ((ty ^ tx) << 3)) = q;
     }
   }
