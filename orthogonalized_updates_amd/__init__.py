@@ -612,9 +612,16 @@ class Fp8Matrix:
         """Storage with undefined contents."""
         import torch
         c, s = _fp8_layout(rows, cols, block)
-        dev = device if device is not None else "cuda"
-        return cls(torch.empty(c, dtype=torch.float8_e4m3fn, device=dev),
-                   torch.empty(s, dtype=torch.float8_e8m0fnu, device=dev), (rows, cols), block)
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            raise ValueError("codes and scales must be on one ROCm GPU")
+        # made in its layout, so without __init__'s checks
+        m = cls.__new__(cls)
+        m.codes = torch.empty(c, dtype=torch.float8_e4m3fn, device=dev)
+        m.scales = torch.empty(s, dtype=torch.float8_e8m0fnu, device=dev)
+        m.shape, m.block, m.device = (rows, cols), block, m.codes.device
+        m.desc = Fp8Desc(m.codes.data_ptr(), m.scales.data_ptr(), rows, cols, FP8_BLOCKS[block])
+        return m
 
     def dequantize(self):
         """The values it stands for, fp32 (torch operations; for inspection)."""
@@ -669,12 +676,26 @@ def _fp8_dt(torch, dtype) -> int:
 def _row_pitch(t, name: str) -> int:
     """Elements between the rows of a 2-d tensor whose rows are contiguous."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name}'s rows must be contiguous (stride 1 along columns)")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if rows <= 1:
+        return max(cols, 1)
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
     return ld
+
+
+def _on_device(torch, dev, fn, *args) -> None:
+    """fn(*args, stream) with dev current, on its current stream. The raw
+    stream handle and the comparison cost well under a microsecond; a device
+    guard and a Stream object on every call took about a third of a small
+    call's host time."""
+    if torch.cuda.current_device() == dev.index:
+        check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
 
 
 def fp8_quantize(x, block: str = "rows", forms: str = "plain",
@@ -712,9 +733,8 @@ def fp8_quantize(x, block: str = "rows", forms: str = "plain",
             raise ValueError(f"{name} must be a {shape} Fp8Matrix of block {block!r} on {dev}")
         got.append(o)
     ptr = [v for o in got for v in ((o.desc.codes, o.desc.scales) if o is not None else (None, None))]
-    with torch.cuda.device(dev):
-        check(get_lib().muonh_fp8_quantize(x.data_ptr(), dt, rows, cols, ld, FP8_BLOCKS[block], *ptr,
-                                           int(torch.cuda.current_stream(dev).cuda_stream)))
+    _on_device(torch, dev, get_lib().muonh_fp8_quantize, x.data_ptr(), dt, rows, cols, ld,
+               FP8_BLOCKS[block], *ptr)
     return tuple(got)
 
 
@@ -754,12 +774,10 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
             raise ValueError(f"out must be a {shape} tensor on {dev}")
     ld = _row_pitch(out, "out")
     lib = get_lib()
-    with torch.cuda.device(dev):
-        nbytes = lib.muonh_fp8_matmul_workspace_bytes(m, n, a.shape[1], dt)
-        # from torch's allocator on the current stream: calls on other streams
-        # and captured graphs get memory of their own
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        check(lib.muonh_fp8_matmul(ctypes.byref(a.desc), ctypes.byref(b.desc), out.data_ptr(), dt, ld,
-                                   int(bool(accumulate)), ws.data_ptr() if nbytes else None, nbytes,
-                                   int(torch.cuda.current_stream(dev).cuda_stream)))
+    nbytes = lib.muonh_fp8_matmul_workspace_bytes(m, n, a.shape[1], dt)
+    # from torch's allocator on the current stream: calls on other streams and
+    # captured graphs get memory of their own
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _on_device(torch, dev, lib.muonh_fp8_matmul, a.desc, b.desc, out.data_ptr(), dt, ld,
+               1 if accumulate else 0, None if ws is None else ws.data_ptr(), nbytes)
     return out

@@ -48,7 +48,6 @@ struct MatArgs {
   void* out;
   int64_t ldo;
   int accumulate;
-  int vec;           // out's address and pitch allow 16-byte accesses
   float* part;       // partial sums [split][m][pld], or nullptr
   int64_t pld;
   int splits, per;   // k blocks per split
@@ -108,8 +107,9 @@ __device__ __forceinline__ void mma_block(const i32x8 (&x)[NX], const i32x8 (&y)
 template <typename T, int CNT>
 __device__ __forceinline__ void put(const MatArgs& a, int64_t i, int64_t j, const float (&v)[CNT]) {
   T* p = static_cast<T*>(a.out) + i * a.ldo + j;
-  typedef T vecT __attribute__((ext_vector_type(CNT)));
-  if (a.vec && j + CNT <= a.n) {
+  // at any multiple of T's size: gfx950 takes vector accesses at any address
+  typedef T vecT __attribute__((ext_vector_type(CNT), aligned(sizeof(T))));
+  if (j + CNT <= a.n) {
     vecT w;
     if (a.accumulate) {
       const vecT o = *reinterpret_cast<const vecT*>(p);
@@ -134,12 +134,12 @@ __device__ __forceinline__ int b_row(int f, int r) {
   return PAIR ? 32 * (f >> 1) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3) : 16 * f + r;
 }
 
-// Stores a wave's 16 NA rows x 64 columns from row i0, column j0: acc[q][f],
+// Stores a wave's 16 NA rows x 16 NB columns from row i0, column j0: acc[q][f],
 // b's fragment q, a's fragment f; lane l holds row 16 f + l%16 and columns
 // b_row(q, 4 (l/16) ..+3).
-template <typename T, int NA>
+template <typename T, int NA, int NB>
 __device__ __forceinline__ void store_wave(const MatArgs& a, int split, int64_t i0, int64_t j0, int lane,
-                                           const f32x4 (&acc)[4][NA]) {
+                                           const f32x4 (&acc)[NB][NA]) {
   constexpr bool kPair = sizeof(T) == 2;
   const int r16 = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -149,13 +149,13 @@ __device__ __forceinline__ void store_wave(const MatArgs& a, int split, int64_t 
     if (a.part) {
       float* p = a.part + ((int64_t)split * a.m + i) * a.pld;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < NB; ++q) {
         const int64_t j = j0 + b_row<kPair>(q, 4 * g);
         if (j < a.pld) *reinterpret_cast<f32x4*>(p + j) = acc[q][f];  // pld: a multiple of 4
       }
     } else if constexpr (kPair) {
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
+      for (int q = 0; q < NB; q += 2) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -166,7 +166,7 @@ __device__ __forceinline__ void store_wave(const MatArgs& a, int split, int64_t 
       }
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < NB; ++q) {
         const float v[4] = {acc[q][f][0], acc[q][f][1], acc[q][f][2], acc[q][f][3]};
         put<T, 4>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
       }
@@ -204,91 +204,113 @@ __device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// LDS DMA: lane l's 16 (4) bytes at g go to LDS bytes m0 + 16 l (4 l). No
-// register results; waits and barriers are the caller's.
-__device__ __forceinline__ void dma16(const void* g, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "{m0}"(m0) : "memory");
+// LDS DMA: lane l's 16 (4) bytes at base + off go to LDS bytes m0 + 16 l (4 l).
+// No register results; waits and barriers are the caller's.
+__device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
 }
-__device__ __forceinline__ void dma4(const void* g, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "{m0}"(m0) : "memory");
+__device__ __forceinline__ void dma4s(const uint8_t* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
 }
 
 // ---------------------------------------------------------------------------
-// 128 x 128 tiles, 4 waves of 64 x 64, two LDS stages of one k block (2 x 32
-// KB): the DMA of block t + 1 runs under the MFMAs of block t.
-//
-// An LDS row holds the 128 codes of one operand row; 16-byte chunk c of row r
-// sits at position c ^ (r & 7), which spreads the 16 rows x 4 chunks of a
-// fragment read over the banks (measured: 510 GB/s per CU against 290 with
-// chunk pairs 2g, 2g + 1). The DMA writes LDS linearly, so the lane's source
-// chunk is permuted instead. Rows past the matrix reload its last row; their
-// results are not stored.
+// LDS layout of the tiled kernels: an LDS row holds the 128 codes of one
+// operand row; 16-byte chunk c of row r sits at position c ^ (r & 7), which
+// spreads the 16 rows x 4 chunks of a fragment read over the banks (measured:
+// 510 GB/s per CU against 290 with chunk pairs 2g, 2g + 1 per lane). The DMA
+// writes LDS linearly, so the lane's source chunk is permuted instead. Rows
+// past the matrix reload its last row; their results are not stored.
 //
 // The b operand is the MFMA's first one, so a lane's 4 accumulators are 4
 // consecutive columns of one row of out. For 2-byte results b's rows are
 // also dealt to the fragments so that a lane holds 8 consecutive columns in
-// two neighbouring fragments: 16-byte stores, whole 64-byte runs per row.
+// two neighbouring fragments (b_row): 16-byte stores, 64-byte runs per row.
+//
+// 128 x 128 tiles, a ring of 4 LDS stages of one k block (32 KB each). The 8
+// waves form two groups of 4 (2 x 2, wave tile 64 x 64), one wave of each per
+// SIMD, that take the k blocks in turn: in phase p one group reads block p's
+// fragments and sends the DMA of block p+3, into the stage that the other
+// group read in phase p-1, while the other group multiplies block p-1. A
+// block lands within the two phases after its own, waited for by the waves
+// that sent it. Every phase ends in a barrier that retires LDS reads. At the
+// end each wave hands half of its sums to its partner in the other group.
+//
+// With one group of 4 waves, reads, DMA and MFMAs follow one another: 0.5-0.7
+// us a block however many stages were in flight; with two groups of 64 x 32
+// waves that share each block, the reads and DMA of a phase outlast its 8
+// MFMAs: 0.45 us.
 // ---------------------------------------------------------------------------
 constexpr int kT = 128;
 constexpr int kOpStage = kT * kBlock;     // 16 KB
-constexpr int kStageBytes = 2 * kOpStage;
-constexpr int kScaleBytes = 2 * kT * 4;   // 4 k blocks of both operands' rows
+constexpr int kStageBytes = 2 * kOpStage; // A, then B
+constexpr int kScaleBytes = 2 * kT * 4;   // 4 bytes of each row of both operands
+constexpr int kRing = 4;
+// 32-bit offsets from a tile's first row: 256 rows of less than 2^23 bytes
+constexpr int64_t kMaxTileLd = 1 << 23;
 
 template <typename T, bool WIDE>
-__global__ __launch_bounds__(256, 2) void k_matmul_tile(MatArgs a) {
+__global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
   constexpr bool kPair = sizeof(T) == 2;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes + 2 * kScaleBytes];
+  __shared__ __attribute__((aligned(1024))) char lds[kRing * (kStageBytes + kScaleBytes)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.y;
+  const int w4 = wave & 3, group = wave >> 2, split = blockIdx.y;
   int ti, tj;
   if (!map_tile(a, blockIdx.x, ti, tj)) return;
-  const int kb0 = split * a.per, kb1 = min(kb0 + a.per, a.nkb);
+  const int kb0 = split * a.per, nk = min(a.per, a.nkb - kb0);
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
+  const int64_t ra = (int64_t)ti * kT, rb = (int64_t)tj * kT;
 
-  // DMA of one stage: waves 0, 1 fill a's 128 rows, waves 2, 3 b's; 8
-  // instructions of 8 rows each. Lane l: row l / 8, position l % 8.
-  const Operand& op = wave < 2 ? a.a : a.b;
-  const int64_t row0 = (int64_t)(wave < 2 ? ti : tj) * kT;
-  const uint8_t* src[8];
+  // DMA of a block by one group: waves 0, 1 fill a's 128 rows, waves 2, 3 b's;
+  // 8 instructions of 8 rows (lane l: row l / 8, position l % 8), then the
+  // scales of 64 rows. Offsets from the tile's first row.
+  const bool is_a = w4 < 2;
+  const Operand& op = is_a ? a.a : a.b;
+  const int64_t first = is_a ? ra : rb;
+  auto row = [&](int lr) {
+    return min(first + (is_a ? lr : 64 * (lr >> 6) + b_row<kPair>((lr & 63) >> 4, lr & 15)), op.rows - 1);
+  };
+  uint32_t off[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const int lr = 64 * (wave & 1) + 8 * q + (lane >> 3);  // LDS row
-    const int mr = wave < 2 ? lr : 64 * (lr >> 6) + b_row<kPair>((lr & 63) >> 4, lr & 15);
-    const int64_t r = min(row0 + mr, op.rows - 1);
-    src[q] = op.codes + r * op.ld + (((lane & 7) ^ (lr & 7)) << 4);
+    const int lr = 64 * (w4 & 1) + 8 * q + (lane >> 3);
+    off[q] = (uint32_t)(row(lr) - first) * (uint32_t)op.ld + (uint32_t)(((lane & 7) ^ (lr & 7)) << 4);
   }
-  const uint32_t dst = base + (wave < 2 ? 0 : kOpStage) + (wave & 1) * 64 * kBlock;
-  // Scales: every 4 k blocks each wave fetches 4 bytes of 64 rows.
-  const uint8_t* ssrc;
-  {
-    const int lr = 64 * (wave & 1) + lane;
-    const int mr = wave < 2 ? lr : 64 * (lr >> 6) + b_row<kPair>((lr & 63) >> 4, lr & 15);
-    ssrc = op.scales + (min(row0 + mr, op.rows - 1) >> op.sshift) * op.sld;
-  }
-  const uint32_t sdst = base + 2 * kStageBytes + (wave < 2 ? 0 : kT * 4) + (wave & 1) * 64 * 4;
-  auto issue = [&](int kb) {
-    const int buf = (kb - kb0) & 1;
+  const int64_t s0 = first >> op.sshift;
+  const uint32_t soff = (uint32_t)((row(64 * (w4 & 1) + lane) >> op.sshift) - s0) * (uint32_t)op.sld;
+  const uint8_t* codes = op.codes + first * op.ld;
+  const uint8_t* scales = op.scales + s0 * op.sld;
+  const uint32_t dst = base + (is_a ? 0 : kOpStage) + (w4 & 1) * 64 * kBlock;
+  const uint32_t sdst = base + kRing * kStageBytes + w4 * 256;
+  auto fetch_part = [&](int s, int c) {  // quarter c
+    const int slot = s & (kRing - 1);
+    const int64_t k = (int64_t)(kb0 + s) * kBlock;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dma16(src[q] + (int64_t)kb * kBlock, dst + buf * kStageBytes + q * 1024);
-    if (kb == kb0 || (kb & 3) == 0) dma4(ssrc + (kb & ~3), sdst + ((kb >> 2) & 1) * kScaleBytes);
+    for (int q = 2 * c; q < 2 * c + 2; ++q)
+      dma16s(codes + k, off[q], dst + slot * kStageBytes + q * 1024);
+    if (c == 3) dma4s(scales + ((kb0 + s) & ~3), soff, sdst + slot * kScaleBytes);
   };
+  auto fetch = [&](int s) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) fetch_part(s, c);
+  };
+  constexpr int kOps = 9;  // memory operations of fetch()
 
-  const int wm = wave >> 1, wn = wave & 1;
-  const int r16 = lane & 15, g = lane >> 4;
+  const int wm = w4 >> 1, wn = w4 & 1, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);  // fragment rows start at multiples of 16
   f32x4 acc[4][4];  // [b fragment][a fragment]
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
-
-  if (kb0 < kb1) issue(kb0);
-  for (int kb = kb0; kb < kb1; ++kb) {
-    stage_barrier<0>();  // block kb has landed for all waves; the other stage is free
-    if (kb + 1 < kb1) issue(kb + 1);
-    const char* st = lds + ((kb - kb0) & 1) * kStageBytes;
-    const char* ss = lds + 2 * kStageBytes + ((kb >> 2) & 1) * kScaleBytes;
+  // Phases s (read, fetch) and s + 1 (multiply) of block s. No branch between
+  // the phases: the compiler moves MFMAs across barriers into later basic
+  // blocks, and then keeps two sets of fragments alive.
+  auto block = [&](int s, auto more) {
+    constexpr bool kMore = decltype(more)::value;
+    const char* st = lds + (s & (kRing - 1)) * kStageBytes;
+    const char* ss = lds + kRing * kStageBytes + (s & (kRing - 1)) * kScaleBytes;
+    const int sh = ((kb0 + s) & 3) * 8;
     auto frag = [&](const char* p) {
       const i32x4 lo = *reinterpret_cast<const i32x4*>(p + foff);
       const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (foff ^ 64));
@@ -296,18 +318,60 @@ __global__ __launch_bounds__(256, 2) void k_matmul_tile(MatArgs a) {
     };
     i32x8 fa[4], fb[4];
     int sa[4], sb[4];
-    const int sh = (kb & 3) * 8;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(st + (64 * wm + 16 * f) * kBlock);
       fb[f] = frag(st + kOpStage + (64 * wn + 16 * f) * kBlock);
-      sa[f] = *reinterpret_cast<const int*>(ss + (64 * wm + 16 * f + r16) * 4) >> sh;
-      sb[f] = *reinterpret_cast<const int*>(ss + kT * 4 + (64 * wn + 16 * f + r16) * 4) >> sh;
+      sa[f] = *reinterpret_cast<const int*>(ss + (64 * wm + 16 * f + r16) * 4);
+      sb[f] = *reinterpret_cast<const int*>(ss + (kT + 64 * wn + 16 * f + r16) * 4);
+      // between the reads: one after the other, reads and DMA outlast the
+      // other group's MFMAs
+      if constexpr (kMore) fetch_part(s + 3, f);
+    }
+    // block s + 1, sent by this group two phases ago, has landed
+    stage_barrier<(kMore ? kOps : 0)>();
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      sa[f] >>= sh;
+      sb[f] >>= sh;
     }
     mma_block<WIDE, 4, 4>(fb, fa, sb, sa, acc);
+    stage_barrier<63>();
+  };
+  if (group == 0) {
+    if (nk > 1) fetch(1);
+    stage_barrier<63>();
+  } else {
+    if (nk > 0) fetch(0);
+    if (nk > 2) {
+      fetch(2);
+      stage_barrier<kOps>();  // block 0 has landed
+    } else {
+      stage_barrier<0>();
+    }
+    stage_barrier<63>();  // phase 0
   }
+  int s = group;
+  for (; s + 3 < nk; s += 2) block(s, std::true_type{});
+  for (; s < nk; s += 2) block(s, std::false_type{});
+  if ((nk & 1) == group) stage_barrier<63>();  // the other group's last phase
 
-  store_wave<T, 4>(a, split, (int64_t)ti * kT + 64 * wm, (int64_t)tj * kT + 64 * wn, lane, acc);
+  // Sums: group 0 keeps a's fragments 0, 1 of the wave tile, group 1 the
+  // others; the rest goes through LDS (8 KB a wave, all DMA and reads are done).
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      red[((wave ^ 4) * 8 + q * 2 + f) * 64 + lane] = group == 0 ? acc[q][2 + f] : acc[q][f];
+  __syncthreads();
+  f32x4 sum[4][2];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      sum[q][f] = (group == 0 ? acc[q][f] : acc[q][2 + f]) + red[(wave * 8 + q * 2 + f) * 64 + lane];
+  store_wave<T, 2, 4>(a, split, ra + 64 * wm + 32 * group, rb + 64 * wn, lane, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -324,13 +388,12 @@ __global__ __launch_bounds__(256, 2) void k_matmul_tile(MatArgs a) {
 //   4s+1  multiply A0        | read B, A0
 //   4s+2  read A1            | multiply A0
 //   4s+3  multiply A1        | read A1
-// A stage is refilled part by part as it falls free, each part at least
-// three phases before block s+2 needs it:
-//   4s+2  group 0: B and b's scales (last read in 4s+1)
-//   4s+3  group 1: A rows 0-191 (group 0's half, last read in 4s+2, and group
-//         1's A0, last read in 4s+1)
-//   4s+4  group 0: A rows 192-255 (group 1's A1, last read in 4s+3) and a's
-//         scales (read with each half): refill_tail
+// A stage is refilled part by part as it falls free, 24 DMA instructions in
+// each of three phases, between the LDS reads, each at least three phases
+// before block s+2 needs it:
+//   4s+2  group 0: B rows 0-159, b's scales (B was last read in 4s+1)
+//   4s+3  group 1: B rows 160-255, A rows 0-95 (group 0's, last read in 4s+2)
+//   4s+4  group 0: A rows 96-255 (group 1's A1 was last read in 4s+3), a's scales
 // and waited for at the end of 4s+7. Every phase ends in a barrier that
 // retires the wave's LDS reads.
 // ---------------------------------------------------------------------------
@@ -338,16 +401,6 @@ constexpr int kB = 256;
 constexpr int kBigOp = kB * kBlock;            // 32 KB
 constexpr int kBigStage = 2 * kBigOp;          // A, then B
 constexpr int kBigScales = 2 * kB * 4;         // a's rows, then b's: 4 k blocks each
-// 32-bit offsets from a tile's first row: 256 rows of less than 2^23 bytes
-constexpr int64_t kBigMaxLd = 1 << 23;
-
-// As dma16 / dma4, the source at a scalar base plus the lane's 32-bit offset.
-__device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
-}
-__device__ __forceinline__ void dma4s(const uint8_t* base, uint32_t off, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
-}
 
 template <typename T, bool WIDE, int G>
 __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint32_t base, const uint8_t* pa,
@@ -369,20 +422,51 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
     const char* q = lds + 2 * kBigStage + (s & 1) * kBigScales;
     return *reinterpret_cast<const int*>(q + (row + r16) * 4) >> (((kb0 + s) & 3) * 8);
   };
-  auto load_a = [&](int s, int half) {
+  // the DMA of this group for block s: `part` 0 in phase 4(s-2)+2 or +3, 1
+  // (group 0) in phase 4(s-2)+4; instruction q of 6
+  auto fetch = [&](int s, int part, int q) {
+    const uint32_t st = base + (s & 1) * kBigStage;
+    const uint32_t sc = base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 256;
+    const int64_t k = (int64_t)(kb0 + s) * kBlock;
+    if (G == 1) {
+      if (q < 3) dma16s(pb + k, off[q], st + kBigOp + (20 + 3 * w4 + q) * 1024);
+      else dma16s(pa + k, off[q], st + (3 * w4 + q - 3) * 1024);
+    } else if (part == 0) {
+      if (q < 5) dma16s(pb + k, off[q], st + kBigOp + (5 * w4 + q) * 1024);
+      else dma4s(scb + ((kb0 + s) & ~3), sob, sc + kB * 4);
+    } else {
+      if (q < 5) dma16s(pa + k, off[5 + q], st + (12 + 5 * w4 + q) * 1024);
+      else dma4s(sca + ((kb0 + s) & ~3), soa, sc);
+    }
+  };
+  constexpr int kOps = 6;  // memory operations of a part
+  auto fetch_all = [&](int s, int part) {
+#pragma unroll
+    for (int q = 0; q < kOps; ++q) fetch(s, part, q);
+  };
+  // reads of block s with the DMA of block t (FETCH) between them
+  auto load_a = [&](int s, int half, auto dma, int t) {
     const char* p = lds + (s & 1) * kBigStage + (128 * G + 64 * half) * kBlock;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(p + 16 * f * kBlock);
       sa[f] = scale(s, 128 * G + 64 * half + 16 * f);
+      if constexpr (decltype(dma)::value) {  // q 0-5 beside four fragments
+        fetch(t, 0, f);
+        if (f >= 2) fetch(t, 0, 2 + f);
+      }
     }
   };
-  auto load_b = [&](int s) {
+  auto load_b = [&](int s, auto dma, int t) {
     const char* p = lds + (s & 1) * kBigStage + kBigOp + 64 * w4 * kBlock;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       fb[f] = frag(p + 16 * f * kBlock);
       sb[f] = scale(s, kB + 64 * w4 + 16 * f);
+      if constexpr (decltype(dma)::value) {
+        fetch(t, 1, f);
+        if (f >= 2) fetch(t, 1, 2 + f);
+      }
     }
   };
   auto mul = [&](int half) {
@@ -409,33 +493,11 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
       }
     }
   };
-  // this group's part of a refill of block s (see the table above)
-  auto refill = [&](int s) {
-    const uint32_t st = base + (s & 1) * kBigStage;
-    const int64_t k = (int64_t)(kb0 + s) * kBlock;
-    if (G == 0) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) dma16s(pb + k, off[q], st + kBigOp + (8 * w4 + q) * 1024);
-      dma4s(scb + ((kb0 + s) & ~3), sob, base + 2 * kBigStage + (s & 1) * kBigScales + kB * 4 + w4 * 256);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 6; ++q) dma16s(pa + k, off[q], st + (6 * w4 + q) * 1024);
-    }
-  };
-  auto refill_tail = [&](int s) {  // group 0
-    const uint32_t st = base + (s & 1) * kBigStage;
-    const int64_t k = (int64_t)(kb0 + s) * kBlock;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) dma16s(pa + k, off[8 + q], st + (24 + 2 * w4 + q) * 1024);
-    dma4s(sca + ((kb0 + s) & ~3), soa, base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 256);
-  };
-  constexpr int kPart = G == 0 ? 9 : 6;  // memory operations of refill()
-
-  refill(0);
-  if (G == 0) refill_tail(0);
+  fetch_all(0, 0);
+  if (G == 0) fetch_all(0, 1);
   if (nk > 1) {
-    refill(1);
-    stage_barrier<kPart>();
+    fetch_all(1, 0);
+    stage_barrier<kOps>();
   } else {
     stage_barrier<0>();
   }
@@ -445,17 +507,16 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
   // later basic blocks, and then keeps two sets of fragments alive.
   auto block = [&](int s, auto left) {
     constexpr int kLeft = decltype(left)::value;
-    load_b(s);
-    load_a(s, 0);
-    if constexpr (G == 0 && kLeft >= 1) refill_tail(s + 1);
+    constexpr std::false_type none{};
+    load_b(s, std::bool_constant<G == 0 && kLeft >= 1>{}, s + 1);
+    load_a(s, 0, none, 0);
     stage_barrier<63>();
     mul(0);
     stage_barrier<63>();
-    load_a(s, 1);
-    if constexpr (kLeft >= 2) refill(s + 2);
+    load_a(s, 1, std::bool_constant<kLeft >= 2>{}, s + 2);
     // the end of phase 4s+3: block s+1 has landed; what was just issued for
     // block s+2 may be in flight
-    constexpr int kLand = kLeft >= 2 ? kPart : 0;
+    constexpr int kLand = kLeft >= 2 ? kOps : 0;
     stage_barrier<(G == 1 ? kLand : 63)>();
     mul(1);
     stage_barrier<(G == 0 ? kLand : 63)>();
@@ -501,9 +562,10 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
   uint32_t off[10];
   if (wave < 4) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) off[q] = off_b(8 * w4 + q);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) off[8 + q] = off_a(24 + 2 * w4 + q);
+    for (int q = 0; q < 5; ++q) {
+      off[q] = off_b(5 * w4 + q);
+      off[5 + q] = off_a(12 + 5 * w4 + q);
+    }
     const int64_t r = min(ra + 64 * w4 + lane, a.m - 1);
     const int64_t c = min(rb + 64 * w4 + b_row<kPair>(lane >> 4, lane & 15), a.n - 1);
     const int64_t a0 = ra >> a.a.sshift, b0 = rb >> a.b.sshift;
@@ -513,10 +575,10 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
                    kb0, nk, wave, lane, acc);
   } else {
 #pragma unroll
-    for (int q = 0; q < 6; ++q) off[q] = off_a(6 * w4 + q);
+    for (int q = 0; q < 6; ++q) off[q] = q < 3 ? off_b(20 + 3 * w4 + q) : off_a(3 * w4 + q - 3);
     big_loop<T, WIDE, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, kb0, nk, wave, lane, acc);
   }
-  store_wave<T, 8>(a, split, ra + 128 * (wave >> 2), rb + 64 * w4, lane, acc);
+  store_wave<T, 8, 4>(a, split, ra + 128 * (wave >> 2), rb + 64 * w4, lane, acc);
 }
 
 // out (+)= the partial sums, split by split in order; 4 columns per thread.
@@ -533,58 +595,190 @@ __global__ __launch_bounds__(256) void k_matmul_join(MatArgs a) {
   put<T, 4>(a, i, j, v);
 }
 
-// ---------------------------------------------------------------------------
-// Few rows of a (m <= 16 NA): one workgroup per 16 columns of out; its waves
-// take the k blocks in turn, straight from global memory (every code of b is
-// read once, by one wave), and join their sums through LDS.
-// ---------------------------------------------------------------------------
-constexpr int kSkinnyWaves = 8;
+constexpr int kWaves = 8;  // of the kernels whose waves share out a tile's k blocks
 
-template <typename T, bool WIDE, int NA>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void k_matmul_skinny(MatArgs a) {
-  __shared__ __attribute__((aligned(16))) f32x4 red[kSkinnyWaves][NA][64];
+// Sums the waves' tiles (acc[q][f] as in store_wave) through LDS, in wave
+// order, and stores the result: wave w's sums in red[w * pitch ..], NA * NB * 64
+// units of 16 bytes.
+template <typename T, int NA, int NB>
+__device__ __forceinline__ void join_waves(const MatArgs& a, int split, int64_t i0, int64_t j0, f32x4* red,
+                                           int pitch, const f32x4 (&acc)[NB][NA]) {
+  constexpr bool kPair = sizeof(T) == 2 && NB >= 2;
+  constexpr int kUnits = NA * NB * 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int64_t j0 = (int64_t)blockIdx.x * 16;
-  auto row_of = [&](const Operand& o, int64_t r, const uint8_t*& codes, const uint8_t*& scales) {
-    r = min(r, o.rows - 1);
-    codes = o.codes + r * o.ld + 16 * g;
-    scales = o.scales + (r >> o.sshift) * o.sld;
-  };
-  const uint8_t *bc, *bs, *ac[NA], *as[NA];
-  row_of(a.b, j0 + r16, bc, bs);
 #pragma unroll
-  for (int f = 0; f < NA; ++f) row_of(a.a, 16 * f + r16, ac[f], as[f]);
+  for (int q = 0; q < NB; ++q)
+#pragma unroll
+    for (int f = 0; f < NA; ++f) red[wave * pitch + (f * NB + q) * 64 + lane] = acc[q][f];
+  __syncthreads();
+  // a thread takes one unit (4 columns of a row), or for 2-byte results two
+  // units of neighbouring fragments (8 columns)
+  constexpr int kStep = kPair ? 2 : 1;
+  for (int e = tid; e < kUnits / kStep; e += 64 * kWaves) {
+    const int l = e & 63, fq = (e >> 6) * kStep, f = fq / NB, q = fq % NB;
+    f32x4 s[kStep];
+#pragma unroll
+    for (int h = 0; h < kStep; ++h) {
+      s[h] = red[(fq + h) * 64 + l];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) s[h] += red[w * pitch + (fq + h) * 64 + l];
+    }
+    const int64_t i = i0 + 16 * f + (l & 15), j = j0 + b_row<kPair>(q, 4 * (l >> 4));
+    if (i >= a.m) continue;
+    if (a.part) {
+      float* p = a.part + ((int64_t)split * a.m + i) * a.pld + j;
+#pragma unroll
+      for (int h = 0; h < kStep; ++h)
+        if (j + 4 * h < a.pld) *reinterpret_cast<f32x4*>(p + 4 * h) = s[h];
+    } else {
+      float v[4 * kStep];
+#pragma unroll
+      for (int h = 0; h < kStep; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[4 * h + c] = s[h][c];
+      put<T, 4 * kStep>(a, i, j, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 16 x 16 tiles: the waves of a workgroup take its k blocks in turn, with
+// fragments read straight from global memory (two sets in registers: the next
+// block's loads run under the current one's MFMA), and join their sums in
+// wave order. Short dependent chains and every code of b read once, for
+// single tokens and other products whose time is latency.
+// ---------------------------------------------------------------------------
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(64 * kWaves) void k_matmul_direct(MatArgs a) {
+  __shared__ __attribute__((aligned(16))) f32x4 red[kWaves * 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4, split = blockIdx.y;
+  int ti, tj;
+  if (!map_tile(a, blockIdx.x, ti, tj)) return;
+  const int64_t i0 = (int64_t)ti * 16, j0 = (int64_t)tj * 16;
+  const int kb0 = split * a.per, kb1 = min(kb0 + a.per, a.nkb);
+  const int64_t ra = min(i0 + r16, a.m - 1), rb = min(j0 + r16, a.n - 1);
+  const uint8_t *ca = a.a.codes + ra * a.a.ld + 16 * g, *cb = a.b.codes + rb * a.b.ld + 16 * g;
+  const uint8_t *sa = a.a.scales + (ra >> a.a.sshift) * a.a.sld, *sb = a.b.scales + (rb >> a.b.sshift) * a.b.sld;
+  struct Set {
+    i32x8 a[1], b[1];
+    int sa[1], sb[1];
+  };
   auto frag = [](const uint8_t* p) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(p), hi = *reinterpret_cast<const i32x4*>(p + 64);
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
-  f32x4 acc[1][NA];
+  auto load = [&](Set& s, int kb) {
+    const int64_t k = (int64_t)kb * kBlock;
+    s.a[0] = frag(ca + k);
+    s.b[0] = frag(cb + k);
+    s.sa[0] = sa[kb];
+    s.sb[0] = sb[kb];
+  };
+  f32x4 acc[1][1] = {{f32x4{}}};
+  int kb = kb0 + wave;
+  Set s0, s1;
+  if (kb < kb1) load(s0, kb);
+  for (; kb + kWaves < kb1; kb += 2 * kWaves) {
+    load(s1, kb + kWaves);
+    mma_block<WIDE, 1, 1>(s0.b, s0.a, s0.sb, s0.sa, acc);
+    if (kb + 2 * kWaves < kb1) load(s0, kb + 2 * kWaves);
+    mma_block<WIDE, 1, 1>(s1.b, s1.a, s1.sb, s1.sa, acc);
+  }
+  if (kb < kb1) mma_block<WIDE, 1, 1>(s0.b, s0.a, s0.sb, s0.sa, acc);
+  join_waves<T, 1, 1>(a, split, i0, j0, red, 64, acc);
+}
+
+// ---------------------------------------------------------------------------
+// 64 x 64 tiles, 8 waves that take the tile's k blocks in turn: for products
+// with too few larger tiles for the chip. Each wave has an LDS stage of its
+// own (64 rows of both operands, 16 KB, and their scales), filled by DMA in
+// whole cache lines; it reads the fragments into registers, sends the DMA of
+// its next block after them and multiplies. Nothing waits for another wave
+// before the sums are joined (in LDS, in wave order). Reading fragments from
+// global memory instead, 64 bytes of a line at a time, took 1.5 times as long.
+// ---------------------------------------------------------------------------
+constexpr int kS = 64;
+constexpr int kSmallOp = kS * kBlock;                       // 8 KB
+constexpr int kSmallStage = 2 * kSmallOp + 2 * kS * 4;      // both operands, then 4 bytes of scales per row
+
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_matmul_small(MatArgs a) {
+  constexpr bool kPair = sizeof(T) == 2;
+  __shared__ __attribute__((aligned(1024))) char lds[kWaves * kSmallStage];
+  static_assert(kSmallStage >= 16 * 64 * 16, "the stage also holds a wave's sums");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4, split = blockIdx.y;
+  int ti, tj;
+  if (!map_tile(a, blockIdx.x, ti, tj)) return;
+  const int64_t i0 = (int64_t)ti * kS, j0 = (int64_t)tj * kS;
+  const int kb0 = split * a.per, kb1 = min(kb0 + a.per, a.nkb);
+  // DMA instruction q: LDS rows 8 q .. +7 (a's 64, then b's), lane l: row
+  // l / 8, position l % 8 (chunks permuted as in the larger tiles). Offsets
+  // from the tile's first rows: 64 rows of at most 2^24 bytes.
+  auto row_a = [&](int r) { return min(i0 + r, a.m - 1) - i0; };
+  auto row_b = [&](int r) { return min(j0 + b_row<kPair>(r >> 4, r & 15), a.n - 1) - j0; };
+  uint32_t off[16];
 #pragma unroll
-  for (int f = 0; f < NA; ++f) acc[0][f] = f32x4{};
-#pragma unroll 2
-  for (int kb = wave; kb < a.nkb; kb += kSkinnyWaves) {
-    i32x8 fb[1] = {frag(bc + (int64_t)kb * kBlock)}, fa[NA];
-    int sb[1] = {bs[kb]}, sa[NA];
+  for (int q = 0; q < 16; ++q) {
+    const int lr = 8 * (q & 7) + (lane >> 3);
+    off[q] = (uint32_t)(q < 8 ? row_a(lr) : row_b(lr)) * (uint32_t)(q < 8 ? a.a.ld : a.b.ld) +
+             (uint32_t)(((lane & 7) ^ (lr & 7)) << 4);
+  }
+  const int64_t as0 = i0 >> a.a.sshift, bs0 = j0 >> a.b.sshift;
+  const uint32_t soa = (uint32_t)(((i0 + row_a(lane)) >> a.a.sshift) - as0) * (uint32_t)a.a.sld;
+  const uint32_t sob = (uint32_t)(((j0 + row_b(lane)) >> a.b.sshift) - bs0) * (uint32_t)a.b.sld;
+  const uint8_t *pa = a.a.codes + i0 * a.a.ld, *pb = a.b.codes + j0 * a.b.ld;
+  const uint8_t *sa = a.a.scales + as0 * a.a.sld, *sb = a.b.scales + bs0 * a.b.sld;
+  char* st = lds + wave * kSmallStage;
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds + wave * kSmallStage;
+  auto fetch = [&](int kb) {
+    const int64_t k = (int64_t)kb * kBlock;
 #pragma unroll
-    for (int f = 0; f < NA; ++f) {
-      fa[f] = frag(ac[f] + (int64_t)kb * kBlock);
-      sa[f] = as[f][kb];
+    for (int q = 0; q < 16; ++q) dma16s((q < 8 ? pa : pb) + k, off[q], base + q * 1024);
+    dma4s(sa + (kb & ~3), soa, base + 2 * kSmallOp);
+    dma4s(sb + (kb & ~3), sob, base + 2 * kSmallOp + kS * 4);
+  };
+  const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[q][f] = f32x4{};
+  int kb = kb0 + wave;
+  if (kb < kb1) fetch(kb);
+  for (; kb < kb1; kb += kWaves) {
+    // this wave's block has landed (memory operations retire in order, and it
+    // has no others); the empty asm keeps the reads below the wait
+    __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xF << 8));  // vmcnt(0)
+    asm volatile("" ::: "memory");
+    i32x8 fa[4], fb[4];
+    int ea[4], eb[4];
+    auto frag = [&](const char* p) {
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(p + foff);
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (foff ^ 64));
+      return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    const char* ss = st + 2 * kSmallOp;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      fa[f] = frag(st + 16 * f * kBlock);
+      fb[f] = frag(st + kSmallOp + 16 * f * kBlock);
+      ea[f] = *reinterpret_cast<const int*>(ss + (16 * f + r16) * 4) >> ((kb & 3) * 8);
+      eb[f] = *reinterpret_cast<const int*>(ss + (kS + 16 * f + r16) * 4) >> ((kb & 3) * 8);
     }
-    mma_block<WIDE, 1, NA>(fb, fa, sb, sa, acc);
+    if (kb + kWaves < kb1) {
+      // the reads have retired before the stage is refilled
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4) | (0 << 8));  // lgkmcnt(0)
+      asm volatile("" ::: "memory");
+      fetch(kb + kWaves);
+    }
+    mma_block<WIDE, 4, 4>(fb, fa, eb, ea, acc);
   }
-#pragma unroll
-  for (int f = 0; f < NA; ++f) red[wave][f][lane] = acc[0][f];
-  __syncthreads();
-  for (int e = tid; e < NA * 64; e += 64 * kSkinnyWaves) {
-    const int f = e >> 6, l = e & 63;
-    f32x4 s = red[0][f][l];
-#pragma unroll
-    for (int w = 1; w < kSkinnyWaves; ++w) s += red[w][f][l];
-    const int64_t i = 16 * f + (l & 15);
-    const float v[4] = {s[0], s[1], s[2], s[3]};
-    if (i < a.m) put<T, 4>(a, i, j0 + 4 * (l >> 4), v);
-  }
+  join_waves<T, 4, 4>(a, split, i0, j0, reinterpret_cast<f32x4*>(lds), kSmallStage / 16, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -593,56 +787,80 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_matmul_skinny(MatArgs a) 
 constexpr int64_t kCUs = 256;
 constexpr int64_t kMaxTiles = (1 << 22) - 1;
 
-enum Kind { kSkinny = 0, kTile = 1, kBig = 2 };
+enum Kind { kDirect, kSmall, kTile, kBig };
 struct Choice {
   Kind kind;
+  int edge;  // of a tile
   int splits, per;
   size_t ws_bytes;
 };
 
+// Estimated time in us of a kernel on `tiles` tiles of nkb blocks: a launch,
+// then rounds of one tile per CU, each a fixed part (first loads, last stores)
+// and a part per block, which is less where a round leaves CUs idle (power,
+// cache bandwidth). Fitted to times of 30 products from 512 x 2048 x 2048 to
+// 8192^3, which it meets within about 15 %.
+struct Cost {
+  double fixed, block;
+};
+double estimate(const Cost& c, int64_t tiles, double nkb) {
+  const int64_t part = tiles % kCUs;
+  double t = 1.5 + (double)(tiles / kCUs) * (c.fixed + c.block * nkb);
+  if (part) t += c.fixed + c.block * nkb * (0.75 + 0.25 * (double)part / (double)kCUs);
+  return t;
+}
+
+// The kernel for a product: the cheapest by the estimate. Examples (measured
+// us, 8-bit path, tiles of 16, 64, 128, 256): 1x6144x2048: 5.4, 6.6, -, 21;
+// 512x2048x2048: 39, 7.7, 11, 24; 1024x4096x4096: -, 37, 21, 43;
+// 6144x2048x8192: -, 192, 112, 90.
 Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
-  Choice c{kTile, 1, (int)ceil_div(k, kBlock), 0};
   const int64_t nkb = ceil_div(k, kBlock);
-  if (m <= 64) {
-    c.kind = kSkinny;
-    return c;
-  }
-  if (k > 0 && code_ld(k) < kBigMaxLd &&
-      ceil_div(m, kB) * ceil_div(n, kB) >= kCUs / 2) {
-    c.kind = kBig;
-    return c;
-  }
-  // Two workgroups fit a CU. Fewer tiles than that leave CUs idle: the k
-  // blocks are split over up to 16 workgroups per tile, 4 blocks each at least.
-  const int64_t tiles = ceil_div(m, kT) * ceil_div(n, kT);
-  int64_t s = std::min<int64_t>({2 * kCUs / std::max<int64_t>(tiles, 1), nkb / 4, 16});
-  if (s > 1) {
+  auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };
+  Choice c{kSmall, kS, 1, (int)nkb, 0};
+  if (m == 0 || n == 0) return c;
+  const bool wide = out_dtype == MUONH_DT_FP32;
+  const Cost small = wide ? Cost{2.5, 0.29} : Cost{2.3, 0.24};
+  double best = 0;
+  // 64 x 64, the k blocks split over up to 16 workgroups where tiles are few:
+  // a second launch joins the partial sums
+  for (int s = 1; s <= 16 && (s == 1 || (s * tiles(kS) <= kCUs && nkb >= 8 * s)); s *= 2) {
+    const double t = estimate(small, s * tiles(kS), (double)nkb / s) + (s > 1 ? 2.5 + 2e-6 * s * m * n : 0.0);
+    if (s > 1 && t >= best) continue;
+    best = t;
     c.per = (int)ceil_div(nkb, s);
-    c.splits = (int)ceil_div(nkb, c.per);
-    c.ws_bytes = (size_t)c.splits * m * (ceil_div(n, 4) * 4) * sizeof(float);
+    c.splits = s == 1 ? 1 : (int)ceil_div(nkb, c.per);
   }
+  // 16 x 16 tiles, all at once: a floor of latency per block, then the rate
+  // at which the caches deliver both operands' rows
+  const double t16 = 2.8 + (double)nkb * std::max(0.08, 5e-4 * (double)tiles(16));
+  if (t16 < best) {
+    best = t16;
+    c = Choice{kDirect, 16, 1, (int)nkb, 0};
+  }
+  if (code_ld(k) < kMaxTileLd) {
+    const Cost tile = wide ? Cost{4.0, 0.85} : Cost{3.0, 0.51}, big = wide ? Cost{8.0, 2.75} : Cost{7.0, 1.43};
+    for (const Kind kind : {kTile, kBig}) {
+      const double t = kind == kTile ? estimate(tile, tiles(kT), (double)nkb) : estimate(big, tiles(kB), (double)nkb);
+      if (t >= best) continue;
+      best = t;
+      c = Choice{kind, kind == kTile ? kT : kB, 1, (int)nkb, 0};
+    }
+  }
+  if (c.splits > 1) c.ws_bytes = (size_t)c.splits * m * (ceil_div(n, 4) * 4) * sizeof(float);
   return c;
 }
 
 template <typename T, bool WIDE>
 int launch(const MatArgs& a, const Choice& c, hipStream_t s) {
-  if (c.kind == kSkinny) {
-    const dim3 grid((unsigned)ceil_div(a.n, 16)), thr(64 * kSkinnyWaves);
-    if (a.m <= 16)
-      hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 1>), grid, thr, 0, s, a);
-    else if (a.m <= 32)
-      hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 2>), grid, thr, 0, s, a);
-    else
-      hipLaunchKernelGGL((k_matmul_skinny<T, WIDE, 4>), grid, thr, 0, s, a);
-  } else if (c.kind == kBig) {
-    hipLaunchKernelGGL((k_matmul_big<T, WIDE>), dim3((unsigned)map_grid((int64_t)a.tm * a.tn)), dim3(512), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((k_matmul_tile<T, WIDE>),
-                       dim3((unsigned)map_grid((int64_t)a.tm * a.tn), (unsigned)a.splits), dim3(256), 0, s, a);
-    if (a.part)
-      hipLaunchKernelGGL((k_matmul_join<T>), dim3((unsigned)ceil_div(a.m * (a.pld >> 2), 256)),
-                         dim3(256), 0, s, a);
-  }
+  const dim3 grid((unsigned)map_grid((int64_t)a.tm * a.tn), (unsigned)a.splits), direct(64 * kWaves);
+  if (c.kind == kBig) hipLaunchKernelGGL((k_matmul_big<T, WIDE>), grid, dim3(512), 0, s, a);
+  else if (c.kind == kTile) hipLaunchKernelGGL((k_matmul_tile<T, WIDE>), grid, dim3(512), 0, s, a);
+  else if (c.kind == kSmall) hipLaunchKernelGGL((k_matmul_small<T, WIDE>), grid, direct, 0, s, a);
+  else hipLaunchKernelGGL((k_matmul_direct<T, WIDE>), grid, direct, 0, s, a);
+  if (a.part)
+    hipLaunchKernelGGL((k_matmul_join<T>), dim3((unsigned)ceil_div(a.m * (a.pld >> 2), 256)), dim3(256),
+                       0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(MUONH_EHIP, "fp8 matmul: %s (%d)", hipGetErrorString(e), (int)e);
   return MUONH_OK;
@@ -728,14 +946,12 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   x.out = out;
   x.ldo = out_ld;
   x.accumulate = accumulate != 0;
-  x.vec = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(out_ld * esize)) & 15u) == 0;
   x.splits = c.splits;
   x.per = c.per;
   x.pld = ceil_div(n, 4) * 4;
   x.part = c.ws_bytes ? static_cast<float*>(workspace) : nullptr;
-  const int edge = c.kind == kBig ? kB : kT;
-  x.tm = (int)ceil_div(m, edge);
-  x.tn = (int)ceil_div(n, edge);
+  x.tm = (int)ceil_div(m, c.edge);
+  x.tn = (int)ceil_div(n, c.edge);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return out_dtype == MUONH_DT_BF16 ? launch<__bf16, false>(x, c, s) : launch<float, true>(x, c, s);
 }

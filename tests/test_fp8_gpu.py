@@ -246,7 +246,8 @@ def test_product_of_empty_operands(dtype):
 @pytest.mark.parametrize("m,k", [(5, 300), (140, 300), (140, 5000)])
 def test_nan_and_overflow_stay_in_their_rows(m, k, dtype):
     n = 150
-    x, w = torch.randn(m, k, device="cuda"), torch.randn(n, k, device="cuda")
+    g = torch.Generator("cuda").manual_seed(4)
+    x, w = torch.randn(m, k, device="cuda", generator=g), torch.randn(n, k, device="cuda", generator=g)
     x[2, 7] = float("nan")
     x[3, 290] = float("inf")
     w[9, 150] = -float("inf")
@@ -255,14 +256,19 @@ def test_nan_and_overflow_stay_in_their_rows(m, k, dtype):
     a, b = mh().fp8_quantize(x)[0], mh().fp8_quantize(w)[0]
     out = mh().fp8_matmul(a, b, out_dtype=DT[dtype]).double().cpu().numpy()
     with np.errstate(over="ignore", invalid="ignore"):
-        v = fo.values(*host(a), (m, k)) @ fo.values(*host(b), (n, k)).T
+        va, vb = fo.values(*host(a), (m, k)), fo.values(*host(b), (n, k))
+        v, p = va @ vb.T, np.abs(va) @ np.abs(vb).T
     # [4, 11]: products of both signs near 2^240, so partial sums in fp32 are
     # +inf and -inf, whose sum is NaN: not finite is all that fp32 sums promise
     rest = np.ones((m, n), bool)
     rest[4, 11] = False
     assert not np.isfinite(out[4, 11])
     assert np.array_equal(np.isnan(out)[rest], np.isnan(v)[rest])
-    assert np.isfinite(out[rest & ~np.isnan(v)]).all()
+    # where all magnitudes together stay below 2^127, no partial sum overflows
+    # (2^120 times 5000 normal products does not: such results may be infinite)
+    with np.errstate(invalid="ignore"):
+        assert np.isfinite(out[rest & (p < 2.0 ** 127)]).all()
+    assert (rest & (p < 2.0 ** 127)).sum() > (m - 4) * (n - 2) // 2
 
 
 def test_product_of_long_rows_and_far_offsets():
