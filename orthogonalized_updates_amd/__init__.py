@@ -26,6 +26,7 @@ step(..., fp8=set) leaves the updated weights quantized for them.
 from __future__ import annotations
 
 import ctypes
+import functools
 import re
 from collections import OrderedDict
 from pathlib import Path
@@ -569,6 +570,7 @@ def _up(v: int, m: int) -> int:
     return -(-v // m) * m
 
 
+@functools.lru_cache(maxsize=1024)
 def _fp8_layout(rows: int, cols: int, block: str):
     """(codes shape, scales shape) of a rows x cols matrix."""
     if block not in FP8_BLOCKS:
@@ -577,6 +579,13 @@ def _fp8_layout(rows: int, cols: int, block: str):
         raise ValueError(f"shape {(rows, cols)} out of [0, {MUONH_MAX_FP8_DIM}]")
     srows = rows if block == "rows" else -(-rows // FP8_BLOCK)
     return (rows, _up(cols, FP8_BLOCK)), (srows, _up(-(-cols // FP8_BLOCK), 4))
+
+
+def _check_part(name: str, t, dtype, shape) -> None:
+    if getattr(t, "dtype", None) != dtype:
+        raise TypeError(f"{name} must be a {dtype} torch tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {shape} tensor")
 
 
 class Fp8Matrix:
@@ -594,13 +603,9 @@ class Fp8Matrix:
     def __init__(self, codes, scales, shape: Tuple[int, int], block: str = "rows"):
         import torch
         rows, cols = int(shape[0]), int(shape[1])
-        for name, t, dt, want in zip(("codes", "scales"), (codes, scales),
-                                     (torch.float8_e4m3fn, torch.float8_e8m0fnu),
-                                     _fp8_layout(rows, cols, block)):
-            if not isinstance(t, torch.Tensor) or t.dtype != dt:
-                raise TypeError(f"{name} must be a {dt} torch tensor")
-            if tuple(t.shape) != want or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {want} tensor")
+        c, e = _fp8_layout(rows, cols, block)
+        _check_part("codes", codes, torch.float8_e4m3fn, c)
+        _check_part("scales", scales, torch.float8_e8m0fnu, e)
         if codes.device != scales.device or codes.device.type != "cuda":
             raise ValueError("codes and scales must be on one ROCm GPU")
         self.codes, self.scales, self.shape, self.block = codes, scales, (rows, cols), block
@@ -612,7 +617,7 @@ class Fp8Matrix:
         """Storage with undefined contents."""
         import torch
         c, s = _fp8_layout(rows, cols, block)
-        dev = torch.device("cuda" if device is None else device)
+        dev = device if isinstance(device, torch.device) else torch.device(device or "cuda")
         if dev.type != "cuda":
             raise ValueError("codes and scales must be on one ROCm GPU")
         # made in its layout, so without __init__'s checks
@@ -719,23 +724,30 @@ def fp8_quantize(x, block: str = "rows", forms: str = "plain",
         raise ValueError(f"forms must be one of {FP8_FORMS}, got {forms!r}")
     rows, cols = x.shape
     ld = _row_pitch(x, "x")
-    got = []
-    for name, o, want, shape in (("out", out, forms != "transposed", (rows, cols)),
-                                 ("out_t", out_t, forms != "plain", (cols, rows))):
-        if not want:
-            if o is not None:
-                raise ValueError(f"{name} given, but forms={forms!r}")
-        elif o is None:
-            o = Fp8Matrix.empty(*shape, block, dev)
-        elif not isinstance(o, Fp8Matrix):
-            raise TypeError(f"{name} must be an Fp8Matrix")
-        elif o.shape != shape or o.block != block or o.device != dev:
-            raise ValueError(f"{name} must be a {shape} Fp8Matrix of block {block!r} on {dev}")
-        got.append(o)
-    ptr = [v for o in got for v in ((o.desc.codes, o.desc.scales) if o is not None else (None, None))]
+    q = _form("out", out, forms != "transposed", rows, cols, block, dev)
+    qt = _form("out_t", out_t, forms != "plain", cols, rows, block, dev)
+    d, t = _NO_FORM if q is None else q.desc, _NO_FORM if qt is None else qt.desc
     _on_device(torch, dev, get_lib().muonh_fp8_quantize, x.data_ptr(), dt, rows, cols, ld,
-               FP8_BLOCKS[block], *ptr)
-    return tuple(got)
+               FP8_BLOCKS[block], d.codes, d.scales, t.codes, t.scales)
+    return q, qt
+
+
+_NO_FORM = Fp8Desc(None, None, 0, 0, 0)
+
+
+def _form(name: str, o, wanted: bool, rows: int, cols: int, block: str, dev):
+    """The output for one form of fp8_quantize: `o` checked, a new one, or None."""
+    if not wanted:
+        if o is not None:
+            raise ValueError(f"{name} given for a form that was not asked for")
+        return None
+    if o is None:
+        return Fp8Matrix.empty(rows, cols, block, dev)
+    if not isinstance(o, Fp8Matrix):
+        raise TypeError(f"{name} must be an Fp8Matrix")
+    if o.shape != (rows, cols) or o.block != block or o.device != dev:
+        raise ValueError(f"{name} must be a {(rows, cols)} Fp8Matrix of block {block!r} on {dev}")
+    return o
 
 
 def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate: bool = False):
