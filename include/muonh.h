@@ -345,7 +345,8 @@ int muonh_check_disjoint(const muonh_plan* plan, const void* const* W, const voi
  * past cols; scales, row-major, one row per matrix row (ROWS) or per 128
  * matrix rows (TILES), muonh_fp8_scale_ld(cols) = ceil(cols/128) rounded up
  * to a multiple of 4 bytes per row, zeros past ceil(cols/128). codes 16-byte,
- * scales 4-byte aligned. Matrices without rows or columns are allowed.
+ * scales 4-byte aligned. The quantizing calls write all of it; an operand
+ * of muonh_fp8_matmul from elsewhere needs the zeros and scale bytes in [1, 254]. Matrices without rows or columns are allowed.
  */
 enum { MUONH_FP8_ROWS = 0, MUONH_FP8_TILES = 1 };
 enum { MUONH_DT_FP32 = 0, MUONH_DT_BF16 = 1 };
@@ -421,7 +422,7 @@ int muonh_fp8_weights(const muonh_plan* plan, const float* const* W, void* const
  * need workspaces of their own. Asynchronous on `stream`, capturable.
  * Errors: MUONH_EINVAL (NULL argument, bad block or dtype, misaligned codes or
  * scales, out_ld < n), MUONH_ESHAPE (a dim out of range, a and b of different
- * cols, or 2^22 output tiles of 128 x 128 or more), MUONH_EWORKSPACE, MUONH_EALIAS (out or
+ * cols, or 2^21 output tiles of 128 x 128 or more), MUONH_EWORKSPACE, MUONH_EALIAS (out or
  * the workspace overlaps an operand or each other), MUONH_EHIP.
  */
 size_t muonh_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t out_dtype);

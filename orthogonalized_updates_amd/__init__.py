@@ -444,7 +444,7 @@ class MuonH:
         .weights[i] is matrix i as the forward product reads it,
         .transposed[i] its transpose (for the data gradient). Contents are
         undefined until a quantize_weights() or a step(..., fp8=set)."""
-        return Fp8Weights(self.shapes, self.device, transposed)
+        return Fp8Weights(self.shapes, self.device, transposed, self.plan_order)
 
     def quantize_weights(self, weights, out: "Fp8Weights") -> "Fp8Weights":
         """Quantize the weights into `out` (a set from fp8_weights()), in
@@ -457,7 +457,7 @@ class MuonH:
     def _check_fp8(self, out, *lists) -> None:
         if not isinstance(out, Fp8Weights):
             raise TypeError("expected an Fp8Weights set (see fp8_weights())")
-        if out.shapes != self.shapes or out.device != self.device:
+        if out.shapes != self.shapes or out.device != self.device or out.order != self.plan_order:
             raise ValueError("the Fp8Weights set has other shapes or another device")
         lo, hi = out.span
         for ts in lists:
@@ -467,11 +467,8 @@ class MuonH:
                     raise MuonHAliasError("a tensor of the call overlaps the Fp8Weights set")
 
     def _quantize(self, weights, out) -> None:
-        arrs = [self._ptr_array("W", weights)]
-        for ms in (out.weights, out.transposed):
-            for field in ("codes", "scales"):
-                arrs.append(self._ptr_array(field, [getattr(m, field) for m in ms]) if ms else None)
-        check(get_lib().muonh_fp8_weights(self.plan.handle, *arrs, self._stream()))
+        _on_device(self.torch, self.device, get_lib().muonh_fp8_weights, self.plan.handle,
+                   self._ptr_array("W", weights), *out.arrays)
 
     def read_update(self, index: int):
         """The update O of matrix `index` from the last step (fp32, rows x cols)."""
@@ -640,12 +637,15 @@ class Fp8Matrix:
 class Fp8Weights:
     """The weights of a MuonH optimizer in 8 bits (MuonH.fp8_weights): lists
     of Fp8Matrix with block "tiles" in the caller's order, `weights` and
-    `transposed` (empty without transposed forms), in one allocation."""
+    `transposed` (empty without transposed forms), in one allocation. The set
+    keeps the device pointer arrays of its parts (`order`: matrices in plan
+    order), so a captured graph that writes it needs nothing else alive."""
 
-    def __init__(self, shapes, device, transposed: bool = True):
+    def __init__(self, shapes, device, transposed: bool, order: Sequence[int]):
         import torch
         self.shapes = list(shapes)
         self.device = device
+        self.order = list(order)
         self.weights: List[Fp8Matrix] = []
         self.transposed: List[Fp8Matrix] = []
         places, total = [], 0
@@ -663,6 +663,11 @@ class Fp8Weights:
             parts = [self.storage[o:o + h * w].view(dt).view(h, w)
                      for (o, h, w), dt in zip(at, (torch.float8_e4m3fn, torch.float8_e8m0fnu))]
             to.append(Fp8Matrix(*parts, shape, "tiles"))
+        self._ptrs = [torch.tensor([getattr(ms[i], part).data_ptr() for i in self.order],
+                                   dtype=torch.int64, device=device) if ms else None
+                      for ms in (self.weights, self.transposed) for part in ("codes", "scales")]
+        # codes, scales, codes_t, scales_t of muonh_fp8_weights
+        self.arrays = [None if t is None else t.data_ptr() for t in self._ptrs]
 
     @property
     def span(self) -> Tuple[int, int]:

@@ -785,7 +785,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul_small(MatArgs a) {
 // host side
 // ---------------------------------------------------------------------------
 constexpr int64_t kCUs = 256;
-constexpr int64_t kMaxTiles = (1 << 22) - 1;
+// Output tiles of 128 x 128: a launch has fewer than 2^32 threads, and of 64 x 64
+// tiles, which have as many threads each, there are at most 4 times as many.
+constexpr int64_t kMaxTiles = (1 << 21) - 8;
 
 enum Kind { kDirect, kSmall, kTile, kBig };
 struct Choice {
@@ -819,6 +821,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
   auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };
   Choice c{kSmall, kS, 1, (int)nkb, 0};
   if (m == 0 || n == 0) return c;
+  if (nkb == 0) return Choice{kTile, kT, 1, 0, 0};  // zeros; that kernel's loop may be empty
   const bool wide = out_dtype == MUONH_DT_FP32;
   const Cost small = wide ? Cost{2.5, 0.29} : Cost{2.3, 0.24};
   double best = 0;
@@ -917,7 +920,7 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   if (reinterpret_cast<uintptr_t>(out) & (uintptr_t)(esize - 1))
     return fail(MUONH_EINVAL, "out is not aligned to its type");
   if (ceil_div(m, kT) * ceil_div(n, kT) > kMaxTiles)
-    return fail(MUONH_ESHAPE, "2^22 output tiles of 128 x 128 or more");
+    return fail(MUONH_ESHAPE, "2^21 output tiles of 128 x 128 or more");
   const Choice c = choose(m, n, k, out_dtype);
   if (c.ws_bytes) {
     if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the product needs %zu bytes", c.ws_bytes);

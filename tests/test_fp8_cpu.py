@@ -161,7 +161,7 @@ def _matmul(a=None, b=None, out=5 * A, dt=1, ld=None, acc=0, ws=None, nbytes=0):
     (dict(out=None), mh.MUONH_EINVAL),
     (dict(out=5 * A + 1), mh.MUONH_EINVAL),
     (dict(out=5 * A + 2, dt=0), mh.MUONH_EINVAL),
-    (dict(a=_desc(rows=1 << 24), b=_desc(rows=1 << 12), out=9 * A), mh.MUONH_ESHAPE),
+    (dict(a=_desc(rows=1 << 24), b=_desc(rows=1 << 11), out=9 * A), mh.MUONH_ESHAPE),
     (dict(out=A), mh.MUONH_EALIAS),                               # a's codes
     (dict(out=3 * A + 299 * 256), mh.MUONH_EALIAS),               # b's last row
     (dict(out=2 * A - 100 * 300 * 2 + 2), mh.MUONH_EALIAS),       # ends inside a's scales
