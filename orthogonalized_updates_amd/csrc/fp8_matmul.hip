@@ -596,6 +596,7 @@ __global__ __launch_bounds__(256) void k_matmul_join(MatArgs a) {
 }
 
 constexpr int kWaves = 8;  // of the kernels whose waves share out a tile's k blocks
+static_assert(kWaves == 8, "k_matmul_small deals eighths");
 
 // Sums the waves' tiles (acc[q][f] as in store_wave) through LDS, in wave
 // order, and stores the result: wave w's sums in red[w * pitch ..], NA * NB * 64
@@ -691,7 +692,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_matmul_direct(MatArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// 64 x 64 tiles, 8 waves that take the tile's k blocks in turn: for products
+// 64 x 64 tiles, 8 waves that share out the tile's k blocks: for products
 // with too few larger tiles for the chip. Each wave has an LDS stage of its
 // own (64 rows of both operands, 16 KB, and their scales), filled by DMA in
 // whole cache lines; it reads the fragments into registers, sends the DMA of
@@ -734,12 +735,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul_small(MatArgs a) {
   const uint8_t *sa = a.a.scales + as0 * a.a.sld, *sb = a.b.scales + bs0 * a.b.sld;
   char* st = lds + wave * kSmallStage;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds + wave * kSmallStage;
-  auto fetch = [&](int kb) {
+  auto fetch = [&](int kb, bool first) {
     const int64_t k = (int64_t)kb * kBlock;
 #pragma unroll
     for (int q = 0; q < 16; ++q) dma16s((q < 8 ? pa : pb) + k, off[q], base + q * 1024);
-    dma4s(sa + (kb & ~3), soa, base + 2 * kSmallOp);
-    dma4s(sb + (kb & ~3), sob, base + 2 * kSmallOp + kS * 4);
+    if (first || (kb & 3) == 0) {
+      dma4s(sa + (kb & ~3), soa, base + 2 * kSmallOp);
+      dma4s(sb + (kb & ~3), sob, base + 2 * kSmallOp + kS * 4);
+    }
   };
   const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);
   f32x4 acc[4][4];
@@ -747,9 +750,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul_small(MatArgs a) {
   for (int q = 0; q < 4; ++q)
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[q][f] = f32x4{};
-  int kb = kb0 + wave;
-  if (kb < kb1) fetch(kb);
-  for (; kb < kb1; kb += kWaves) {
+  // An eighth of the blocks for each wave, consecutive ones: a fetch of scales
+  // serves up to 4 of them (64 rows are 64 cache lines, a quarter of a
+  // block's). Waves w and w + 4, which share a SIMD, take neighbouring
+  // eighths, so that the SIMDs' shares differ by one block at most.
+  const int order = 2 * (wave & 3) + (wave >> 2), nk = max(kb1 - kb0, 0);
+  int kb = kb0 + (int)((int64_t)order * nk >> 3);
+  const int end = kb0 + (int)((int64_t)(order + 1) * nk >> 3);
+  if (kb < end) fetch(kb, true);
+  for (; kb < end; ++kb) {
     // this wave's block has landed (memory operations retire in order, and it
     // has no others); the empty asm keeps the reads below the wait
     __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xF << 8));  // vmcnt(0)
@@ -769,12 +778,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul_small(MatArgs a) {
       ea[f] = *reinterpret_cast<const int*>(ss + (16 * f + r16) * 4) >> ((kb & 3) * 8);
       eb[f] = *reinterpret_cast<const int*>(ss + (kS + 16 * f + r16) * 4) >> ((kb & 3) * 8);
     }
-    if (kb + kWaves < kb1) {
+    if (kb + 1 < end) {
       // the reads have retired before the stage is refilled
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4) | (0 << 8));  // lgkmcnt(0)
       asm volatile("" ::: "memory");
-      fetch(kb + kWaves);
+      fetch(kb + 1, false);
     }
     mma_block<WIDE, 4, 4>(fb, fa, eb, ea, acc);
   }
@@ -823,7 +832,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
   if (m == 0 || n == 0) return c;
   if (nkb == 0) return Choice{kTile, kT, 1, 0, 0};  // zeros; that kernel's loop may be empty
   const bool wide = out_dtype == MUONH_DT_FP32;
-  const Cost small = wide ? Cost{2.5, 0.29} : Cost{2.3, 0.24};
+  const Cost small = wide ? Cost{3.2, 0.25} : Cost{2.8, 0.205};
   double best = 0;
   // 64 x 64, the k blocks split over up to 16 workgroups where tiles are few:
   // a second launch joins the partial sums
