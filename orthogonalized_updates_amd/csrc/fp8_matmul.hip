@@ -28,6 +28,7 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -48,6 +49,7 @@ struct MatArgs {
   void* out;
   int64_t ldo;
   int accumulate;
+  int odd;           // 2-byte results: some rows of out start off a multiple of 4 bytes
   float* part;       // partial sums [split][m][pld], or nullptr
   int64_t pld;
   int splits, per;   // k blocks per split
@@ -134,6 +136,40 @@ __device__ __forceinline__ int b_row(int f, int r) {
   return PAIR ? 32 * (f >> 1) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3) : 16 * f + r;
 }
 
+// One row's 16 + 16 bytes of 2-byte results of a lane (columns 8 g .. +7 and
+// 32 + 8 g .. +7 from p's 64; the 4 lanes l%16, g = l/16, hold the row) to an
+// address that is 2 bytes off a multiple of 4 where `off`: vector stores to
+// such addresses run at a third of the rate, so those rows are stored one
+// element on, each lane taking the first element of its right neighbour, the
+// first and the last element of the 64 by themselves.
+__device__ __forceinline__ void put_odd(__bf16* p, u32x4 x, u32x4 y, int lane, bool off, bool live) {
+  const int g = lane >> 4, next = ((lane + 16) & 63) << 2;
+  const uint32_t nx = (uint32_t)__builtin_amdgcn_ds_bpermute(next, (int)x[0]);
+  const uint32_t ny = (uint32_t)__builtin_amdgcn_ds_bpermute(next, (int)y[0]);
+  if (!live) return;
+  typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+  typedef uint32_t u32x3_a2 __attribute__((ext_vector_type(3), aligned(2)));
+  uint16_t* q = reinterpret_cast<uint16_t*>(p) + 8 * g;
+  if (!off) {
+    *reinterpret_cast<u32x4_a2*>(q) = x;
+    *reinterpret_cast<u32x4_a2*>(q + 32) = y;
+    return;
+  }
+  auto shift = [](const u32x4& v, uint32_t n) {
+    return u32x4{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16),
+                 (v[3] >> 16) | (n << 16)};
+  };
+  if (g == 0) *q = (uint16_t)x[0];
+  *reinterpret_cast<u32x4_a2*>(q + 1) = shift(x, g == 3 ? ny : nx);
+  const u32x4 z = shift(y, ny);
+  if (g < 3) {
+    *reinterpret_cast<u32x4_a2*>(q + 33) = z;
+  } else {
+    *reinterpret_cast<u32x3_a2*>(q + 33) = u32x3_a2{z[0], z[1], z[2]};
+    q[39] = (uint16_t)(y[3] >> 16);
+  }
+}
+
 // Stores a wave's 16 NA rows x 16 NB columns from row i0, column j0: acc[q][f],
 // b's fragment q, a's fragment f; lane l holds row 16 f + l%16 and columns
 // b_row(q, 4 (l/16) ..+3).
@@ -142,6 +178,25 @@ __device__ __forceinline__ void store_wave(const MatArgs& a, int split, int64_t 
                                            const f32x4 (&acc)[NB][NA]) {
   constexpr bool kPair = sizeof(T) == 2;
   const int r16 = lane & 15, g = lane >> 4;
+  if constexpr (kPair && NB == 4) {
+    if (a.odd && !a.part && !a.accumulate && j0 + 64 <= a.n) {
+#pragma unroll
+      for (int f = 0; f < NA; ++f) {
+        u32x4 w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 u = acc[2 * h][f], v = acc[2 * h + 1][f];
+          const bf16x8 c = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
+                            (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+          w[h] = __builtin_bit_cast(u32x4, c);
+        }
+        const int64_t i = i0 + 16 * f + r16;
+        __bf16* p = static_cast<__bf16*>(a.out) + i * a.ldo + j0;
+        put_odd(p, w[0], w[1], lane, (reinterpret_cast<uintptr_t>(p) & 2) != 0, i < a.m);
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int f = 0; f < NA; ++f) {
     const int64_t i = i0 + 16 * f + r16;
@@ -958,6 +1013,7 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   x.out = out;
   x.ldo = out_ld;
   x.accumulate = accumulate != 0;
+  x.odd = out_dtype == MUONH_DT_BF16 && ((reinterpret_cast<uintptr_t>(out) & 2) != 0 || (out_ld & 1) != 0);
   x.splits = c.splits;
   x.per = c.per;
   x.pld = ceil_div(n, 4) * 4;
