@@ -17,6 +17,7 @@
 // use v_mfma_f32_16x16x32_bf16, whose sums are accurate to fp32 (measured 1e-7
 // at k = 8192), at half the matrix rate.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fp8_internal.h"
@@ -431,7 +432,11 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
 
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles, 8 waves (2 x 4, wave tile 128 x 64), two LDS stages of one
-// k block (2 x 64 KB): 8-bit products with enough tiles for the chip.
+// k block (2 x 64 KB): products with enough tiles for the chip. 192 x 256
+// tiles (FA = 3 instead of 4 fragments of a per half wave tile) where they
+// fill the chip better: 6144 x 2048 x 8192, 192 tiles or 256 for 256 CUs, takes
+// 139 instead of 154 us with fp32 and 78 instead of 80.5 with bf16 results
+// (fewer active CUs clock higher). 256 x 192 tiles gained 3-7 % there.
 //
 // The waves form two groups of 4, one wave of each per SIMD, that take turns
 // phase by phase: one group's 16 MFMAs run while the other reads LDS and
@@ -449,6 +454,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
 //   4s+2  group 0: B rows 0-159, b's scales (B was last read in 4s+1)
 //   4s+3  group 1: B rows 160-255, A rows 0-95 (group 0's, last read in 4s+2)
 //   4s+4  group 0: A rows 96-255 (group 1's A1 was last read in 4s+3), a's scales
+// (rows 96-191 of 192; group 0 reads the first half of A's rows, group 1 the other)
 // and waited for at the end of 4s+7. Every phase ends in a barrier that
 // retires the wave's LDS reads.
 // ---------------------------------------------------------------------------
@@ -457,15 +463,15 @@ constexpr int kBigOp = kB * kBlock;            // 32 KB
 constexpr int kBigStage = 2 * kBigOp;          // A, then B
 constexpr int kBigScales = 2 * kB * 4;         // a's rows, then b's: 4 k blocks each
 
-template <typename T, bool WIDE, int G>
+template <typename T, bool WIDE, int FA, int G>
 __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint32_t base, const uint8_t* pa,
                                          const uint8_t* pb, const uint8_t* sca, const uint8_t* scb,
                                          const uint32_t (&off)[10], uint32_t soa, uint32_t sob, int kb0, int nk, int wave, int lane,
-                                         f32x4 (&acc)[4][8]) {
+                                         f32x4 (&acc)[4][2 * FA]) {
   const int w4 = wave & 3, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);
-  i32x8 fa[4], fb[4];
-  int sa[4], sb[4];
+  i32x8 fa[FA], fb[4];
+  int sa[FA], sb[4];
   auto frag = [&](const char* p) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(p + foff);
     const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (foff ^ 64));
@@ -478,7 +484,9 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
     return *reinterpret_cast<const int*>(q + (row + r16) * 4) >> (((kb0 + s) & 3) * 8);
   };
   // the DMA of this group for block s: `part` 0 in phase 4(s-2)+2 or +3, 1
-  // (group 0) in phase 4(s-2)+4; instruction q of 6
+  // (group 0) in phase 4(s-2)+4; instruction q
+  constexpr int kA1 = 2 * FA - 3;         // a's rows by a wave of group 0, 8 per instruction
+  constexpr int kOps[2] = {6, kA1 + 1};   // memory operations of a part
   auto fetch = [&](int s, int part, int q) {
     const uint32_t st = base + (s & 1) * kBigStage;
     const uint32_t sc = base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 256;
@@ -490,26 +498,24 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
       if (q < 5) dma16s(pb + k, off[q], st + kBigOp + (5 * w4 + q) * 1024);
       else dma4s(scb + ((kb0 + s) & ~3), sob, sc + kB * 4);
     } else {
-      if (q < 5) dma16s(pa + k, off[5 + q], st + (12 + 5 * w4 + q) * 1024);
+      if (q < kA1) dma16s(pa + k, off[5 + q], st + (12 + kA1 * w4 + q) * 1024);
       else dma4s(sca + ((kb0 + s) & ~3), soa, sc);
     }
   };
-  constexpr int kOps = 6;  // memory operations of a part
   auto fetch_all = [&](int s, int part) {
 #pragma unroll
-    for (int q = 0; q < kOps; ++q) fetch(s, part, q);
+    for (int q = 0; q < kOps[part]; ++q) fetch(s, part, q);
   };
   // reads of block s with the DMA of block t (FETCH) between them
   auto load_a = [&](int s, int half, auto dma, int t) {
-    const char* p = lds + (s & 1) * kBigStage + (128 * G + 64 * half) * kBlock;
+    const char* p = lds + (s & 1) * kBigStage + (2 * G + half) * 16 * FA * kBlock;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
+    for (int f = 0; f < FA; ++f) {
       fa[f] = frag(p + 16 * f * kBlock);
-      sa[f] = scale(s, 128 * G + 64 * half + 16 * f);
-      if constexpr (decltype(dma)::value) {  // q 0-5 beside four fragments
-        fetch(t, 0, f);
-        if (f >= 2) fetch(t, 0, 2 + f);
-      }
+      sa[f] = scale(s, (2 * G + half) * 16 * FA + 16 * f);
+      if constexpr (decltype(dma)::value)  // spread over the fragments
+#pragma unroll
+        for (int q = kOps[0] * f / FA; q < kOps[0] * (f + 1) / FA; ++q) fetch(t, 0, q);
     }
   };
   auto load_b = [&](int s, auto dma, int t) {
@@ -518,20 +524,19 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
     for (int f = 0; f < 4; ++f) {
       fb[f] = frag(p + 16 * f * kBlock);
       sb[f] = scale(s, kB + 64 * w4 + 16 * f);
-      if constexpr (decltype(dma)::value) {
-        fetch(t, 1, f);
-        if (f >= 2) fetch(t, 1, 2 + f);
-      }
+      if constexpr (decltype(dma)::value)
+#pragma unroll
+        for (int q = kOps[1] * f / 4; q < kOps[1] * (f + 1) / 4; ++q) fetch(t, 1, q);
     }
   };
   auto mul = [&](int half) {
     if constexpr (!WIDE) {
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
+      for (int f = 0; f < FA; ++f)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          acc[q][4 * half + f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              fb[q], fa[f], acc[q][4 * half + f], 0, 0, 0, sb[q], 0, sa[f]);
+          acc[q][FA * half + f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fb[q], fa[f], acc[q][FA * half + f], 0, 0, 0, sb[q], 0, sa[f]);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -539,11 +544,11 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
 #pragma unroll
         for (int q = 0; q < 4; ++q) wb[q] = widen8(fb[q][2 * k], fb[q][2 * k + 1], scale_of(sb[q] & 255));
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
+        for (int f = 0; f < FA; ++f) {
           const bf16x8 wa = widen8(fa[f][2 * k], fa[f][2 * k + 1], scale_of(sa[f] & 255));
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            acc[q][4 * half + f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], wa, acc[q][4 * half + f], 0, 0, 0);
+            acc[q][FA * half + f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], wa, acc[q][FA * half + f], 0, 0, 0);
         }
       }
     }
@@ -552,7 +557,7 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
   if (G == 0) fetch_all(0, 1);
   if (nk > 1) {
     fetch_all(1, 0);
-    stage_barrier<kOps>();
+    stage_barrier<kOps[0]>();
   } else {
     stage_barrier<0>();
   }
@@ -571,7 +576,7 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
     load_a(s, 1, std::bool_constant<kLeft >= 2>{}, s + 2);
     // the end of phase 4s+3: block s+1 has landed; what was just issued for
     // block s+2 may be in flight
-    constexpr int kLand = kLeft >= 2 ? kOps : 0;
+    constexpr int kLand = kLeft >= 2 ? kOps[0] : 0;
     stage_barrier<(G == 1 ? kLand : 63)>();
     mul(1);
     stage_barrier<(G == 0 ? kLand : 63)>();
@@ -583,7 +588,7 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
   if (G == 0) stage_barrier<63>();  // group 1's last phase
 }
 
-template <typename T, bool WIDE>
+template <typename T, bool WIDE, int FA>
 __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
   constexpr bool kPair = sizeof(T) == 2;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kBigStage + 2 * kBigScales];
@@ -596,7 +601,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
   // Tile bases, and this lane's source offsets for each DMA instruction: LDS
   // rows 8 i .. +7 of an operand, lane l: row l / 8, position l % 8.
-  const int64_t ra = (int64_t)ti * kB, rb = (int64_t)tj * kB;
+  const int64_t ra = (int64_t)ti * 64 * FA, rb = (int64_t)tj * kB;
   const uint8_t* pa = a.a.codes + ra * a.a.ld;
   const uint8_t* pb = a.b.codes + rb * a.b.ld;
   const int w4 = wave & 3;
@@ -609,31 +614,30 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
     const int r = 64 * (lr >> 6) + b_row<kPair>((lr & 63) >> 4, lr & 15);
     return (uint32_t)(min(rb + r, a.n - 1) - rb) * (uint32_t)a.b.ld + (uint32_t)(((lane & 7) ^ (lr & 7)) << 4);
   };
-  f32x4 acc[4][8];
+  f32x4 acc[4][2 * FA];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{};
+    for (int j = 0; j < 2 * FA; ++j) acc[i][j] = f32x4{};
   uint32_t off[10];
   if (wave < 4) {
 #pragma unroll
-    for (int q = 0; q < 5; ++q) {
-      off[q] = off_b(5 * w4 + q);
-      off[5 + q] = off_a(12 + 5 * w4 + q);
-    }
+    for (int q = 0; q < 5; ++q) off[q] = off_b(5 * w4 + q);
+#pragma unroll
+    for (int q = 0; q < 2 * FA - 3; ++q) off[5 + q] = off_a(12 + (2 * FA - 3) * w4 + q);
     const int64_t r = min(ra + 64 * w4 + lane, a.m - 1);
     const int64_t c = min(rb + 64 * w4 + b_row<kPair>(lane >> 4, lane & 15), a.n - 1);
     const int64_t a0 = ra >> a.a.sshift, b0 = rb >> a.b.sshift;
     const uint32_t soa = (uint32_t)((r >> a.a.sshift) - a0) * (uint32_t)a.a.sld;
     const uint32_t sob = (uint32_t)((c >> a.b.sshift) - b0) * (uint32_t)a.b.sld;
-    big_loop<T, WIDE, 0>(a, lds, base, pa, pb, a.a.scales + a0 * a.a.sld, a.b.scales + b0 * a.b.sld, off, soa, sob,
+    big_loop<T, WIDE, FA, 0>(a, lds, base, pa, pb, a.a.scales + a0 * a.a.sld, a.b.scales + b0 * a.b.sld, off, soa, sob,
                    kb0, nk, wave, lane, acc);
   } else {
 #pragma unroll
     for (int q = 0; q < 6; ++q) off[q] = q < 3 ? off_b(20 + 3 * w4 + q) : off_a(3 * w4 + q - 3);
-    big_loop<T, WIDE, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, kb0, nk, wave, lane, acc);
+    big_loop<T, WIDE, FA, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, kb0, nk, wave, lane, acc);
   }
-  store_wave<T, 8, 4>(a, split, ra + 128 * (wave >> 2), rb + 64 * w4, lane, acc);
+  store_wave<T, 2 * FA, 4>(a, split, ra + 32 * FA * (wave >> 2), rb + 64 * w4, lane, acc);
 }
 
 // out (+)= the partial sums, split by split in order; 4 columns per thread.
@@ -856,7 +860,7 @@ constexpr int64_t kMaxTiles = (1 << 21) - 8;
 enum Kind { kDirect, kSmall, kTile, kBig };
 struct Choice {
   Kind kind;
-  int edge;  // of a tile
+  int em, en;  // tile rows and columns
   int splits, per;
   size_t ws_bytes;
 };
@@ -864,30 +868,32 @@ struct Choice {
 // Estimated time in us of a kernel on `tiles` tiles of nkb blocks: a launch,
 // then rounds of one tile per CU, each a fixed part (first loads, last stores)
 // and a part per block, which is less where a round leaves CUs idle (power,
-// cache bandwidth). Fitted to times of 30 products from 512 x 2048 x 2048 to
-// 8192^3, which it meets within about 15 %.
+// cache bandwidth). Fitted to times of 130 random products up to 12288 x 8192 x
+// 12288 with either result type: off by 6 (64-tiles) to 14 % (256-tiles); the
+// kernel taken is on average 0.7 % slower than the fastest, 24 % at worst.
 struct Cost {
   double fixed, block;
 };
 double estimate(const Cost& c, int64_t tiles, double nkb) {
   const int64_t part = tiles % kCUs;
   double t = 1.5 + (double)(tiles / kCUs) * (c.fixed + c.block * nkb);
-  if (part) t += c.fixed + c.block * nkb * (0.75 + 0.25 * (double)part / (double)kCUs);
+  if (part) t += c.fixed + c.block * nkb * (0.6 + 0.4 * std::sqrt((double)part / (double)kCUs));
   return t;
 }
 
 // The kernel for a product: the cheapest by the estimate. Examples (measured
 // us, 8-bit path, tiles of 16, 64, 128, 256): 1x6144x2048: 5.4, 6.6, -, 21;
 // 512x2048x2048: 39, 7.7, 11, 24; 1024x4096x4096: -, 37, 21, 43;
-// 6144x2048x8192: -, 192, 112, 90.
+// 6144x2048x8192: -, 192, 107, 81 (192 x 256: 78); 8192x6144x2048: -, -, 122,
+// 90 (192 x 256: 106).
 Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
   const int64_t nkb = ceil_div(k, kBlock);
   auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };
-  Choice c{kSmall, kS, 1, (int)nkb, 0};
+  Choice c{kSmall, kS, kS, 1, (int)nkb, 0};
   if (m == 0 || n == 0) return c;
-  if (nkb == 0) return Choice{kTile, kT, 1, 0, 0};  // zeros; that kernel's loop may be empty
+  if (nkb == 0) return Choice{kTile, kT, kT, 1, 0, 0};  // zeros; that kernel's loop may be empty
   const bool wide = out_dtype == MUONH_DT_FP32;
-  const Cost small = wide ? Cost{3.2, 0.25} : Cost{2.8, 0.205};
+  const Cost small = wide ? Cost{3.1, 0.261} : Cost{2.7, 0.204};
   double best = 0;
   // 64 x 64, the k blocks split over up to 16 workgroups where tiles are few:
   // a second launch joins the partial sums
@@ -899,20 +905,24 @@ Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
     c.splits = s == 1 ? 1 : (int)ceil_div(nkb, c.per);
   }
   // 16 x 16 tiles, all at once: a floor of latency per block, then the rate
-  // at which the caches deliver both operands' rows
-  const double t16 = 2.8 + (double)nkb * std::max(0.08, 5e-4 * (double)tiles(16));
+  // at which the caches deliver both operands' rows, which are up to 32 a tile
+  // and 17 for a single token
+  const double rows = 1.0 + (double)std::min<int64_t>(std::min(m, n), 16) / 24.0;
+  const double t16 = 2.8 + (double)nkb * rows * std::max(0.08, 5e-4 * (double)tiles(16));
   if (t16 < best) {
     best = t16;
-    c = Choice{kDirect, 16, 1, (int)nkb, 0};
+    c = Choice{kDirect, 16, 16, 1, (int)nkb, 0};
   }
   if (code_ld(k) < kMaxTileLd) {
-    const Cost tile = wide ? Cost{4.0, 0.85} : Cost{3.0, 0.51}, big = wide ? Cost{8.0, 2.75} : Cost{7.0, 1.43};
-    for (const Kind kind : {kTile, kBig}) {
-      const double t = kind == kTile ? estimate(tile, tiles(kT), (double)nkb) : estimate(big, tiles(kB), (double)nkb);
-      if (t >= best) continue;
+    auto take = [&](Kind kind, int em, int en, const Cost& cost) {
+      const double t = estimate(cost, ceil_div(m, em) * ceil_div(n, en), (double)nkb);
+      if (t >= best) return;
       best = t;
-      c = Choice{kind, kind == kTile ? kT : kB, 1, (int)nkb, 0};
-    }
+      c = Choice{kind, em, en, 1, (int)nkb, 0};
+    };
+    take(kTile, kT, kT, wide ? Cost{4.6, 0.831} : Cost{3.6, 0.503});
+    take(kBig, kB, kB, wide ? Cost{8.9, 2.91} : Cost{7.0, 1.39});
+    take(kBig, kB - 64, kB, wide ? Cost{7.4, 2.2} : Cost{5.5, 1.15});
   }
   if (c.splits > 1) c.ws_bytes = (size_t)c.splits * m * (ceil_div(n, 4) * 4) * sizeof(float);
   return c;
@@ -921,10 +931,18 @@ Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
 template <typename T, bool WIDE>
 int launch(const MatArgs& a, const Choice& c, hipStream_t s) {
   const dim3 grid((unsigned)map_grid((int64_t)a.tm * a.tn), (unsigned)a.splits), direct(64 * kWaves);
-  if (c.kind == kBig) hipLaunchKernelGGL((k_matmul_big<T, WIDE>), grid, dim3(512), 0, s, a);
-  else if (c.kind == kTile) hipLaunchKernelGGL((k_matmul_tile<T, WIDE>), grid, dim3(512), 0, s, a);
-  else if (c.kind == kSmall) hipLaunchKernelGGL((k_matmul_small<T, WIDE>), grid, direct, 0, s, a);
-  else hipLaunchKernelGGL((k_matmul_direct<T, WIDE>), grid, direct, 0, s, a);
+  if (c.kind == kBig) {
+    if (c.em == kB)
+      hipLaunchKernelGGL((k_matmul_big<T, WIDE, 4>), grid, dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_matmul_big<T, WIDE, 3>), grid, dim3(512), 0, s, a);
+  } else if (c.kind == kTile) {
+    hipLaunchKernelGGL((k_matmul_tile<T, WIDE>), grid, dim3(512), 0, s, a);
+  } else if (c.kind == kSmall) {
+    hipLaunchKernelGGL((k_matmul_small<T, WIDE>), grid, direct, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_matmul_direct<T, WIDE>), grid, direct, 0, s, a);
+  }
   if (a.part)
     hipLaunchKernelGGL((k_matmul_join<T>), dim3((unsigned)ceil_div(a.m * (a.pld >> 2), 256)), dim3(256),
                        0, s, a);
@@ -1018,8 +1036,8 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   x.per = c.per;
   x.pld = ceil_div(n, 4) * 4;
   x.part = c.ws_bytes ? static_cast<float*>(workspace) : nullptr;
-  x.tm = (int)ceil_div(m, c.edge);
-  x.tn = (int)ceil_div(n, c.edge);
+  x.tm = (int)ceil_div(m, c.em);
+  x.tn = (int)ceil_div(n, c.en);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return out_dtype == MUONH_DT_BF16 ? launch<__bf16, false>(x, c, s) : launch<float, true>(x, c, s);
 }

@@ -196,9 +196,9 @@ def test_product_against_fp64(m, n, k, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("k", [64, 128, 129, 300, 400, 520, 700, 1100, 2300])
-@pytest.mark.parametrize("m,n", [(9, 150), (200, 190), (1500, 1420), (3100, 3300)])
+@pytest.mark.parametrize("m,n", [(9, 150), (200, 190), (640, 730), (1500, 1420), (3100, 3300), (4090, 3900)])
 def test_product_at_every_tile_size_and_loop_length(m, n, k, dtype):
-    """16, 64, 128 and 256 wide tiles; 1 to 18 blocks of k: shorter than,
+    """Tiles of 16, 64, 128, 192 x 256 and 256; 1 to 18 blocks of k: shorter than,
     as long as and longer than every ring, ending in a ragged block or not."""
     a, va = operand(m, k, 21)
     b, vb = operand(n, k, 22)
@@ -207,8 +207,8 @@ def test_product_at_every_tile_size_and_loop_length(m, n, k, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("ab", [("rows", "rows"), ("tiles", "rows"), ("tiles", "tiles"), ("rows", "tiles")])
-@pytest.mark.parametrize("m,n,k", [(40, 300, 700), (300, 260, 700), (140, 200, 5000), (1400, 1500, 300),
-                                   (3200, 3100, 300)])
+@pytest.mark.parametrize("m,n,k", [(40, 300, 700), (300, 260, 700), (140, 200, 5000), (640, 730, 300), (1400, 1500, 300),
+                                   (3200, 3100, 300), (3900, 4050, 300)])
 def test_product_of_block_kinds_accumulates(m, n, k, ab, dtype):
     a, va = operand(m, k, 13, ab[0], spread=False)
     b, vb = operand(n, k, 14, ab[1], spread=False)
@@ -225,8 +225,8 @@ def test_product_of_block_kinds_accumulates(m, n, k, ab, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("m,n,k", [(3, 200, 256), (150, 203, 256), (150, 203, 6000), (1400, 1433, 300),
-                                   (3100, 3099, 200)])
+@pytest.mark.parametrize("m,n,k", [(3, 200, 256), (150, 203, 256), (150, 203, 6000), (640, 733, 300), (1400, 1433, 300),
+                                   (3100, 3099, 200), (4000, 3999, 200)])
 @pytest.mark.parametrize("extra,first", [(53, 0), (8, 0), (0, 1), (61, 8)])
 def test_product_into_strided_rows_writes_nothing_else(m, n, k, extra, first, dtype):
     ld = n + extra
@@ -257,8 +257,8 @@ def test_product_of_empty_operands(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("m,n,k", [(5, 150, 300), (140, 150, 300), (140, 150, 5000), (1500, 1400, 300),
-                                   (3100, 3200, 300)])
+@pytest.mark.parametrize("m,n,k", [(5, 150, 300), (140, 150, 300), (140, 150, 5000), (640, 730, 300), (1500, 1400, 300),
+                                   (3100, 3200, 300), (3900, 4050, 300)])
 def test_nan_and_overflow_stay_in_their_rows(m, n, k, dtype):
     g = torch.Generator("cuda").manual_seed(4)
     x, w = torch.randn(m, k, device="cuda", generator=g), torch.randn(n, k, device="cuda", generator=g)
