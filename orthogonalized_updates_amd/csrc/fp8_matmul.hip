@@ -171,60 +171,81 @@ __device__ __forceinline__ void put_odd(__bf16* p, u32x4 x, u32x4 y, int lane, b
   }
 }
 
-// Stores a wave's 16 NA rows x 16 NB columns from row i0, column j0: acc[q][f],
+// Lanes 2i and 2i + 1 hold 16 bytes x and, 64 bytes on, 16 bytes y of rows r
+// and r + 1. Afterwards their x are both of row r (x of lane 2i, y of lane
+// 2i + 1) and their y both of row r + 1, so that a store of x writes 8 rows of
+// 128 bytes instead of 16 of 64.
+template <typename V>
+__device__ __forceinline__ void pair_rows(V& x, V& y, bool odd_lane) {
+  i32x4 u = __builtin_bit_cast(i32x4, x), v = __builtin_bit_cast(i32x4, y);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int got = __builtin_amdgcn_mov_dpp(odd_lane ? u[e] : v[e], 0xB1, 0xF, 0xF, false);  // quad [1,0,3,2]
+    u[e] = odd_lane ? got : u[e];
+    v[e] = odd_lane ? v[e] : got;
+  }
+  x = __builtin_bit_cast(V, u);
+  y = __builtin_bit_cast(V, v);
+}
+
+// Stores a wave's 16 NA rows x 64 columns from row i0, column j0: acc[q][f],
 // b's fragment q, a's fragment f; lane l holds row 16 f + l%16 and columns
 // b_row(q, 4 (l/16) ..+3).
-template <typename T, int NA, int NB>
-__device__ __forceinline__ void store_wave(const MatArgs& a, int split, int64_t i0, int64_t j0, int lane,
-                                           const f32x4 (&acc)[NB][NA]) {
-  constexpr bool kPair = sizeof(T) == 2;
-  const int r16 = lane & 15, g = lane >> 4;
-  if constexpr (kPair && NB == 4) {
-    if (a.odd && !a.part && !a.accumulate && j0 + 64 <= a.n) {
+template <typename T, int NA>
+__device__ __forceinline__ void store_wave(const MatArgs& a, int64_t i0, int64_t j0, int lane,
+                                           const f32x4 (&acc)[4][NA]) {
+  const int r16 = lane & 15, g = lane >> 4, r2 = r16 & ~1;
+  const bool odd_lane = lane & 1;
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int f = 0; f < NA; ++f) {
-        u32x4 w[2];
+    for (int f = 0; f < NA; ++f)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x4 u = acc[2 * h][f], v = acc[2 * h + 1][f];
-          const bf16x8 c = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
-                            (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-          w[h] = __builtin_bit_cast(u32x4, c);
-        }
+      for (int q = 0; q < 4; q += 2) {
+        f32x4 x = acc[q][f], y = acc[q + 1][f];
+        pair_rows(x, y, odd_lane);
+        const int64_t i = i0 + 16 * f + r2, j = j0 + 16 * q + 4 * g + (odd_lane ? 16 : 0);
+        const float u[4] = {x[0], x[1], x[2], x[3]}, v[4] = {y[0], y[1], y[2], y[3]};
+        if (i < a.m) put<T, 4>(a, i, j, u);
+        if (i + 1 < a.m) put<T, 4>(a, i + 1, j, v);
+      }
+  } else if (!a.accumulate && j0 + 64 <= a.n) {
+#pragma unroll
+    for (int f = 0; f < NA; ++f) {
+      u32x4 w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 u = acc[2 * h][f], v = acc[2 * h + 1][f];
+        const bf16x8 c = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
+                          (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        w[h] = __builtin_bit_cast(u32x4, c);
+      }
+      if (a.odd) {
         const int64_t i = i0 + 16 * f + r16;
         __bf16* p = static_cast<__bf16*>(a.out) + i * a.ldo + j0;
         put_odd(p, w[0], w[1], lane, (reinterpret_cast<uintptr_t>(p) & 2) != 0, i < a.m);
+      } else {
+        typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+        pair_rows(w[0], w[1], odd_lane);
+        const int64_t i = i0 + 16 * f + r2;
+        __bf16* p = static_cast<__bf16*>(a.out) + i * a.ldo + j0 + 8 * g + (odd_lane ? 32 : 0);
+        if (i < a.m) *reinterpret_cast<u32x4_a4*>(p) = w[0];
+        if (i + 1 < a.m) *reinterpret_cast<u32x4_a4*>(p + a.ldo) = w[1];
       }
-      return;
     }
-  }
+  } else {
 #pragma unroll
-  for (int f = 0; f < NA; ++f) {
-    const int64_t i = i0 + 16 * f + r16;
-    if (i >= a.m) continue;
-    if (a.part) {
-      float* p = a.part + ((int64_t)split * a.m + i) * a.pld;
+    for (int f = 0; f < NA; ++f) {
+      const int64_t i = i0 + 16 * f + r16;
+      if (i >= a.m) continue;
 #pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        const int64_t j = j0 + b_row<kPair>(q, 4 * g);
-        if (j < a.pld) *reinterpret_cast<f32x4*>(p + j) = acc[q][f];  // pld: a multiple of 4
-      }
-    } else if constexpr (kPair) {
-#pragma unroll
-      for (int q = 0; q < NB; q += 2) {
+      for (int q = 0; q < 4; q += 2) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[e] = acc[q][f][e];
           v[4 + e] = acc[q + 1][f][e];
         }
-        put<T, 8>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        const float v[4] = {acc[q][f][0], acc[q][f][1], acc[q][f][2], acc[q][f][3]};
-        put<T, 4>(a, i, j0 + b_row<kPair>(q, 4 * g), v);
+        put<T, 8>(a, i, j0 + b_row<true>(q, 4 * g), v);
       }
     }
   }
@@ -280,7 +301,9 @@ __device__ __forceinline__ void dma4s(const uint8_t* base, uint32_t off, uint32_
 // The b operand is the MFMA's first one, so a lane's 4 accumulators are 4
 // consecutive columns of one row of out. For 2-byte results b's rows are
 // also dealt to the fragments so that a lane holds 8 consecutive columns in
-// two neighbouring fragments (b_row): 16-byte stores, 64-byte runs per row.
+// two neighbouring fragments (b_row): 16-byte stores, 64-byte runs per row,
+// which lane pairs join to runs of 128 (pair_rows; 8192 x 6144 x 128 with bf16
+// results 26.8 -> 24.7 us, 8192 x 6144 x 2048 95 -> 90).
 //
 // 128 x 128 tiles, a ring of 4 LDS stages of one k block (32 KB each). The 8
 // waves form two groups of 4 (2 x 2, wave tile 64 x 64), one wave of each per
@@ -310,10 +333,10 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[kRing * (kStageBytes + kScaleBytes)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int w4 = wave & 3, group = wave >> 2, split = blockIdx.y;
+  const int w4 = wave & 3, group = wave >> 2;
   int ti, tj;
   if (!map_tile(a, blockIdx.x, ti, tj)) return;
-  const int kb0 = split * a.per, nk = min(a.per, a.nkb - kb0);
+  const int nk = a.nkb;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
   const int64_t ra = (int64_t)ti * kT, rb = (int64_t)tj * kT;
 
@@ -340,11 +363,11 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
   const uint32_t sdst = base + kRing * kStageBytes + w4 * 256;
   auto fetch_part = [&](int s, int c) {  // quarter c
     const int slot = s & (kRing - 1);
-    const int64_t k = (int64_t)(kb0 + s) * kBlock;
+    const int64_t k = (int64_t)s * kBlock;
 #pragma unroll
     for (int q = 2 * c; q < 2 * c + 2; ++q)
       dma16s(codes + k, off[q], dst + slot * kStageBytes + q * 1024);
-    if (c == 3) dma4s(scales + ((kb0 + s) & ~3), soff, sdst + slot * kScaleBytes);
+    if (c == 3) dma4s(scales + (s & ~3), soff, sdst + slot * kScaleBytes);
   };
   auto fetch = [&](int s) {
 #pragma unroll
@@ -366,7 +389,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
     constexpr bool kMore = decltype(more)::value;
     const char* st = lds + (s & (kRing - 1)) * kStageBytes;
     const char* ss = lds + kRing * kStageBytes + (s & (kRing - 1)) * kScaleBytes;
-    const int sh = ((kb0 + s) & 3) * 8;
+    const int sh = (s & 3) * 8;
     auto frag = [&](const char* p) {
       const i32x4 lo = *reinterpret_cast<const i32x4*>(p + foff);
       const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (foff ^ 64));
@@ -427,7 +450,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
 #pragma unroll
     for (int f = 0; f < 2; ++f)
       sum[q][f] = (group == 0 ? acc[q][f] : acc[q][2 + f]) + red[(wave * 8 + q * 2 + f) * 64 + lane];
-  store_wave<T, 2, 4>(a, split, ra + 64 * wm + 32 * group, rb + 64 * wn, lane, sum);
+  store_wave<T, 2>(a, ra + 64 * wm + 32 * group, rb + 64 * wn, lane, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -466,7 +489,7 @@ constexpr int kBigScales = 2 * kB * 4;         // a's rows, then b's: 4 k blocks
 template <typename T, bool WIDE, int FA, int G>
 __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint32_t base, const uint8_t* pa,
                                          const uint8_t* pb, const uint8_t* sca, const uint8_t* scb,
-                                         const uint32_t (&off)[10], uint32_t soa, uint32_t sob, int kb0, int nk, int wave, int lane,
+                                         const uint32_t (&off)[10], uint32_t soa, uint32_t sob, int nk, int wave, int lane,
                                          f32x4 (&acc)[4][2 * FA]) {
   const int w4 = wave & 3, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);
@@ -481,7 +504,7 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
   // follow a's 256
   auto scale = [&](int s, int row) {
     const char* q = lds + 2 * kBigStage + (s & 1) * kBigScales;
-    return *reinterpret_cast<const int*>(q + (row + r16) * 4) >> (((kb0 + s) & 3) * 8);
+    return *reinterpret_cast<const int*>(q + (row + r16) * 4) >> ((s & 3) * 8);
   };
   // the DMA of this group for block s: `part` 0 in phase 4(s-2)+2 or +3, 1
   // (group 0) in phase 4(s-2)+4; instruction q
@@ -490,16 +513,16 @@ __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint
   auto fetch = [&](int s, int part, int q) {
     const uint32_t st = base + (s & 1) * kBigStage;
     const uint32_t sc = base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 256;
-    const int64_t k = (int64_t)(kb0 + s) * kBlock;
+    const int64_t k = (int64_t)s * kBlock;
     if (G == 1) {
       if (q < 3) dma16s(pb + k, off[q], st + kBigOp + (20 + 3 * w4 + q) * 1024);
       else dma16s(pa + k, off[q], st + (3 * w4 + q - 3) * 1024);
     } else if (part == 0) {
       if (q < 5) dma16s(pb + k, off[q], st + kBigOp + (5 * w4 + q) * 1024);
-      else dma4s(scb + ((kb0 + s) & ~3), sob, sc + kB * 4);
+      else dma4s(scb + (s & ~3), sob, sc + kB * 4);
     } else {
       if (q < kA1) dma16s(pa + k, off[5 + q], st + (12 + kA1 * w4 + q) * 1024);
-      else dma4s(sca + ((kb0 + s) & ~3), soa, sc);
+      else dma4s(sca + (s & ~3), soa, sc);
     }
   };
   auto fetch_all = [&](int s, int part) {
@@ -594,10 +617,9 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kBigStage + 2 * kBigScales];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.y;
   int ti, tj;
   if (!map_tile(a, blockIdx.x, ti, tj)) return;
-  const int kb0 = split * a.per, nk = min(a.per, a.nkb - kb0);
+  const int nk = a.nkb;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
   // Tile bases, and this lane's source offsets for each DMA instruction: LDS
   // rows 8 i .. +7 of an operand, lane l: row l / 8, position l % 8.
@@ -631,13 +653,13 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
     const uint32_t soa = (uint32_t)((r >> a.a.sshift) - a0) * (uint32_t)a.a.sld;
     const uint32_t sob = (uint32_t)((c >> a.b.sshift) - b0) * (uint32_t)a.b.sld;
     big_loop<T, WIDE, FA, 0>(a, lds, base, pa, pb, a.a.scales + a0 * a.a.sld, a.b.scales + b0 * a.b.sld, off, soa, sob,
-                   kb0, nk, wave, lane, acc);
+                   nk, wave, lane, acc);
   } else {
 #pragma unroll
     for (int q = 0; q < 6; ++q) off[q] = q < 3 ? off_b(20 + 3 * w4 + q) : off_a(3 * w4 + q - 3);
-    big_loop<T, WIDE, FA, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, kb0, nk, wave, lane, acc);
+    big_loop<T, WIDE, FA, 1>(a, lds, base, pa, pb, nullptr, nullptr, off, 0, 0, nk, wave, lane, acc);
   }
-  store_wave<T, 2 * FA, 4>(a, split, ra + 32 * FA * (wave >> 2), rb + 64 * w4, lane, acc);
+  store_wave<T, 2 * FA>(a, ra + 32 * FA * (wave >> 2), rb + 64 * w4, lane, acc);
 }
 
 // out (+)= the partial sums, split by split in order; 4 columns per thread.
@@ -713,11 +735,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_matmul_direct(MatArgs a) {
   __shared__ __attribute__((aligned(16))) f32x4 red[kWaves * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r16 = lane & 15, g = lane >> 4, split = blockIdx.y;
+  const int r16 = lane & 15, g = lane >> 4;
   int ti, tj;
   if (!map_tile(a, blockIdx.x, ti, tj)) return;
   const int64_t i0 = (int64_t)ti * 16, j0 = (int64_t)tj * 16;
-  const int kb0 = split * a.per, kb1 = min(kb0 + a.per, a.nkb);
+  const int kb1 = a.nkb;
   const int64_t ra = min(i0 + r16, a.m - 1), rb = min(j0 + r16, a.n - 1);
   const uint8_t *ca = a.a.codes + ra * a.a.ld + 16 * g, *cb = a.b.codes + rb * a.b.ld + 16 * g;
   const uint8_t *sa = a.a.scales + (ra >> a.a.sshift) * a.a.sld, *sb = a.b.scales + (rb >> a.b.sshift) * a.b.sld;
@@ -737,7 +759,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_matmul_direct(MatArgs a) {
     s.sb[0] = sb[kb];
   };
   f32x4 acc[1][1] = {{f32x4{}}};
-  int kb = kb0 + wave;
+  int kb = wave;
   Set s0, s1;
   if (kb < kb1) load(s0, kb);
   for (; kb + kWaves < kb1; kb += 2 * kWaves) {
@@ -747,7 +769,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_matmul_direct(MatArgs a) {
     mma_block<WIDE, 1, 1>(s1.b, s1.a, s1.sb, s1.sa, acc);
   }
   if (kb < kb1) mma_block<WIDE, 1, 1>(s0.b, s0.a, s0.sb, s0.sa, acc);
-  join_waves<T, 1, 1>(a, split, i0, j0, red, 64, acc);
+  join_waves<T, 1, 1>(a, 0, i0, j0, red, 64, acc);
 }
 
 // ---------------------------------------------------------------------------
