@@ -191,64 +191,108 @@ __device__ __forceinline__ void pair_rows(V& x, V& y, bool odd_lane) {
 // Stores a wave's 16 NA rows x 64 columns from row i0, column j0: acc[q][f],
 // b's fragment q, a's fragment f; lane l holds row 16 f + l%16 and columns
 // b_row(q, 4 (l/16) ..+3).
-template <typename T, int NA>
-__device__ __forceinline__ void store_wave(const MatArgs& a, int64_t i0, int64_t j0, int lane,
+template <typename T, int NA, bool ADD>
+__device__ __forceinline__ void store_rows(const MatArgs& a, int64_t i0, int64_t j0, int lane,
                                            const f32x4 (&acc)[4][NA]) {
   const int r16 = lane & 15, g = lane >> 4, r2 = r16 & ~1;
   const bool odd_lane = lane & 1;
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int f = 0; f < NA; ++f)
-#pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        f32x4 x = acc[q][f], y = acc[q + 1][f];
-        pair_rows(x, y, odd_lane);
-        const int64_t i = i0 + 16 * f + r2, j = j0 + 16 * q + 4 * g + (odd_lane ? 16 : 0);
-        const float u[4] = {x[0], x[1], x[2], x[3]}, v[4] = {y[0], y[1], y[2], y[3]};
-        if (i < a.m) put<T, 4>(a, i, j, u);
-        if (i + 1 < a.m) put<T, 4>(a, i + 1, j, v);
-      }
-  } else if (!a.accumulate && j0 + 64 <= a.n) {
-#pragma unroll
-    for (int f = 0; f < NA; ++f) {
-      u32x4 w[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4 u = acc[2 * h][f], v = acc[2 * h + 1][f];
-        const bf16x8 c = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
-                          (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        w[h] = __builtin_bit_cast(u32x4, c);
-      }
-      if (a.odd) {
-        const int64_t i = i0 + 16 * f + r16;
-        __bf16* p = static_cast<__bf16*>(a.out) + i * a.ldo + j0;
-        put_odd(p, w[0], w[1], lane, (reinterpret_cast<uintptr_t>(p) & 2) != 0, i < a.m);
-      } else {
-        typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-        pair_rows(w[0], w[1], odd_lane);
-        const int64_t i = i0 + 16 * f + r2;
-        __bf16* p = static_cast<__bf16*>(a.out) + i * a.ldo + j0 + 8 * g + (odd_lane ? 32 : 0);
-        if (i < a.m) *reinterpret_cast<u32x4_a4*>(p) = w[0];
-        if (i + 1 < a.m) *reinterpret_cast<u32x4_a4*>(p + a.ldo) = w[1];
-      }
-    }
-  } else {
+  // rows of fragments whose old values are read together
+  constexpr int kGroup = NA % 3 == 0 ? 3 : sizeof(T) == 2 && NA % 4 == 0 ? 4 : 2;
+  if (j0 + 64 > a.n) {  // the tile ends in these columns
 #pragma unroll
     for (int f = 0; f < NA; ++f) {
       const int64_t i = i0 + 16 * f + r16;
       if (i >= a.m) continue;
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        float v[8];
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {acc[q][f][0], acc[q][f][1], acc[q][f][2], acc[q][f][3]};
+        put<T, 4>(a, i, j0 + b_row<sizeof(T) == 2>(q, 4 * g), v);
+      }
+    }
+  } else if constexpr (sizeof(T) == 4) {
+    typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+    const int64_t j = j0 + 4 * g + (odd_lane ? 16 : 0);
+    auto at = [&](int f, int q, int y) {
+      return reinterpret_cast<f32x4_a4*>(static_cast<float*>(a.out) +
+                                         min(i0 + 16 * f + r2 + y, a.m - 1) * a.ldo + j + 16 * q);
+    };
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[q][f][e];
-          v[4 + e] = acc[q + 1][f][e];
+    for (int f0 = 0; f0 < NA; f0 += kGroup) {
+      f32x4 old[kGroup][4];
+      if constexpr (ADD) {
+#pragma unroll
+        for (int f = 0; f < kGroup; ++f)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) old[f][q] = *at(f0 + f, q & 2, q & 1);
+      }
+#pragma unroll
+      for (int f = 0; f < kGroup; ++f)
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          f32x4 x = acc[q][f0 + f], y = acc[q + 1][f0 + f];
+          pair_rows(x, y, odd_lane);
+          if constexpr (ADD) {
+            x += old[f][q];
+            y += old[f][q + 1];
+          }
+          const int64_t i = i0 + 16 * (f0 + f) + r2;
+          if (i < a.m) *at(f0 + f, q, 0) = x;
+          if (i + 1 < a.m) *at(f0 + f, q, 1) = y;
         }
-        put<T, 8>(a, i, j0 + b_row<true>(q, 4 * g), v);
+    }
+  } else {
+    typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+    typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+#pragma unroll
+    for (int f0 = 0; f0 < NA; f0 += kGroup) {
+      u32x4 old[kGroup][2];
+      if constexpr (ADD) {
+#pragma unroll
+        for (int f = 0; f < kGroup; ++f)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            old[f][h] = *reinterpret_cast<const u32x4_a2*>(
+                static_cast<const __bf16*>(a.out) + min(i0 + 16 * (f0 + f) + r16, a.m - 1) * a.ldo + j0 + 32 * h + 8 * g);
+      }
+#pragma unroll
+      for (int f = 0; f < kGroup; ++f) {
+        u32x4 w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f32x4 u = acc[2 * h][f0 + f], v = acc[2 * h + 1][f0 + f];
+          if constexpr (ADD) {
+            const bf16x8 o = __builtin_bit_cast(bf16x8, old[f][h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              u[e] += (float)o[e];
+              v[e] += (float)o[4 + e];
+            }
+          }
+          const bf16x8 c = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
+                            (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+          w[h] = __builtin_bit_cast(u32x4, c);
+        }
+        if (a.odd) {
+          const int64_t i = i0 + 16 * (f0 + f) + r16;
+          __bf16* p = static_cast<__bf16*>(a.out) + i * a.ldo + j0;
+          put_odd(p, w[0], w[1], lane, (reinterpret_cast<uintptr_t>(p) & 2) != 0, i < a.m);
+        } else {
+          pair_rows(w[0], w[1], odd_lane);
+          const int64_t i = i0 + 16 * (f0 + f) + r2;
+          __bf16* p = static_cast<__bf16*>(a.out) + i * a.ldo + j0 + 8 * g + (odd_lane ? 32 : 0);
+          if (i < a.m) *reinterpret_cast<u32x4_a4*>(p) = w[0];
+          if (i + 1 < a.m) *reinterpret_cast<u32x4_a4*>(p + a.ldo) = w[1];
+        }
       }
     }
   }
+}
+
+template <typename T, int NA>
+__device__ __forceinline__ void store_wave(const MatArgs& a, int64_t i0, int64_t j0, int lane,
+                                           const f32x4 (&acc)[4][NA]) {
+  if (a.accumulate) store_rows<T, NA, true>(a, i0, j0, lane, acc);
+  else store_rows<T, NA, false>(a, i0, j0, lane, acc);
 }
 
 // Block -> tile. Blocks are dealt to the 8 XCDs in turn; each XCD takes a
@@ -279,6 +323,14 @@ __device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// A pointer that is the same in all lanes, in scalar registers (the compiler
+// may compute uniform values in vector registers, which the DMA's base cannot be).
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+  return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
 }
 
 // LDS DMA: lane l's 16 (4) bytes at base + off go to LDS bytes m0 + 16 l (4 l).
@@ -624,8 +676,8 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
   // Tile bases, and this lane's source offsets for each DMA instruction: LDS
   // rows 8 i .. +7 of an operand, lane l: row l / 8, position l % 8.
   const int64_t ra = (int64_t)ti * 64 * FA, rb = (int64_t)tj * kB;
-  const uint8_t* pa = a.a.codes + ra * a.a.ld;
-  const uint8_t* pb = a.b.codes + rb * a.b.ld;
+  const uint8_t* pa = scalar(a.a.codes + ra * a.a.ld);
+  const uint8_t* pb = scalar(a.b.codes + rb * a.b.ld);
   const int w4 = wave & 3;
   auto off_a = [&](int i) {
     const int lr = 8 * i + (lane >> 3);
@@ -652,7 +704,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
     const int64_t a0 = ra >> a.a.sshift, b0 = rb >> a.b.sshift;
     const uint32_t soa = (uint32_t)((r >> a.a.sshift) - a0) * (uint32_t)a.a.sld;
     const uint32_t sob = (uint32_t)((c >> a.b.sshift) - b0) * (uint32_t)a.b.sld;
-    big_loop<T, WIDE, FA, 0>(a, lds, base, pa, pb, a.a.scales + a0 * a.a.sld, a.b.scales + b0 * a.b.sld, off, soa, sob,
+    big_loop<T, WIDE, FA, 0>(a, lds, base, pa, pb, scalar(a.a.scales + a0 * a.a.sld), scalar(a.b.scales + b0 * a.b.sld), off, soa, sob,
                    nk, wave, lane, acc);
   } else {
 #pragma unroll
