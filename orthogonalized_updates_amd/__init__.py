@@ -614,7 +614,7 @@ class Fp8Matrix:
         """Storage with undefined contents."""
         import torch
         c, s = _fp8_layout(rows, cols, block)
-        dev = device if isinstance(device, torch.device) else torch.device(device or "cuda")
+        dev = device if isinstance(device, torch.device) else torch.device("cuda" if device is None else device)
         if dev.type != "cuda":
             raise ValueError("codes and scales must be on one ROCm GPU")
         # made in its layout, so without __init__'s checks

@@ -928,7 +928,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul_small(MatArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int64_t kCUs = 256;
 // Output tiles of 128 x 128: a launch has fewer than 2^32 threads, and of 64 x 64
-// tiles, which have as many threads each, there are at most 4 times as many.
+// tiles, which have as many threads each, there are at most 4 times as many (the
+// rule takes 16 x 16 tiles at such sizes for up to 32 rows only, 2^21 of them).
 constexpr int64_t kMaxTiles = (1 << 21) - 8;
 
 enum Kind { kDirect, kSmall, kTile, kBig };

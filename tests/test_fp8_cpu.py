@@ -220,3 +220,13 @@ def test_binding_refuses_without_a_gpu():
         mh.Fp8Matrix(codes, scales.view(torch.uint8), (4, 100))
     with pytest.raises(ValueError, match="shape"):
         mh.Fp8Matrix(codes, scales, (4, -1))
+
+
+@pytest.mark.parametrize("device,on", [(0, "cuda:0"), (3, "cuda:3"), (None, "cuda"), ("cuda:1", "cuda:1")])
+def test_empty_takes_the_device_asked_for(monkeypatch, device, on):
+    """Number 0 is the first GPU, not "no device given"."""
+    torch = pytest.importorskip("torch")
+    asked, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda s, dtype, device: asked.append(device) or empty(s, dtype=dtype))
+    mh.Fp8Matrix.empty(4, 100, device=device)
+    assert asked == [torch.device(on)] * 2
