@@ -13,6 +13,8 @@
 // it, rounds once (to nearest, ties to even). The
 // exponent comes from the bits of the maximum a = 1.f * 2^E: 448 = 1.75 * 2^8,
 // so e = E - 8 where 1.f <= 1.75, else E - 7.
+#include <type_traits>
+
 #include "fp8_internal.h"
 
 namespace muonh {
@@ -77,6 +79,51 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// bf16 entries stay in pairs of 16 bits, whose magnitudes order like their
+// bits: one packed instruction for two of a maximum, a scale or a conversion.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pmax(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x05040100);
+}
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302);
+}
+// Two magnitudes with those that are not finite as zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t m) {
+  return ((m & 0xffffu) < 0x7f80u ? m & 0xffffu : 0u) | (m < 0x7f800000u ? m & 0xffff0000u : 0u);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t pmax_dpp(uint32_t v) {
+  return pmax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t pmax_row16(uint32_t v) {  // as max_row16
+  return pmax_dpp<0x140>(pmax_dpp<0x141>(pmax_dpp<0x4E>(pmax_dpp<0xB1>(v))));
+}
+// Two scale bytes, as scale_byte of the magnitudes' 32 bits.
+__device__ __forceinline__ uint32_t scale_bytes2(uint32_t m) {
+  const u16x2 e = (__builtin_bit_cast(u16x2, m) + u16x2{0x1f, 0x1f}) >> u16x2{7, 7};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(e, u16x2{9, 9}) - u16x2{8, 8});
+}
+__device__ __forceinline__ float scale_lo(uint32_t b) { return __uint_as_float(b << 23); }
+__device__ __forceinline__ float scale_hi(uint32_t b) { return __uint_as_float((b << 7) & 0x7f800000u); }
+// The bytes of 8 scales from 4 pairs.
+__device__ __forceinline__ uint2 bytes8(const uint32_t (&b)[4]) {
+  return make_uint2(__builtin_amdgcn_perm(b[1], b[0], 0x06040200), __builtin_amdgcn_perm(b[3], b[2], 0x06040200));
+}
+// 8 entries (4 pairs) over a scale to 8 codes.
+__device__ __forceinline__ uint2 codes8(uint32_t a, uint32_t b, uint32_t c, uint32_t d, float s) {
+  auto two = [&](s16x2 v, uint32_t x, auto hi) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2, x), s, decltype(hi)::value);
+  };
+  const s16x2 x = two(two(s16x2{0, 0}, a, std::false_type{}), b, std::true_type{});
+  const s16x2 y = two(two(s16x2{0, 0}, c, std::false_type{}), d, std::true_type{});
+  return make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
+}
+
 struct Group {
   int64_t rows, cols, src_ld;
   uint32_t first, tiles_c;  // first matrix (grouped launches); tiles per tile row
@@ -92,32 +139,58 @@ struct Args {
   void *codes, *scales, *codes_t, *scales_t;
 };
 
-template <bool BF>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if (BF) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
-  return static_cast<const float*>(p)[i];
-}
 // 8 consecutive entries from i, at any multiple of the entry's size (gfx950
 // takes vector accesses at any address).
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-template <bool BF>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if (BF) {
-    const u32x4_a2 w = *reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(p) + i);
+
+// A thread's 8 x 8 entries: zeros past the matrix.
+__device__ __forceinline__ void load_patch(const float* p, int64_t ld, int64_t r0, int64_t c0, int64_t rows,
+                                           int64_t cols, float (&v)[8][8]) {
+  if (c0 + 8 <= cols) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) {
+      // rows past the end reload the last one, so that no load waits in a branch
+      const int64_t r = r0 + i < rows ? r0 + i : rows - 1;
+      const f32x4_a4* q = reinterpret_cast<const f32x4_a4*>(p + r * ld + c0);
+      const f32x4_a4 a = q[0], b = q[1];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[i][k] = a[k];
+        v[i][4 + k] = b[k];
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i >= rows)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
   } else {
-    const f32x4_a4* q = reinterpret_cast<const f32x4_a4*>(static_cast<const float*>(p) + i);
-    const f32x4_a4 a = q[0], b = q[1];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = a[k];
-      v[4 + k] = b[k];
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = r0 + i < rows && c0 + j < cols ? p[(r0 + i) * ld + c0 + j] : 0.f;
+  }
+}
+__device__ __forceinline__ void load_patch(const uint16_t* p, int64_t ld, int64_t r0, int64_t c0, int64_t rows,
+                                           int64_t cols, u32x4_a2 (&v)[8]) {
+  if (c0 + 8 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + i < rows ? r0 + i : rows - 1;
+      v[i] = *reinterpret_cast<const u32x4_a2*>(p + r * ld + c0);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i >= rows) v[i] = u32x4_a2{0, 0, 0, 0};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        auto at = [&](int64_t c) { return r0 + i < rows && c < cols ? (uint32_t)p[(r0 + i) * ld + c] : 0u; };
+        v[i][j] = at(c0 + 2 * j) | at(c0 + 2 * j + 1) << 16;
+      }
   }
 }
 
@@ -141,7 +214,7 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, i
 template <bool BF, bool TILES, bool PLAIN, bool TRANS>
 __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   __shared__ __attribute__((aligned(16))) uint32_t red[4][kBlock];                                  // maxima by wave
-  __shared__ uint8_t byte_of[2][kBlock];                               // scale bytes of rows, columns
+  __shared__ __attribute__((aligned(8))) uint8_t byte_of[2][kBlock];  // scale bytes of rows, columns
   __shared__ __attribute__((aligned(16))) uint8_t stage[TRANS ? kBlock * kBlock : 16];  // transposed codes
   const uint32_t x = blockIdx.x & 7;
   const uint32_t index = (uint32_t)(((uint64_t)x * a.tiles) >> 3) + (blockIdx.x >> 3);
@@ -163,33 +236,42 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   const int64_t r0 = tr * kBlock + 8 * ty, c0 = tc * kBlock + 8 * tx;
   const int64_t rows = g.rows, cols = g.cols;
 
-  float v[8][8];
-  if (c0 + 8 <= cols) {
+  // fp32: the entries; bf16: pairs of them, and the maxima of the rows' and
+  // columns' magnitudes, pair by pair
+  float v[BF ? 1 : 8][8];
+  u32x4_a2 w[BF ? 8 : 1];
+  uint32_t rmax[8], cmax[4];
+  if constexpr (BF) {
+    load_patch(static_cast<const uint16_t*>(src), g.src_ld, r0, c0, rows, cols, w);
+    auto maxima = [&](auto clean) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // rows past the end reload the last one, so that no load waits in a branch
-      const int64_t r = r0 + i < rows ? r0 + i : rows - 1;
-      load8<BF>(src, r * g.src_ld + c0, v[i]);
-    }
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (r0 + i >= rows)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        for (int d = 0; d < 4; ++d) {
+          uint32_t m = w[i][d] & 0x7fff7fffu;
+          if constexpr (decltype(clean)::value) m = finite2(m);
+          rmax[i] = d ? pmax(rmax[i], m) : m;
+          cmax[d] = i ? pmax(cmax[d], m) : m;
+        }
+    };
+    maxima(std::false_type{});
+    const uint32_t all = pmax(pmax(cmax[0], cmax[1]), pmax(cmax[2], cmax[3]));
+    if (finite2(all) != all) maxima(std::true_type{});
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[i][j] = r0 + i < rows && c0 + j < cols ? load1<BF>(src, (r0 + i) * g.src_ld + c0 + j) : 0.f;
+    load_patch(static_cast<const float*>(src), g.src_ld, r0, c0, rows, cols, v);
   }
 
   float scale = 1.f;  // of the tile
   if (TILES) {
     uint32_t mx = 0;
+    if constexpr (BF) {
+      const uint32_t all = pmax(pmax(cmax[0], cmax[1]), pmax(cmax[2], cmax[3]));
+      mx = umax(all << 16, all & 0xffff0000u);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      mx = umax(mx, amax8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7]));
+      for (int i = 0; i < 8; ++i)
+        mx = umax(mx, amax8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7]));
+    }
     mx = max_row16(mx);
     mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
     mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
@@ -206,11 +288,25 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   if (PLAIN) {
     uint8_t* codes = pick(a.codes);
     const int64_t ld = code_ld(cols);
+    // the 16 threads of a row are the lanes of a DPP row
+    uint32_t pair[4];  // scale bytes of rows 2k, 2k + 1
+    if constexpr (BF && !TILES) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        pair[k] = scale_bytes2(pmax_row16(pmax(low_halves(rmax[2 * k], rmax[2 * k + 1]),
+                                               high_halves(rmax[2 * k], rmax[2 * k + 1]))));
+      if (tx == 0) *reinterpret_cast<uint2*>(&byte_of[0][8 * ty]) = bytes8(pair);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      if constexpr (BF) {
+        const float s = TILES ? scale : i & 1 ? scale_hi(pair[i >> 1]) : scale_lo(pair[i >> 1]);
+        if (r0 + i < rows)
+          *reinterpret_cast<uint2*>(codes + (r0 + i) * ld + c0) = codes8(w[i][0], w[i][1], w[i][2], w[i][3], s);
+        continue;
+      }
       float s = scale;
       if (!TILES) {
-        // the 16 threads of a row are the lanes of a DPP row
         const uint32_t byte = scale_byte(
             max_row16(amax8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7])));
         s = scale_of(byte);
@@ -227,7 +323,30 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
 
   if (TRANS) {
     float s[8];
-    if (!TILES) {
+    if constexpr (BF && !TILES) {
+      // the wave's 4 thread rows: a swap of lane halves brings both halves'
+      // maxima of one pair of columns together, of pair d in the lower lanes
+      // and of d + 2 in the upper ones; then the same with rows of 16 lanes
+      uint32_t h[2];
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const auto p = __builtin_amdgcn_permlane32_swap(cmax[d], cmax[d + 2], false, false);
+        h[d] = pmax(p[0], p[1]);
+      }
+      const auto p = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+      // lane 16 g + tx: pair g of the 4
+      red[wave][4 * tx + (lane >> 4)] = pmax(p[0], p[1]);
+      __syncthreads();
+      uint32_t pair[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int c = 4 * tx + d;
+        pair[d] = scale_bytes2(pmax(pmax(red[0][c], red[1][c]), pmax(red[2][c], red[3][c])));
+        s[2 * d] = scale_lo(pair[d]);
+        s[2 * d + 1] = scale_hi(pair[d]);
+      }
+      if (ty == 0) *reinterpret_cast<uint2*>(&byte_of[1][8 * tx]) = bytes8(pair);
+    } else if (!TILES) {
       uint32_t mx[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -267,8 +386,15 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       uint2 q;
-      q.x = codes4(v[0][j], v[1][j], v[2][j], v[3][j], s[j]);
-      q.y = codes4(v[4][j], v[5][j], v[6][j], v[7][j], s[j]);
+      if constexpr (BF) {
+        auto rows2 = [&](int i) {
+          return j & 1 ? high_halves(w[i][j >> 1], w[i + 1][j >> 1]) : low_halves(w[i][j >> 1], w[i + 1][j >> 1]);
+        };
+        q = codes8(rows2(0), rows2(2), rows2(4), rows2(6), s[j]);
+      } else {
+        q.x = codes4(v[0][j], v[1][j], v[2][j], v[3][j], s[j]);
+        q.y = codes4(v[4][j], v[5][j], v[6][j], v[7][j], s[j]);
+      }
       *reinterpret_cast<uint2*>(stage + (8 * tx + j) * kBlock + ((ty ^ tx) << 3)) = q;
     }
   }
