@@ -210,15 +210,26 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, i
 //
 // Blocks are dealt to the 8 XCDs in turn; each XCD takes a contiguous eighth
 // of the tiles, so that the scale bytes of neighbouring tiles, which share
-// cache lines in both forms, meet in one L2.
+// cache lines in both forms, meet in one L2. XCD x begins x eighths into its
+// part: from the beginning, rows of a power of two bytes put all XCDs on the
+// same memory channels (4096 x 8192 bf16 in both forms 39.1 -> 31.8 us, 8192 x
+// 2048 fp32 26.7 -> 25.1, other sizes +-1 %).
+//
+// Measured with inputs from memory, a copy of as many bytes in parentheses:
+// bf16 in both forms 8192 x 2048 17.7 us (14.6), x 4096 33.1 (27.5), x 14336
+// 103 (91).
 template <bool BF, bool TILES, bool PLAIN, bool TRANS>
 __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   __shared__ __attribute__((aligned(16))) uint32_t red[4][kBlock];                                  // maxima by wave
   __shared__ __attribute__((aligned(8))) uint8_t byte_of[2][kBlock];  // scale bytes of rows, columns
   __shared__ __attribute__((aligned(16))) uint8_t stage[TRANS ? kBlock * kBlock : 16];  // transposed codes
   const uint32_t x = blockIdx.x & 7;
-  const uint32_t index = (uint32_t)(((uint64_t)x * a.tiles) >> 3) + (blockIdx.x >> 3);
-  if (index >= (uint32_t)(((uint64_t)(x + 1) * a.tiles) >> 3)) return;
+  const uint32_t lo = (uint32_t)(((uint64_t)x * a.tiles) >> 3);
+  const uint32_t count = (uint32_t)(((uint64_t)(x + 1) * a.tiles) >> 3) - lo;
+  if ((blockIdx.x >> 3) >= count) return;
+  uint32_t index = (blockIdx.x >> 3) + ((x * count) >> 3);
+  if (index >= count) index -= count;
+  index += lo;
   int gi = 0;
   for (int i = 1; i < a.ngroups; ++i)
     if (index >= a.g[i].begin) gi = i;
