@@ -4,15 +4,13 @@
 //
 // One workgroup takes one 128 x 128 tile of the source, which holds whole
 // blocks of every kind: 128 row groups, 128 column groups (the transposed
-// form's row groups) or one tile. It reads the tile once into registers (16 x 16
-// threads, each an 8 x 8 patch), takes the
-// maxima by lane exchanges and LDS, and writes one or both forms: 4 (fp32) or
-// 2 (bf16) bytes read and 1 or 2 written per entry, HBM-bound.
+// form's row groups) or one tile. It reads the tile once into registers (16 x
+// 16 threads, each an 8 x 8 patch), takes the maxima by lane exchanges and
+// LDS, and writes one or both forms: 4 (fp32) or 2 (bf16) bytes read and 1 or
+// 2 written per entry, HBM-bound.
 //
 // A scale is a power of two, so the conversion instruction, which divides by
-// it, rounds once (to nearest, ties to even). The
-// exponent comes from the bits of the maximum a = 1.f * 2^E: 448 = 1.75 * 2^8,
-// so e = E - 8 where 1.f <= 1.75, else E - 7.
+// it, rounds once (to nearest, ties to even).
 #include <type_traits>
 
 #include "fp8_internal.h"
@@ -26,50 +24,7 @@ constexpr int kMaxGroups = 16;
 // Blocks of one launch: a launch has fewer than 2^32 threads.
 constexpr int64_t kMaxBlocks = (1 << 24) - 8;
 
-// Bits of max |x| over finite entries -> scale byte e + 127, e >= -126.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
-  const int b = (int)((amax_bits + 0x1fffffu) >> 23) - 8;
-  return (uint32_t)(b < 1 ? 1 : b);
-}
-// The scale itself, 2^e: byte in [1, 247], a normal number.
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
-
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
-// Bits of max |x| over the finite ones of 8 values (they order like the
-// values). One v_max3_f32 takes two of them, magnitudes included; only where
-// that meets an infinity or a NaN are the finite ones picked one by one.
-__device__ __forceinline__ float max3(float m, float a, float b) {
-  float r;
-  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(m), "v"(a), "v"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t amax8(float a, float b, float c, float d, float e, float f, float g,
-                                          float h) {
-  uint32_t m = __float_as_uint(max3(max3(max3(max3(0.f, a, b), c, d), e, f), g, h));
-  if (m >= 0x7f800000u) {
-    const float v[8] = {a, b, c, d, e, f, g, h};
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
-      if (u < 0x7f800000u) m = umax(m, u);
-    }
-  }
-  return m;
-}
-
-// Maximum over the 16 lanes of a DPP row, in all of them.
-template <int CTRL>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
-  return umax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ uint32_t max_row16(uint32_t v) {
-  v = max_dpp<0xB1>(v);   // quad [1,0,3,2]
-  v = max_dpp<0x4E>(v);   // quad [2,3,0,1]
-  v = max_dpp<0x141>(v);  // mirrored halves: the other quad of 8
-  return max_dpp<0x140>(v);  // mirrored row: the other 8
-}
 
 // 4 values over a scale 2^e (exact) to 4 codes, the first in the low byte.
 typedef short s16x2 __attribute__((ext_vector_type(2)));
@@ -79,8 +34,11 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// bf16 entries stay in pairs of 16 bits, whose magnitudes order like their
-// bits: one packed instruction for two of a maximum, a scale or a conversion.
+// Magnitudes order like their bits, compared as integers: a floating-point
+// maximum answers a signaling NaN with a NaN and forgets what came before. A
+// scale's exponent depends on the upper 16 bits of the maximum, rounded up, so
+// maxima are handled in pairs of 16 bits, two in one packed instruction, and
+// bf16 entries stay in pairs throughout.
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pmax(uint32_t a, uint32_t b) {
@@ -96,18 +54,29 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t finite2(uint32_t m) {
   return ((m & 0xffffu) < 0x7f80u ? m & 0xffffu : 0u) | (m < 0x7f800000u ? m & 0xffff0000u : 0u);
 }
+// Upper halves of two fp32 magnitudes, rounded up.
+__device__ __forceinline__ uint32_t upper2(uint32_t a, uint32_t b) {
+  return high_halves(a + 0xffffu, b + 0xffffu);
+}
+// Maxima over the 16 lanes of a DPP row, in all of them.
 template <int CTRL>
 __device__ __forceinline__ uint32_t pmax_dpp(uint32_t v) {
   return pmax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ uint32_t pmax_row16(uint32_t v) {  // as max_row16
-  return pmax_dpp<0x140>(pmax_dpp<0x141>(pmax_dpp<0x4E>(pmax_dpp<0xB1>(v))));
+__device__ __forceinline__ uint32_t pmax_row16(uint32_t v) {
+  v = pmax_dpp<0xB1>(v);   // quad [1,0,3,2]
+  v = pmax_dpp<0x4E>(v);   // quad [2,3,0,1]
+  v = pmax_dpp<0x141>(v);  // mirrored halves: the other quad of 8
+  return pmax_dpp<0x140>(v);  // mirrored row: the other 8
 }
-// Two scale bytes, as scale_byte of the magnitudes' 32 bits.
+// Maxima over finite entries -> scale bytes e + 127, e >= -126: with a = 1.f *
+// 2^E and 448 = 1.75 * 2^8, e = E - 8 where 1.f <= 1.75 (0x60 of the 7 bits),
+// else E - 7.
 __device__ __forceinline__ uint32_t scale_bytes2(uint32_t m) {
   const u16x2 e = (__builtin_bit_cast(u16x2, m) + u16x2{0x1f, 0x1f}) >> u16x2{7, 7};
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(e, u16x2{9, 9}) - u16x2{8, 8});
 }
+// The scale 2^e of a pair's byte in [1, 247], a normal number.
 __device__ __forceinline__ float scale_lo(uint32_t b) { return __uint_as_float(b << 23); }
 __device__ __forceinline__ float scale_hi(uint32_t b) { return __uint_as_float((b << 7) & 0x7f800000u); }
 // The bytes of 8 scales from 4 pairs.
@@ -220,7 +189,7 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, i
 // 103 (91).
 template <bool BF, bool TILES, bool PLAIN, bool TRANS>
 __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
-  __shared__ __attribute__((aligned(16))) uint32_t red[4][kBlock];                                  // maxima by wave
+  __shared__ __attribute__((aligned(16))) uint32_t red[4][kBlock / 2];  // maxima by wave
   __shared__ __attribute__((aligned(8))) uint8_t byte_of[2][kBlock];  // scale bytes of rows, columns
   __shared__ __attribute__((aligned(16))) uint8_t stage[TRANS ? kBlock * kBlock : 16];  // transposed codes
   const uint32_t x = blockIdx.x & 7;
@@ -247,94 +216,105 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   const int64_t r0 = tr * kBlock + 8 * ty, c0 = tc * kBlock + 8 * tx;
   const int64_t rows = g.rows, cols = g.cols;
 
-  // fp32: the entries; bf16: pairs of them, and the maxima of the rows' and
-  // columns' magnitudes, pair by pair
+  // the entries (bf16: pairs of them), and the maxima of magnitudes of rows
+  // 2k, 2k + 1 and of columns 2k, 2k + 1
+  constexpr bool kRows = PLAIN && !TILES, kCols = TRANS || TILES;
   float v[BF ? 1 : 8][8];
   u32x4_a2 w[BF ? 8 : 1];
-  uint32_t rmax[8], cmax[4];
+  uint32_t rmax[4], cmax[4];
   if constexpr (BF) {
     load_patch(static_cast<const uint16_t*>(src), g.src_ld, r0, c0, rows, cols, w);
     auto maxima = [&](auto clean) {
+      uint32_t r[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           uint32_t m = w[i][d] & 0x7fff7fffu;
           if constexpr (decltype(clean)::value) m = finite2(m);
-          rmax[i] = d ? pmax(rmax[i], m) : m;
+          r[i] = d ? pmax(r[i], m) : m;
           cmax[d] = i ? pmax(cmax[d], m) : m;
         }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        rmax[k] = pmax(low_halves(r[2 * k], r[2 * k + 1]), high_halves(r[2 * k], r[2 * k + 1]));
     };
     maxima(std::false_type{});
-    const uint32_t all = pmax(pmax(cmax[0], cmax[1]), pmax(cmax[2], cmax[3]));
+    const auto& any = kCols ? cmax : rmax;
+    const uint32_t all = pmax(pmax(any[0], any[1]), pmax(any[2], any[3]));
     if (finite2(all) != all) maxima(std::true_type{});
   } else {
     load_patch(static_cast<const float*>(src), g.src_ld, r0, c0, rows, cols, v);
+    uint32_t r[8], c[8];
+    auto maxima = [&](auto clean) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t m = __float_as_uint(v[i][j]);
+          // computed anew in the rare second pass, not kept for it in registers
+          if constexpr (decltype(clean)::value) asm("" : "+v"(m));
+          m &= 0x7fffffffu;
+          if constexpr (decltype(clean)::value) m = m < 0x7f800000u ? m : 0u;
+          r[i] = j ? umax(r[i], m) : m;
+          c[j] = i ? umax(c[j], m) : m;
+        }
+    };
+    maxima(std::false_type{});
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all = umax(all, kCols ? c[i] : r[i]);
+    if (all >= 0x7f800000u) maxima(std::true_type{});
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      rmax[k] = upper2(r[2 * k], r[2 * k + 1]);
+      cmax[k] = upper2(c[2 * k], c[2 * k + 1]);
+    }
   }
 
   float scale = 1.f;  // of the tile
-  if (TILES) {
-    uint32_t mx = 0;
-    if constexpr (BF) {
-      const uint32_t all = pmax(pmax(cmax[0], cmax[1]), pmax(cmax[2], cmax[3]));
-      mx = umax(all << 16, all & 0xffff0000u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        mx = umax(mx, amax8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7]));
-    }
-    mx = max_row16(mx);
-    mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
-    mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
+  if constexpr (TILES) {
+    uint32_t mx = pmax_row16(pmax(pmax(cmax[0], cmax[1]), pmax(cmax[2], cmax[3])));
+    mx = pmax(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
+    mx = pmax(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
     if (lane == 0) red[0][wave] = mx;
     __syncthreads();
-    const uint32_t byte = scale_byte(umax(umax(red[0][0], red[0][1]), umax(red[0][2], red[0][3])));
-    scale = scale_of(byte);
+    mx = pmax(pmax(red[0][0], red[0][1]), pmax(red[0][2], red[0][3]));
+    const uint32_t byte = scale_bytes2(pmax(mx, mx >> 16)) & 0xffffu;
+    scale = scale_lo(byte);
     if (tid == 0) {
       if (PLAIN) put_scale(pick(a.scales), tr, tc, cols, byte);
       if (TRANS) put_scale(pick(a.scales_t), tc, tr, rows, byte);
     }
   }
 
-  if (PLAIN) {
+  if constexpr (PLAIN) {
     uint8_t* codes = pick(a.codes);
     const int64_t ld = code_ld(cols);
-    // the 16 threads of a row are the lanes of a DPP row
     uint32_t pair[4];  // scale bytes of rows 2k, 2k + 1
-    if constexpr (BF && !TILES) {
+    if constexpr (kRows) {
+      // the 16 threads of a row are the lanes of a DPP row
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        pair[k] = scale_bytes2(pmax_row16(pmax(low_halves(rmax[2 * k], rmax[2 * k + 1]),
-                                               high_halves(rmax[2 * k], rmax[2 * k + 1]))));
+      for (int k = 0; k < 4; ++k) pair[k] = scale_bytes2(pmax_row16(rmax[k]));
       if (tx == 0) *reinterpret_cast<uint2*>(&byte_of[0][8 * ty]) = bytes8(pair);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      const float s = TILES ? scale : i & 1 ? scale_hi(pair[i >> 1]) : scale_lo(pair[i >> 1]);
+      uint2 q;
       if constexpr (BF) {
-        const float s = TILES ? scale : i & 1 ? scale_hi(pair[i >> 1]) : scale_lo(pair[i >> 1]);
-        if (r0 + i < rows)
-          *reinterpret_cast<uint2*>(codes + (r0 + i) * ld + c0) = codes8(w[i][0], w[i][1], w[i][2], w[i][3], s);
-        continue;
-      }
-      float s = scale;
-      if (!TILES) {
-        const uint32_t byte = scale_byte(
-            max_row16(amax8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7])));
-        s = scale_of(byte);
-        if (tx == 0) byte_of[0][8 * ty + i] = (uint8_t)byte;
-      }
-      if (r0 + i < rows) {
-        uint2 q;
+        q = codes8(w[i][0], w[i][1], w[i][2], w[i][3], s);
+      } else {
         q.x = codes4(v[i][0], v[i][1], v[i][2], v[i][3], s);
         q.y = codes4(v[i][4], v[i][5], v[i][6], v[i][7], s);
-        *reinterpret_cast<uint2*>(codes + (r0 + i) * ld + c0) = q;
       }
+      if (r0 + i < rows) *reinterpret_cast<uint2*>(codes + (r0 + i) * ld + c0) = q;
     }
   }
 
-  if (TRANS) {
+  if constexpr (TRANS) {
     float s[8];
-    if constexpr (BF && !TILES) {
+    if constexpr (!TILES) {
       // the wave's 4 thread rows: a swap of lane halves brings both halves'
       // maxima of one pair of columns together, of pair d in the lower lanes
       // and of d + 2 in the upper ones; then the same with rows of 16 lanes
@@ -357,36 +337,6 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
         s[2 * d + 1] = scale_hi(pair[d]);
       }
       if (ty == 0) *reinterpret_cast<uint2*>(&byte_of[1][8 * tx]) = bytes8(pair);
-    } else if (!TILES) {
-      uint32_t mx[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        mx[j] = amax8(v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]);
-      // The wave's 4 thread rows: a swap of lane halves brings both halves'
-      // maxima of one column together, of column j in the lower lanes and of
-      // j + 4 in the upper ones; then the same with rows of 16 lanes.
-      uint32_t h[4], w[2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const auto p = __builtin_amdgcn_permlane32_swap(mx[j], mx[j + 4], false, false);
-        h[j] = umax(p[0], p[1]);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const auto p = __builtin_amdgcn_permlane16_swap(h[j], h[j + 2], false, false);
-        w[j] = umax(p[0], p[1]);
-      }
-      // lane 16 g + tx: columns 8 tx + 4 (g / 2) + 2 (g % 2) + {0, 1}
-      const int g = lane >> 4;
-      *reinterpret_cast<uint2*>(&red[wave][8 * tx + 4 * (g >> 1) + 2 * (g & 1)]) = make_uint2(w[0], w[1]);
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = 8 * tx + j;
-        const uint32_t byte = scale_byte(umax(umax(red[0][c], red[1][c]), umax(red[2][c], red[3][c])));
-        s[j] = scale_of(byte);
-        if (ty == 0) byte_of[1][c] = (uint8_t)byte;
-      }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] = scale;

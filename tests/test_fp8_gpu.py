@@ -106,6 +106,27 @@ def test_quantize_is_the_definition(rows, cols, dtype, block):
                     assert torch.equal(o.scales.view(torch.uint8), ref.scales.view(torch.uint8))
 
 
+@pytest.mark.parametrize("block", ["rows", "tiles"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_quantize_of_every_kind_of_nan(dtype, block):
+    """Quiet and signaling NaNs of either sign anywhere: NaN codes, and the
+    largest finite entry still counts, whatever stands before or after it."""
+    kinds = [0x7f800001, 0x7fbfffff, 0x7fc00000, 0x7fffffff] if dtype == "fp32" else [0x7f81, 0x7fbf, 0x7fc0, 0x7fff]
+    sign, idt = (1 << 31, torch.int32) if dtype == "fp32" else (1 << 15, torch.int16)
+    rng = np.random.default_rng(31)
+    x = values(200, 264, 9, dtype)
+    bits = x.view(idt).cpu().numpy()
+    pick = rng.choice(np.array(kinds + [k | sign for k in kinds], np.uint64), bits.shape)
+    hit = rng.random(bits.shape) < rng.choice([0.01, 0.2, 0.6], (200, 1))
+    bits = np.where(hit, pick, bits.view(np.uint32 if dtype == "fp32" else np.uint16)).astype(
+        np.uint32 if dtype == "fp32" else np.uint16)
+    x = torch.from_numpy(bits.view(np.int32 if dtype == "fp32" else np.int16)).cuda().view(DT[dtype])
+    x64 = np.where(hit, np.nan, values(200, 264, 9, dtype).double().cpu().numpy())
+    q, qt = mh().fp8_quantize(x, block=block, forms="both")
+    check_matrix(q, x64, block)
+    check_matrix(qt, x64.T, block)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("ld,first", [(512, 0), (520, 8), (303, 0), (301, 1), (1024, 3)])
 def test_quantize_of_strided_rows(ld, first, dtype):
