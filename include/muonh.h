@@ -346,7 +346,8 @@ int muonh_check_disjoint(const muonh_plan* plan, const void* const* W, const voi
  * matrix rows (TILES), muonh_fp8_scale_ld(cols) = ceil(cols/128) rounded up
  * to a multiple of 4 bytes per row, zeros past ceil(cols/128). codes 16-byte,
  * scales 4-byte aligned. The quantizing calls write all of it; an operand
- * of muonh_fp8_matmul from elsewhere needs the zeros and scale bytes in [1, 254]. Matrices without rows or columns are allowed.
+ * of muonh_fp8_matmul from elsewhere needs the zeros and scale bytes in
+ * [1, 254]. Matrices without rows or columns are allowed.
  */
 enum { MUONH_FP8_ROWS = 0, MUONH_FP8_TILES = 1 };
 enum { MUONH_DT_FP32 = 0, MUONH_DT_BF16 = 1 };
@@ -375,9 +376,9 @@ int64_t muonh_fp8_scale_rows(int64_t rows, int32_t block);
  * tokens); with MUONH_FP8_TILES they hold the same values. One pass over
  * src. Deterministic; asynchronous on `stream`, capturable.
  * Errors: MUONH_EINVAL (NULL or half-given pair, bad dtype or block, src_ld <
- * cols or above 2^36, misaligned output), MUONH_ESHAPE (a dim out of range, or 2^24 tiles
- * of 128 x 128 or more), MUONH_EALIAS (an output overlaps src or another
- * output), MUONH_EHIP.
+ * cols or above 2^36, misaligned output), MUONH_ESHAPE (a dim out of range, or
+ * 2^24 tiles of 128 x 128 or more), MUONH_EALIAS (an output overlaps src or
+ * another output), MUONH_EHIP.
  */
 int muonh_fp8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t src_ld,
                        int32_t block, void* codes, void* scales, void* codes_t, void* scales_t,

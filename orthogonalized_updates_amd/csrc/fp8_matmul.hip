@@ -252,7 +252,8 @@ __device__ __forceinline__ void store_rows(const MatArgs& a, int64_t i0, int64_t
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             old[f][h] = *reinterpret_cast<const u32x4_a2*>(
-                static_cast<const __bf16*>(a.out) + min(i0 + 16 * (f0 + f) + r16, a.m - 1) * a.ldo + j0 + 32 * h + 8 * g);
+                static_cast<const __bf16*>(a.out) + min(i0 + 16 * (f0 + f) + r16, a.m - 1) * a.ldo + j0 +
+                32 * h + 8 * g);
       }
 #pragma unroll
       for (int f = 0; f < kGroup; ++f) {
@@ -329,7 +330,8 @@ __device__ __forceinline__ void stage_barrier() {
 // may compute uniform values in vector registers, which the DMA's base cannot be).
 __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
   const uint64_t u = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
   return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
 }
 
@@ -512,6 +514,8 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
 // fill the chip better: 6144 x 2048 x 8192, 192 tiles or 256 for 256 CUs, takes
 // 139 instead of 154 us with fp32 and 78 instead of 80.5 with bf16 results
 // (fewer active CUs clock higher). 256 x 192 tiles gained 3-7 % there.
+// 8192^3 takes 374 us with bf16 results (2940 TFLOP/s) and 721 with fp32
+// (1525): power is what bounds both (about 2 GHz).
 //
 // The waves form two groups of 4, one wave of each per SIMD, that take turns
 // phase by phase: one group's 16 MFMAs run while the other reads LDS and
@@ -541,8 +545,8 @@ constexpr int kBigScales = 2 * kB * 4;         // a's rows, then b's: 4 k blocks
 template <typename T, bool WIDE, int FA, int G>
 __device__ __forceinline__ void big_loop(const MatArgs& a, const char* lds, uint32_t base, const uint8_t* pa,
                                          const uint8_t* pb, const uint8_t* sca, const uint8_t* scb,
-                                         const uint32_t (&off)[10], uint32_t soa, uint32_t sob, int nk, int wave, int lane,
-                                         f32x4 (&acc)[4][2 * FA]) {
+                                         const uint32_t (&off)[10], uint32_t soa, uint32_t sob, int nk,
+                                         int wave, int lane, f32x4 (&acc)[4][2 * FA]) {
   const int w4 = wave & 3, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kBlock + ((g ^ (r16 & 7)) << 4);
   i32x8 fa[FA], fb[4];
@@ -704,8 +708,8 @@ __global__ __launch_bounds__(512, 2) void k_matmul_big(MatArgs a) {
     const int64_t a0 = ra >> a.a.sshift, b0 = rb >> a.b.sshift;
     const uint32_t soa = (uint32_t)((r >> a.a.sshift) - a0) * (uint32_t)a.a.sld;
     const uint32_t sob = (uint32_t)((c >> a.b.sshift) - b0) * (uint32_t)a.b.sld;
-    big_loop<T, WIDE, FA, 0>(a, lds, base, pa, pb, scalar(a.a.scales + a0 * a.a.sld), scalar(a.b.scales + b0 * a.b.sld), off, soa, sob,
-                   nk, wave, lane, acc);
+    big_loop<T, WIDE, FA, 0>(a, lds, base, pa, pb, scalar(a.a.scales + a0 * a.a.sld),
+                             scalar(a.b.scales + b0 * a.b.sld), off, soa, sob, nk, wave, lane, acc);
   } else {
 #pragma unroll
     for (int q = 0; q < 6; ++q) off[q] = q < 3 ? off_b(20 + 3 * w4 + q) : off_a(3 * w4 + q - 3);

@@ -42,7 +42,8 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pmax(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+  return __builtin_bit_cast(
+      uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x05040100);
