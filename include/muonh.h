@@ -351,6 +351,9 @@ int muonh_check_disjoint(const muonh_plan* plan, const void* const* W, const voi
  */
 enum { MUONH_FP8_ROWS = 0, MUONH_FP8_TILES = 1 };
 enum { MUONH_DT_FP32 = 0, MUONH_DT_BF16 = 1 };
+/* In muonh_fp8_matmul's out_dtype beside MUONH_DT_BF16: 8-bit matrix
+ * instructions, twice the rate, with sums of fewer bits than fp32. */
+enum { MUONH_FP8_FAST = 256 };
 #define MUONH_MAX_FP8_DIM (1 << 24) /* rows and cols of a block-scaled matrix */
 
 typedef struct {
@@ -409,13 +412,15 @@ int muonh_fp8_weights(const muonh_plan* plan, const float* const* W, void* const
  *   dX = matmul(dY, W^T)        dY rows; W's transposed tiles
  *   dW = matmul(dY^T, X^T)      transposed rows forms (grouped along tokens);
  *                               fp32 or bf16 G with accumulate: micro-batches
- * k = 0 gives zeros (or leaves out as it is). Sums are fp32; the result is
- * rounded once to out_dtype. bf16 results use the 8-bit matrix instructions,
- * which drop product bits below 2^-13 of the largest of a few products they
- * add at once: about 2e-5 relative error, far below bf16's 2^-9. fp32 results
- * use bf16 matrix instructions on the widened codes, exact up to the fp32
- * sums (about 1e-6; entries under 2^-117 in magnitude may lose bits), at
- * half the rate. NaN codes give NaN in their row or column of out.
+ * k = 0 gives zeros (or leaves out as it is). out_dtype: MUONH_DT_FP32 or
+ * MUONH_DT_BF16. Products of the codes are exact and their sums are fp32 (bf16
+ * matrix instructions on the widened codes; entries under 2^-117 in magnitude
+ * may lose bits); the result is rounded once to out_dtype. With
+ * MUONH_DT_BF16 | MUONH_FP8_FAST, 8-bit matrix instructions multiply at twice
+ * the rate: of the products that one of them adds at once (at most 16) they
+ * drop the bits below 2^-13 of the largest, so beside fp32 sums a result is
+ * off by up to 15 * 2^-13 * sum_k |a[i][k] * b[j][k]|, however small it is
+ * itself, before it is rounded. NaN codes give NaN in their row or column of out.
  * The result does not depend on out_ld or alignment, and is deterministic.
  * workspace: DEVICE, 256-byte aligned, of at least
  * muonh_fp8_matmul_workspace_bytes(m, n, k, out_dtype) bytes (NULL if that is

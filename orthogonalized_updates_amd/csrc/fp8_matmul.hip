@@ -9,13 +9,14 @@
 // (any assignment of k to lanes is right as long as both operands use the
 // same one; this one reads LDS without bank conflicts, see frag_off).
 //
-// bf16 results take that path. Within one instruction the 8-bit products are
-// added in groups whose terms keep no bits below 2^-13 of the largest
-// (measured: 1.4-1.6e-5 relative error on normal data, 5e-5 on codes spread
-// over the whole format, independent of k). fp32 results must not carry
-// that, so they widen the codes to bf16 with their scale applied (exact) and
-// use v_mfma_f32_16x16x32_bf16, whose sums are accurate to fp32 (measured 1e-7
-// at k = 8192), at half the matrix rate.
+// Within one such instruction, though, the products are added in groups whose
+// terms keep no bits below 2^-13 of the largest: small products beside a large
+// one are lost, and where large ones cancel, nothing of the result need be
+// left (fp32 sums of the same codes have a 2^-24 there). So products widen the
+// codes to bf16 with their scale applied (exact) and use
+// v_mfma_f32_16x16x32_bf16, whose sums are accurate to fp32 (measured 1e-7 at
+// k = 8192), at half the matrix rate, for either result type. The 8-bit
+// instructions serve callers that ask for them (MUONH_FP8_FAST).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -356,8 +357,8 @@ __device__ __forceinline__ void dma4s(const uint8_t* base, uint32_t off, uint32_
 // consecutive columns of one row of out. For 2-byte results b's rows are
 // also dealt to the fragments so that a lane holds 8 consecutive columns in
 // two neighbouring fragments (b_row): 16-byte stores, 64-byte runs per row,
-// which lane pairs join to runs of 128 (pair_rows; 8192 x 6144 x 128 with bf16
-// results 26.8 -> 24.7 us, 8192 x 6144 x 2048 95 -> 90).
+// which lane pairs join to runs of 128 (pair_rows; on the 8-bit path 8192 x
+// 6144 x 128 with bf16 results 26.8 -> 24.7 us, 8192 x 6144 x 2048 95 -> 90).
 //
 // 128 x 128 tiles, a ring of 4 LDS stages of one k block (32 KB each). The 8
 // waves form two groups of 4 (2 x 2, wave tile 64 x 64), one wave of each per
@@ -512,10 +513,10 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
 // k block (2 x 64 KB): products with enough tiles for the chip. 192 x 256
 // tiles (FA = 3 instead of 4 fragments of a per half wave tile) where they
 // fill the chip better: 6144 x 2048 x 8192, 192 tiles or 256 for 256 CUs, takes
-// 139 instead of 154 us with fp32 and 78 instead of 80.5 with bf16 results
-// (fewer active CUs clock higher). 256 x 192 tiles gained 3-7 % there.
-// 8192^3 takes 374 us with bf16 results (2940 TFLOP/s) and 721 with fp32
-// (1525): power is what bounds both (about 2 GHz).
+// 139 instead of 154 us with fp32 results and 78 instead of 80.5 on the 8-bit
+// path (fewer active CUs clock higher). 256 x 192 tiles gained 3-7 % there.
+// 8192^3 takes 374 us on the 8-bit path (2940 TFLOP/s) and 721 with fp32
+// results (1525): power is what bounds both (about 2 GHz).
 //
 // The waves form two groups of 4, one wave of each per SIMD, that take turns
 // phase by phase: one group's 16 MFMAs run while the other reads LDS and
@@ -948,7 +949,8 @@ struct Choice {
 // then rounds of one tile per CU, each a fixed part (first loads, last stores)
 // and a part per block, which is less where a round leaves CUs idle (power,
 // cache bandwidth). Fitted to times of 130 random products up to 12288 x 8192 x
-// 12288 with either result type: off by 6 (64-tiles) to 14 % (256-tiles); the
+// 12288 on the 8-bit path and, widened, with fp32 results (bf16 results of the
+// same products store half the bytes): off by 6 (64-tiles) to 14 % (256-tiles); the
 // kernel taken is on average 0.7 % slower than the fastest, 24 % at worst.
 struct Cost {
   double fixed, block;
@@ -965,13 +967,12 @@ double estimate(const Cost& c, int64_t tiles, double nkb) {
 // 512x2048x2048: 39, 7.7, 11, 24; 1024x4096x4096: -, 37, 21, 43;
 // 6144x2048x8192: -, 192, 107, 81 (192 x 256: 78); 8192x6144x2048: -, -, 122,
 // 90 (192 x 256: 106).
-Choice choose(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
+Choice choose(int64_t m, int64_t n, int64_t k, bool wide) {
   const int64_t nkb = ceil_div(k, kBlock);
   auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };
   Choice c{kSmall, kS, kS, 1, (int)nkb, 0};
   if (m == 0 || n == 0) return c;
   if (nkb == 0) return Choice{kTile, kT, kT, 1, 0, 0};  // zeros; that kernel's loop may be empty
-  const bool wide = out_dtype == MUONH_DT_FP32;
   const Cost small = wide ? Cost{3.1, 0.261} : Cost{2.7, 0.204};
   double best = 0;
   // 64 x 64, the k blocks split over up to 16 workgroups where tiles are few:
@@ -1058,7 +1059,7 @@ extern "C" {
 size_t muonh_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
   using namespace muonh::fp8;
   if (bad_dim(m) || bad_dim(n) || bad_dim(k) || m == 0 || n == 0) return 0;
-  return choose(m, n, k, out_dtype).ws_bytes;
+  return choose(m, n, k, !(out_dtype & MUONH_FP8_FAST)).ws_bytes;
 }
 
 int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* out,
@@ -1070,19 +1071,22 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   if (const int err = check_operand("b", b)) return err;
   if (a->cols != b->cols)
     return fail(MUONH_ESHAPE, "a has %lld columns, b %lld", (long long)a->cols, (long long)b->cols);
-  if (out_dtype != MUONH_DT_FP32 && out_dtype != MUONH_DT_BF16)
-    return fail(MUONH_EINVAL, "out_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", out_dtype);
+  const bool fast = out_dtype == (MUONH_DT_BF16 | MUONH_FP8_FAST);
+  if (out_dtype != MUONH_DT_FP32 && out_dtype != MUONH_DT_BF16 && !fast)
+    return fail(MUONH_EINVAL, "out_dtype=%d is none of MUONH_DT_FP32, MUONH_DT_BF16, MUONH_DT_BF16|MUONH_FP8_FAST",
+                out_dtype);
+  const bool bf16 = out_dtype != MUONH_DT_FP32;
   const int64_t m = a->rows, n = b->rows, k = a->cols;
   if (out_ld < n || out_ld > (1LL << 36))
     return fail(MUONH_EINVAL, "out_ld=%lld out of [n=%lld, 2^36]", (long long)out_ld, (long long)n);
   if (m == 0 || n == 0) return MUONH_OK;
   if (!out) return fail(MUONH_EINVAL, "out is NULL");
-  const int esize = out_dtype == MUONH_DT_BF16 ? 2 : 4;
+  const int esize = bf16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(out) & (uintptr_t)(esize - 1))
     return fail(MUONH_EINVAL, "out is not aligned to its type");
   if (ceil_div(m, kT) * ceil_div(n, kT) > kMaxTiles)
     return fail(MUONH_ESHAPE, "2^21 output tiles of 128 x 128 or more");
-  const Choice c = choose(m, n, k, out_dtype);
+  const Choice c = choose(m, n, k, !fast);
   if (c.ws_bytes) {
     if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the product needs %zu bytes", c.ws_bytes);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -1110,7 +1114,7 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   x.out = out;
   x.ldo = out_ld;
   x.accumulate = accumulate != 0;
-  x.odd = out_dtype == MUONH_DT_BF16 && ((reinterpret_cast<uintptr_t>(out) & 2) != 0 || (out_ld & 1) != 0);
+  x.odd = bf16 && ((reinterpret_cast<uintptr_t>(out) & 2) != 0 || (out_ld & 1) != 0);
   x.splits = c.splits;
   x.per = c.per;
   x.pld = ceil_div(n, 4) * 4;
@@ -1118,7 +1122,8 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
   x.tm = (int)ceil_div(m, c.em);
   x.tn = (int)ceil_div(n, c.en);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return out_dtype == MUONH_DT_BF16 ? launch<__bf16, false>(x, c, s) : launch<float, true>(x, c, s);
+  if (fast) return launch<__bf16, false>(x, c, s);
+  return bf16 ? launch<__bf16, true>(x, c, s) : launch<float, true>(x, c, s);
 }
 
 }  // extern "C"

@@ -230,3 +230,15 @@ def test_empty_takes_the_device_asked_for(monkeypatch, device, on):
     monkeypatch.setattr(torch, "empty", lambda s, dtype, device: asked.append(device) or empty(s, dtype=dtype))
     mh.Fp8Matrix.empty(4, 100, device=device)
     assert asked == [torch.device(on)] * 2
+
+
+def test_matmul_takes_fast_for_bf16_results_only():
+    assert f"MUONH_FP8_FAST = {mh.MUONH_FP8_FAST}" in mh.HEADER_PATH.read_text()
+    fast = mh.MUONH_FP8_FAST
+    for dt in (mh.MUONH_DT_FP32 | fast, fast | 2, 2 * fast | mh.MUONH_DT_BF16, -1):
+        assert _matmul(dt=dt) == mh.MUONH_EINVAL
+    assert _matmul(dt=mh.MUONH_DT_BF16 | fast, ld=299) == mh.MUONH_EINVAL  # past the type's check
+    assert "out_ld" in mh.lib.muonh_last_error().decode()
+    need = mh.lib.muonh_fp8_matmul_workspace_bytes(200, 300, 8192, mh.MUONH_DT_BF16 | fast)
+    a, b = _desc(rows=200, cols=8192), _desc(3 * A, 4 * A, 300, 8192)
+    assert need > 0 and _matmul(a, b, dt=mh.MUONH_DT_BF16 | fast, ws=6 * A, nbytes=need - 1) == mh.MUONH_EWORKSPACE
