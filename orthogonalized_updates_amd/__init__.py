@@ -468,6 +468,9 @@ class MuonH:
                     raise MuonHAliasError("a tensor of the call overlaps the Fp8Weights set")
 
     def _quantize(self, weights, out) -> None:
+        # the launch reads the set's pointer arrays and writes its matrices,
+        # perhaps on another stream than the one they were made on
+        out.memory.record_stream(self.torch.cuda.current_stream(self.device))
         _on_device(self.torch, self.device, get_lib().muonh_fp8_weights, self.plan.handle,
                    self._ptr_array("W", weights), *out.arrays)
 
@@ -638,9 +641,11 @@ class Fp8Matrix:
 class Fp8Weights:
     """The weights of a MuonH optimizer in 8 bits (MuonH.fp8_weights): lists
     of Fp8Matrix with block "tiles" in the caller's order, `weights` and
-    `transposed` (empty without transposed forms), in one allocation. The set
-    keeps the device pointer arrays of its parts (`order`: matrices in plan
-    order), so a captured graph that writes it needs nothing else alive."""
+    `transposed` (empty without transposed forms). They and the device arrays
+    of pointers to their parts (`order`: matrices in plan order) share one
+    allocation, which any of the matrices keeps alive, and every call that
+    writes the set records its stream on it. A captured graph that does must
+    not outlive all of them, nor the optimizer."""
 
     def __init__(self, shapes, device, transposed: bool, order: Sequence[int]):
         import torch
@@ -659,21 +664,26 @@ class Fp8Weights:
                     at.append((total, h, w))
                     total = _up(total + h * w, 256)
                 places.append((shape, to, at))
-        self.storage = torch.empty(total, dtype=torch.uint8, device=device)
+        parts = ("codes", "scales")
+        sets = 2 if transposed else 1
+        nptrs = len(parts) * sets * len(self.order)
+        self.memory = torch.empty(total + 8 * nptrs, dtype=torch.uint8, device=device)
+        self.storage = self.memory[:total]  # codes and scales; the pointers follow
         for shape, to, at in places:
-            parts = [self.storage[o:o + h * w].view(dt).view(h, w)
-                     for (o, h, w), dt in zip(at, (torch.float8_e4m3fn, torch.float8_e8m0fnu))]
-            to.append(Fp8Matrix(*parts, shape, "tiles"))
-        self._ptrs = [torch.tensor([getattr(ms[i], part).data_ptr() for i in self.order],
-                                   dtype=torch.int64, device=device) if ms else None
-                      for ms in (self.weights, self.transposed) for part in ("codes", "scales")]
+            held = [self.storage[o:o + h * w].view(dt).view(h, w)
+                    for (o, h, w), dt in zip(at, (torch.float8_e4m3fn, torch.float8_e8m0fnu))]
+            to.append(Fp8Matrix(*held, shape, "tiles"))
+        ptrs = [getattr(ms[i], part).data_ptr() for ms in (self.weights, self.transposed)[:sets] for part in parts
+                for i in self.order]
+        self.memory[total:].view(torch.int64).copy_(torch.tensor(ptrs, dtype=torch.int64))
         # codes, scales, codes_t, scales_t of muonh_fp8_weights
-        self.arrays = [None if t is None else t.data_ptr() for t in self._ptrs]
+        at = int(self.memory.data_ptr()) + total
+        self.arrays = [at + 8 * len(self.order) * i if i < len(parts) * sets else None for i in range(4)]
 
     @property
     def span(self) -> Tuple[int, int]:
-        p = int(self.storage.data_ptr())
-        return p, p + self.storage.numel()
+        p = int(self.memory.data_ptr())
+        return p, p + self.memory.numel()
 
 
 def _fp8_dt(torch, dtype) -> int:
