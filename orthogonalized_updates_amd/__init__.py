@@ -597,9 +597,29 @@ class Fp8Matrix:
     codes: torch.float8_e4m3fn, rows x (cols rounded up to 128), zeros past
     cols; scales: torch.float8_e8m0fnu, (rows, or rows/128 rounded up) x
     (cols/128 rounded up, then to a multiple of 4). Both contiguous, on one
-    GPU. shape: (rows, cols).
+    GPU. shape: (rows, cols). The attributes are read-only, since `desc` holds
+    the tensors' addresses: write into codes and scales, or make another
+    Fp8Matrix. A matrix whose tensors were moved or resized in place is
+    refused by the calls that take it.
     """
     __slots__ = ("codes", "scales", "shape", "block", "device", "desc")
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"Fp8Matrix.{name} is read-only; make another Fp8Matrix")
+
+    __delattr__ = functools.partialmethod(__setattr__, value=None)
+
+    def _set(self, codes, scales, shape, block) -> None:
+        put = object.__setattr__
+        put(self, "codes", codes)
+        put(self, "scales", scales)
+        put(self, "shape", shape)
+        put(self, "block", block)
+        put(self, "device", codes.device)
+        put(self, "desc", Fp8Desc(codes.data_ptr(), scales.data_ptr(), shape[0], shape[1], FP8_BLOCKS[block]))
+
+    def __reduce__(self):  # copies and pickles take the addresses of their own tensors
+        return Fp8Matrix, (self.codes, self.scales, self.shape, self.block)
 
     def __init__(self, codes, scales, shape: Tuple[int, int], block: str = "rows"):
         import torch
@@ -609,9 +629,7 @@ class Fp8Matrix:
         _check_part("scales", scales, torch.float8_e8m0fnu, e)
         if codes.device != scales.device or codes.device.type != "cuda":
             raise ValueError("codes and scales must be on one ROCm GPU")
-        self.codes, self.scales, self.shape, self.block = codes, scales, (rows, cols), block
-        self.device = codes.device
-        self.desc = Fp8Desc(codes.data_ptr(), scales.data_ptr(), rows, cols, FP8_BLOCKS[block])
+        self._set(codes, scales, (rows, cols), block)
 
     @classmethod
     def empty(cls, rows: int, cols: int, block: str = "rows", device=None) -> "Fp8Matrix":
@@ -623,10 +641,8 @@ class Fp8Matrix:
             raise ValueError("codes and scales must be on one ROCm GPU")
         # made in its layout, so without __init__'s checks
         m = cls.__new__(cls)
-        m.codes = torch.empty(c, dtype=torch.float8_e4m3fn, device=dev)
-        m.scales = torch.empty(s, dtype=torch.float8_e8m0fnu, device=dev)
-        m.shape, m.block, m.device = (rows, cols), block, m.codes.device
-        m.desc = Fp8Desc(m.codes.data_ptr(), m.scales.data_ptr(), rows, cols, FP8_BLOCKS[block])
+        m._set(torch.empty(c, dtype=torch.float8_e4m3fn, device=dev),
+               torch.empty(s, dtype=torch.float8_e8m0fnu, device=dev), (rows, cols), block)
         return m
 
     def dequantize(self):
@@ -636,6 +652,14 @@ class Fp8Matrix:
         if self.block == "tiles":
             s = s.repeat_interleave(FP8_BLOCK, 0)[:rows]
         return self.codes[:, :cols].float() * s.repeat_interleave(FP8_BLOCK, 1)[:, :cols]
+
+
+def _held(name: str, m: Fp8Matrix) -> Fp8Desc:
+    """m's descriptor, if its tensors are where they were."""
+    d = m.desc
+    if m.codes.data_ptr() != (d.codes or 0) or m.scales.data_ptr() != (d.scales or 0):
+        raise ValueError(f"{name}'s codes or scales were moved since the Fp8Matrix was made")
+    return d
 
 
 class Fp8Weights:
@@ -763,6 +787,7 @@ def _form(name: str, o, wanted: bool, rows: int, cols: int, block: str, dev):
         raise TypeError(f"{name} must be an Fp8Matrix")
     if o.shape != (rows, cols) or o.block != block or o.device != dev:
         raise ValueError(f"{name} must be a {(rows, cols)} Fp8Matrix of block {block!r} on {dev}")
+    _held(name, o)
     return o
 
 
@@ -785,6 +810,7 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     for name, m in (("a", a), ("b", b)):
         if not isinstance(m, Fp8Matrix):
             raise TypeError(f"{name} must be an Fp8Matrix")
+    da, db = _held("a", a), _held("b", b)
     dev = a.device
     if dev != b.device:
         raise ValueError(f"a is on {dev}, b on {b.device}")
@@ -815,6 +841,6 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     # from torch's allocator on the current stream: calls on other streams and
     # captured graphs get memory of their own
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    _on_device(torch, dev, lib.muonh_fp8_matmul, a.desc, b.desc, out.data_ptr(), dt, ld,
+    _on_device(torch, dev, lib.muonh_fp8_matmul, da, db, out.data_ptr(), dt, ld,
                1 if accumulate else 0, None if ws is None else ws.data_ptr(), nbytes)
     return out

@@ -64,3 +64,54 @@ def test_every_quantization_records_its_stream(monkeypatch):
     monkeypatch.setattr(mh, "_on_device", lambda t, dev, fn, *args: log.append(("launch", dev, args)))
     opt._quantize([], out)
     assert log == [("record", (stream, "cuda:1")), ("launch", "cuda:1", (11, 12, 1, 2, 3, 4))]
+
+
+@pytest.fixture
+def matrix(monkeypatch):
+    """An Fp8Matrix on host memory."""
+    empty = torch.empty
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty", lambda s, dtype, device: empty(s, dtype=dtype))
+        q = mh.Fp8Matrix.empty(4, 300, "rows")
+    return q
+
+
+def test_a_matrix_and_its_addresses_do_not_part(matrix):
+    q = matrix
+    for name in q.__slots__:
+        with pytest.raises(AttributeError, match="read-only"):
+            setattr(q, name, getattr(q, name))
+        with pytest.raises(AttributeError, match="read-only"):
+            delattr(q, name)
+    assert q.shape == (4, 300) and q.desc.codes == q.codes.data_ptr() and q.desc.scales == q.scales.data_ptr()
+    assert mh._held("q", q) is q.desc
+
+
+@pytest.mark.parametrize("part", ["codes", "scales"])
+@pytest.mark.parametrize("how", ["set", "storage", "resize"])
+def test_a_matrix_whose_tensors_moved_is_refused(matrix, part, how):
+    q, t = matrix, getattr(matrix, part)
+    if how == "set":
+        t.set_(t.clone())
+    elif how == "storage":
+        t.untyped_storage().resize_(0)
+    else:
+        t.resize_(1 << 16, 64)
+    with pytest.raises(ValueError, match="a's codes or scales were moved"):
+        mh.fp8_matmul(q, q)
+    with pytest.raises(ValueError, match="out's codes or scales were moved"):
+        mh._form("out", q, True, 4, 300, "rows", q.device)
+
+
+def test_copies_have_addresses_of_their_own(matrix, monkeypatch):
+    import copy
+    q = matrix
+    q.codes.view(torch.uint8).fill_(5)
+    q.scales.view(torch.uint8).fill_(127)
+    # the constructor takes GPU tensors only; the rest of it is what is tested
+    monkeypatch.setattr(mh.Fp8Matrix, "__init__", lambda self, *a: self._set(*a))
+    same, own = copy.copy(q), copy.deepcopy(q)
+    assert same.codes is q.codes and same.desc.codes == q.desc.codes
+    assert own.codes.data_ptr() != q.codes.data_ptr() and own.desc.codes == own.codes.data_ptr()
+    assert own.desc.scales == own.scales.data_ptr() and own.shape == q.shape and own.block == q.block
+    assert torch.equal(own.codes.view(torch.uint8), q.codes.view(torch.uint8))
