@@ -18,9 +18,9 @@
 // k = 8192), at half the matrix rate, for either result type. The 8-bit
 // instructions serve callers that ask for them (MUONH_FP8_FAST).
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
+#include "fp8_choice.h"
 #include "fp8_internal.h"
 
 namespace muonh {
@@ -374,13 +374,10 @@ __device__ __forceinline__ void dma4s(const uint8_t* base, uint32_t off, uint32_
 // waves that share each block, the reads and DMA of a phase outlast its 8
 // MFMAs: 0.45 us.
 // ---------------------------------------------------------------------------
-constexpr int kT = 128;
 constexpr int kOpStage = kT * kBlock;     // 16 KB
 constexpr int kStageBytes = 2 * kOpStage; // A, then B
 constexpr int kScaleBytes = 2 * kT * 4;   // 4 bytes of each row of both operands
 constexpr int kRing = 4;
-// 32-bit offsets from a tile's first row: 256 rows of less than 2^23 bytes
-constexpr int64_t kMaxTileLd = 1 << 23;
 
 template <typename T, bool WIDE>
 __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
@@ -538,7 +535,6 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
 // and waited for at the end of 4s+7. Every phase ends in a barrier that
 // retires the wave's LDS reads.
 // ---------------------------------------------------------------------------
-constexpr int kB = 256;
 constexpr int kBigOp = kB * kBlock;            // 32 KB
 constexpr int kBigStage = 2 * kBigOp;          // A, then B
 constexpr int kBigScales = 2 * kB * 4;         // a's rows, then b's: 4 k blocks each
@@ -838,7 +834,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_matmul_direct(MatArgs a) {
 // before the sums are joined (in LDS, in wave order). Reading fragments from
 // global memory instead, 64 bytes of a line at a time, took 1.5 times as long.
 // ---------------------------------------------------------------------------
-constexpr int kS = 64;
 constexpr int kSmallOp = kS * kBlock;                       // 8 KB
 constexpr int kSmallStage = 2 * kSmallOp + 2 * kS * 4;      // both operands, then 4 bytes of scales per row
 
@@ -931,83 +926,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul_small(MatArgs a) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-constexpr int64_t kCUs = 256;
-// Output tiles of 128 x 128: a launch has fewer than 2^32 threads, and of 64 x 64
-// tiles, which have as many threads each, there are at most 4 times as many (the
-// rule takes 16 x 16 tiles at such sizes for up to 32 rows only, 2^21 of them).
-constexpr int64_t kMaxTiles = (1 << 21) - 8;
-
-enum Kind { kDirect, kSmall, kTile, kBig };
-struct Choice {
-  Kind kind;
-  int em, en;  // tile rows and columns
-  int splits, per;
-  size_t ws_bytes;
-};
-
-// Estimated time in us of a kernel on `tiles` tiles of nkb blocks: a launch,
-// then rounds of one tile per CU, each a fixed part (first loads, last stores)
-// and a part per block, which is less where a round leaves CUs idle (power,
-// cache bandwidth). Fitted to times of 130 random products up to 12288 x 8192 x
-// 12288 on the 8-bit path and, widened, with fp32 results (bf16 results of the
-// same products store half the bytes): off by 6 (64-tiles) to 14 % (256-tiles); the
-// kernel taken is on average 0.7 % slower than the fastest, 24 % at worst.
-struct Cost {
-  double fixed, block;
-};
-double estimate(const Cost& c, int64_t tiles, double nkb) {
-  const int64_t part = tiles % kCUs;
-  double t = 1.5 + (double)(tiles / kCUs) * (c.fixed + c.block * nkb);
-  if (part) t += c.fixed + c.block * nkb * (0.6 + 0.4 * std::sqrt((double)part / (double)kCUs));
-  return t;
-}
-
-// The kernel for a product: the cheapest by the estimate. Examples (measured
-// us, 8-bit path, tiles of 16, 64, 128, 256): 1x6144x2048: 5.4, 6.6, -, 21;
-// 512x2048x2048: 39, 7.7, 11, 24; 1024x4096x4096: -, 37, 21, 43;
-// 6144x2048x8192: -, 192, 107, 81 (192 x 256: 78); 8192x6144x2048: -, -, 122,
-// 90 (192 x 256: 106).
-Choice choose(int64_t m, int64_t n, int64_t k, bool wide) {
-  const int64_t nkb = ceil_div(k, kBlock);
-  auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };
-  Choice c{kSmall, kS, kS, 1, (int)nkb, 0};
-  if (m == 0 || n == 0) return c;
-  if (nkb == 0) return Choice{kTile, kT, kT, 1, 0, 0};  // zeros; that kernel's loop may be empty
-  const Cost small = wide ? Cost{3.1, 0.261} : Cost{2.7, 0.204};
-  double best = 0;
-  // 64 x 64, the k blocks split over up to 16 workgroups where tiles are few:
-  // a second launch joins the partial sums
-  for (int s = 1; s <= 16 && (s == 1 || (s * tiles(kS) <= kCUs && nkb >= 8 * s)); s *= 2) {
-    const double t = estimate(small, s * tiles(kS), (double)nkb / s) + (s > 1 ? 2.5 + 2e-6 * s * m * n : 0.0);
-    if (s > 1 && t >= best) continue;
-    best = t;
-    c.per = (int)ceil_div(nkb, s);
-    c.splits = s == 1 ? 1 : (int)ceil_div(nkb, c.per);
-  }
-  // 16 x 16 tiles, all at once: a floor of latency per block, then the rate
-  // at which the caches deliver both operands' rows, which are up to 32 a tile
-  // and 17 for a single token
-  const double rows = 1.0 + (double)std::min<int64_t>(std::min(m, n), 16) / 24.0;
-  const double t16 = 2.8 + (double)nkb * rows * std::max(0.08, 5e-4 * (double)tiles(16));
-  if (t16 < best) {
-    best = t16;
-    c = Choice{kDirect, 16, 16, 1, (int)nkb, 0};
-  }
-  if (code_ld(k) < kMaxTileLd) {
-    auto take = [&](Kind kind, int em, int en, const Cost& cost) {
-      const double t = estimate(cost, ceil_div(m, em) * ceil_div(n, en), (double)nkb);
-      if (t >= best) return;
-      best = t;
-      c = Choice{kind, em, en, 1, (int)nkb, 0};
-    };
-    take(kTile, kT, kT, wide ? Cost{4.6, 0.831} : Cost{3.6, 0.503});
-    take(kBig, kB, kB, wide ? Cost{8.9, 2.91} : Cost{7.0, 1.39});
-    take(kBig, kB - 64, kB, wide ? Cost{7.4, 2.2} : Cost{5.5, 1.15});
-  }
-  if (c.splits > 1) c.ws_bytes = (size_t)c.splits * m * (ceil_div(n, 4) * 4) * sizeof(float);
-  return c;
-}
-
 template <typename T, bool WIDE>
 int launch(const MatArgs& a, const Choice& c, hipStream_t s) {
   const dim3 grid((unsigned)map_grid((int64_t)a.tm * a.tn), (unsigned)a.splits), direct(64 * kWaves);
