@@ -1,5 +1,6 @@
 """The rule that chooses a kernel for a block-scaled product, built from its
-own source and run on the host: its launches fit whatever its constants say."""
+own source and run on the host: its launches fit whatever its constants say,
+and the sizes of the GPU tests reach every kernel that it chooses between."""
 from __future__ import annotations
 
 import itertools
@@ -10,6 +11,11 @@ import subprocess
 from collections import namedtuple
 
 import pytest
+
+pytest.importorskip("torch")
+import test_fp8_gpu  # noqa: E402
+import test_fp8_split_gpu  # noqa: E402
+import test_fp8_sums_gpu  # noqa: E402
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 ROCM_INCLUDE = "/opt/rocm/include"
@@ -87,3 +93,43 @@ def test_launches_fit_whatever_the_estimates(tmp_path, estimate):
     start = src.index("const double t16 =")
     end = src.index(";", start) + 1
     check_launches(build(tmp_path, src[:start] + estimate + src[end:]))
+
+
+KERNELS = {"16", "64", "64 split", "128", "192 x 256", "256"}
+# what is tested at every kernel, and the GPU tests that do it together
+ASPECTS = {
+    "values": ["test_product_against_fp64", "test_product_at_every_tile_size_and_loop_length"],
+    "adding": ["test_product_of_block_kinds_accumulates", "test_split_products_add_into_strided_rows"],
+    "strided": ["test_product_into_strided_rows_writes_nothing_else", "test_split_products_add_into_strided_rows"],
+    "nan": ["test_nan_and_overflow_stay_in_their_rows", "test_split_products_keep_nan_in_its_rows"],
+    "sums": ["test_sums_are_fp32", "test_split_sums_are_fp32"],
+    "fast": ["test_fast_results_keep_their_bound", "test_split_fast_results_keep_their_bound"],
+    "fast, strided": ["test_fast_results_added_into_strided_rows"],
+}
+
+
+def kernel(c):
+    return {(16, 16): "16", (64, 64): "64 split" if c.splits > 1 else "64", (128, 128): "128", (192, 256): "192 x 256",
+            (256, 256): "256"}[c.em, c.en]
+
+
+def params(test, names):
+    """The values that a test is parametrised with under `names`."""
+    return next(mark.args[1] for mark in test.pytestmark if mark.name == "parametrize" and mark.args[0] == names)
+
+
+def sizes_of(test, k=None):
+    if k is None:
+        return [tuple(s) for s in params(test, "m,n,k")]
+    return [(*mn, kk) for mn in params(test, "m,n") for kk in params(test, k)]
+
+
+@pytest.mark.parametrize("aspect", sorted(ASPECTS))
+def test_gpu_tests_reach_every_kernel(choose, aspect):
+    sizes = []
+    for name in ASPECTS[aspect]:
+        fn = next(getattr(m, name) for m in (test_fp8_gpu, test_fp8_sums_gpu, test_fp8_split_gpu) if hasattr(m, name))
+        sizes += sizes_of(fn, "k" if "loop_length" in name else None)
+    wide = 0 if "fast" in aspect else 1
+    got = {kernel(c) for c in choose([(*s, wide) for s in sizes])}
+    assert got == KERNELS
