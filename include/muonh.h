@@ -335,8 +335,9 @@ int muonh_check_disjoint(const muonh_plan* plan, const void* const* W, const voi
  *     smallest power of two 2^e, e >= -126, with max|x| <= 448 * 2^e over the
  *     block's finite entries (-126 where all are zero or none is finite), so
  *     no entry overflows. x * 2^-e is exact, so a code is x / 2^e rounded
- *     once, to the nearest e4m3 value, ties to even. NaN and infinities
- *     become NaN codes and do not count for the maximum;
+ *     once, to the nearest e4m3 value, ties to even (fp32 entries from 248 *
+ *     2^120, about 3.3e38, to 256 * 2^120, which fp32 itself does not hold).
+ *     NaN and infinities become NaN codes and do not count for the maximum;
  *   - blocks: MUONH_FP8_ROWS: 128 consecutive columns of one row (the last
  *     one of a row may be shorter); MUONH_FP8_TILES: 128 x 128 entries (edge
  *     tiles smaller).
@@ -346,8 +347,9 @@ int muonh_check_disjoint(const muonh_plan* plan, const void* const* W, const voi
  * matrix rows (TILES), muonh_fp8_scale_ld(cols) = ceil(cols/128) rounded up
  * to a multiple of 4 bytes per row, zeros past ceil(cols/128). codes 16-byte,
  * scales 4-byte aligned. The quantizing calls write all of it; an operand
- * of muonh_fp8_matmul from elsewhere needs the zeros and scale bytes in
- * [1, 254]. Matrices without rows or columns are allowed.
+ * of muonh_fp8_matmul from elsewhere needs the zeros past cols; its scale bytes
+ * are 0 to 254, and 255 is NaN, as in E8M0. Matrices without rows or columns
+ * are allowed.
  */
 enum { MUONH_FP8_ROWS = 0, MUONH_FP8_TILES = 1 };
 enum { MUONH_DT_FP32 = 0, MUONH_DT_BF16 = 1 };
@@ -413,14 +415,15 @@ int muonh_fp8_weights(const muonh_plan* plan, const float* const* W, void* const
  *   dW = matmul(dY^T, X^T)      transposed rows forms (grouped along tokens);
  *                               fp32 or bf16 G with accumulate: micro-batches
  * k = 0 gives zeros (or leaves out as it is). out_dtype: MUONH_DT_FP32 or
- * MUONH_DT_BF16. Products of the codes are exact and their sums are fp32 (bf16
- * matrix instructions on the widened codes; entries under 2^-117 in magnitude
- * may lose bits); the result is rounded once to out_dtype. With
+ * MUONH_DT_BF16. Entries are widened to bf16: exact from 2^-130 to below 2^128 in
+ * magnitude, smaller ones to within 2^-134, larger ones count as infinite
+ * (fp32 does not hold them either). Their products are exact, sums are fp32,
+ * and the result is rounded once to out_dtype. With
  * MUONH_DT_BF16 | MUONH_FP8_FAST, 8-bit matrix instructions multiply at twice
  * the rate: of the products that one of them adds at once (at most 16) they
  * drop the bits below 2^-13 of the largest, so beside fp32 sums a result is
  * off by up to 15 * 2^-13 * sum_k |a[i][k] * b[j][k]|, however small it is
- * itself, before it is rounded. NaN codes give NaN in their row or column of out.
+ * itself, before it is rounded; entries of every magnitude are exact. NaN codes give NaN in their row or column of out.
  * The result does not depend on out_ld or alignment, and is deterministic.
  * workspace: DEVICE, 256-byte aligned, of at least
  * muonh_fp8_matmul_workspace_bytes(m, n, k, out_dtype) bytes (NULL if that is

@@ -596,8 +596,8 @@ class Fp8Matrix:
 
     codes: torch.float8_e4m3fn, rows x (cols rounded up to 128), zeros past
     cols; scales: torch.float8_e8m0fnu, (rows, or rows/128 rounded up) x
-    (cols/128 rounded up, then to a multiple of 4). Both contiguous, on one
-    GPU. shape: (rows, cols). The attributes are read-only, since `desc` holds
+    (cols/128 rounded up, then to a multiple of 4); the byte 255 is NaN. Both
+    contiguous, on one GPU. shape: (rows, cols). The attributes are read-only, since `desc` holds
     the tensors' addresses: write into codes and scales, or make another
     Fp8Matrix. A matrix whose tensors were moved or resized in place is
     refused by the calls that take it.
@@ -802,7 +802,8 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     G += matmul(dY_t, X_t) into the gradient the optimizer step reads. Runs on
     the current stream of the operands' device.
 
-    Sums are fp32. fast=True, for bf16 results, takes 8-bit matrix
+    Sums are fp32; entries of 2^128 and more count as infinite and those below
+    2^-130 to within 2^-134. fast=True, for bf16 results, takes 8-bit matrix
     instructions instead, up to twice as fast, whose sums hold fewer bits: a
     result is off by up to 15 * 2^-13 * sum_k |a[i][k] * b[j][k]|.
     """

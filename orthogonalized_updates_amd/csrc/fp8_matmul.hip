@@ -58,7 +58,8 @@ struct MatArgs {
   int tm, tn;        // tile grid
 };
 
-// 8 codes (two dwords) widened to bf16 times a power of two: exact.
+// 8 codes (two dwords) widened to bf16 times a power of two: exact for values
+// that bf16 holds (multiples of 2^-133 below 2^128).
 __device__ __forceinline__ bf16x8 widen8(int lo, int hi, float s) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
@@ -66,7 +67,8 @@ __device__ __forceinline__ bf16x8 widen8(int lo, int hi, float s) {
   const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-// 2^(byte - 127) for bytes 1 .. 254.
+// 2^(byte - 127) for bytes 1 .. 254. Of a scale the conversions take the exponent
+// field: 0 stands for 2^-127 and 255 for NaN, as in E8M0.
 __device__ __forceinline__ float scale_of(int byte) { return __int_as_float(byte << 23); }
 
 // acc[x][y] += X_x Y_y^T for one block of k: NX x NY products of 16 x 16.

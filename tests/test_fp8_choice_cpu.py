@@ -13,6 +13,7 @@ from collections import namedtuple
 import pytest
 
 pytest.importorskip("torch")
+import test_fp8_ends_gpu  # noqa: E402
 import test_fp8_gpu  # noqa: E402
 import test_fp8_split_gpu  # noqa: E402
 import test_fp8_sums_gpu  # noqa: E402
@@ -103,6 +104,8 @@ ASPECTS = {
     "strided": ["test_product_into_strided_rows_writes_nothing_else", "test_split_products_add_into_strided_rows"],
     "nan": ["test_nan_and_overflow_stay_in_their_rows", "test_split_products_keep_nan_in_its_rows"],
     "sums": ["test_sums_are_fp32", "test_split_sums_are_fp32"],
+    "ends": ["test_entries_at_the_ends_of_the_range"],
+    "fast, ends": ["test_entries_at_the_ends_of_the_range"],
     "fast": ["test_fast_results_keep_their_bound", "test_split_fast_results_keep_their_bound"],
     "fast, strided": ["test_fast_results_added_into_strided_rows"],
 }
@@ -128,7 +131,7 @@ def sizes_of(test, k=None):
 def test_gpu_tests_reach_every_kernel(choose, aspect):
     sizes = []
     for name in ASPECTS[aspect]:
-        fn = next(getattr(m, name) for m in (test_fp8_gpu, test_fp8_sums_gpu, test_fp8_split_gpu) if hasattr(m, name))
+        fn = next(getattr(m, name) for m in (test_fp8_gpu, test_fp8_sums_gpu, test_fp8_split_gpu, test_fp8_ends_gpu) if hasattr(m, name))
         sizes += sizes_of(fn, "k" if "loop_length" in name else None)
     wide = 0 if "fast" in aspect else 1
     got = {kernel(c) for c in choose([(*s, wide) for s in sizes])}

@@ -77,3 +77,83 @@ def test_weights_at_the_lowest_scale():
     for w, q, qt in zip(W, ws.weights, ws.transposed):
         check_matrix(q, w.double().numpy(), "tiles")
         check_matrix(qt, w.double().numpy().T, "tiles")
+
+
+# ---- products ---------------------------------------------------------------------
+# every kind of tile: one nonzero code of 1.0 in each row of b picks an entry of
+# a, so each result is one product
+PICKS = [(5, 150, 300), (640, 730, 300), (1500, 1420, 700), (3100, 3300, 300), (4090, 3900, 129), (200, 300, 8192)]
+
+
+def matrix(codes, scale_bytes):
+    rows, cols = codes.shape
+    q = mh().Fp8Matrix.empty(rows, cols)
+    full = np.zeros(tuple(q.codes.shape), np.uint8)
+    full[:, :cols] = codes
+    q.codes.view(torch.uint8).copy_(torch.from_numpy(full))
+    nb = -(-cols // 128)
+    s = np.zeros(tuple(q.scales.shape), np.uint8)
+    s[:, :nb] = scale_bytes
+    q.scales.view(torch.uint8).copy_(torch.from_numpy(s))
+    return q, fo.decode(codes) * np.ldexp(1.0, np.repeat(s[:, :nb].astype(np.int64), 128, axis=1)[:, :cols] - 127)
+
+
+def picked(m, n, k, low, high, byte_b, limit, seed):
+    """(a, b, exact results): a's scale bytes in [low, high], entries below
+    `limit` in magnitude, b's all byte_b."""
+    rng = np.random.default_rng((seed, m, n, k))
+    nb = -(-k // 128)
+    s = rng.integers(low, high + 1, (m, nb))
+    codes = rng.integers(0, 127, (m, k)).astype(np.uint8)
+    scale = np.ldexp(1.0, np.repeat(s, 128, axis=1)[:, :k] - 127)
+    # codes whose entries would reach the limit lose 2^4 .. 2^8 of their exponent
+    while np.any(bad := fo.decode(codes) * scale >= limit):
+        codes = np.where(bad, codes - 8, codes).astype(np.uint8)
+    codes |= (128 * rng.integers(0, 2, codes.shape)).astype(np.uint8)
+    col = rng.integers(0, k, n)
+    cb = np.zeros((n, k), np.uint8)
+    cb[np.arange(n), col] = 56
+    a, va = matrix(codes, s)
+    b, _ = matrix(cb, np.full((n, nb), byte_b))
+    return a, b, va[:, col] * 2.0 ** (byte_b - 127)
+
+
+@pytest.mark.parametrize("dtype,fast", [("bf16", False), ("fp32", False), ("bf16", True)])
+@pytest.mark.parametrize("m,n,k", PICKS)
+def test_entries_at_the_ends_of_the_range(m, n, k, dtype, fast):
+    """Up to the largest that fp32 holds, with scale bytes up to 254, entries
+    count exactly, with bytes down to 0 to within half of bf16's smallest
+    value, 2^-134; fast results take all entries exactly."""
+    for low, high, byte_b in ((0, 20, 247), (226, 254, 20)):
+        a, b, v = picked(m, n, k, low, high, byte_b, np.inf if fast else 2.0 ** 128, 51)
+        out = mh().fp8_matmul(a, b, out_dtype=DT[dtype], fast=fast).double().cpu().numpy()
+        if low and not fast or fast:
+            assert np.array_equal(out, v)
+        else:
+            assert (np.abs(out - v) <= 2.0 ** -134 * 2.0 ** (byte_b - 127)).all()
+            whole = v == np.round(v * 2.0 ** (133 - byte_b + 127)) * 2.0 ** (byte_b - 127 - 133)
+            assert np.array_equal(out[whole], v[whole]) and 0.5 < whole.mean() < 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_an_entry_past_fp32_counts_as_infinite(dtype):
+    """The largest fp32 values are coded 256 * 2^120."""
+    x = torch.full((3, 128), 3.4e38, device="cuda")
+    x[1] = 3.2e38
+    x[2] = -3.4e38
+    q, _ = mh().fp8_quantize(x)
+    assert [int(v) for v in q.scales.view(torch.uint8)[:, 0]] == [247, 247, 247]
+    w, _ = mh().fp8_quantize(torch.full((5, 128), 2.0 ** -60, device="cuda"))
+    out = mh().fp8_matmul(q, w, out_dtype=DT[dtype])
+    assert (out[0] == float("inf")).all() and (out[2] == -float("inf")).all()
+    assert (out[1] == 128 * 240 * 2.0 ** 60).all()  # 3.2e38 = 240.7 * 2^120
+    assert torch.equal(q.dequantize()[0], torch.full((128,), float("inf"), device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,fast", [("bf16", False), ("fp32", False), ("bf16", True)])
+def test_the_scale_byte_255_is_nan(dtype, fast):
+    a, _ = matrix(np.full((4, 300), 56, np.uint8), np.full((4, 3), 127))
+    a.scales.view(torch.uint8)[2, 1] = 255
+    b, _ = matrix(np.full((7, 300), 56, np.uint8), np.full((7, 3), 127))
+    out = mh().fp8_matmul(a, b, out_dtype=DT[dtype], fast=fast)
+    assert torch.isnan(out[2]).all() and (out[[0, 1, 3]] == 300.0).all()
