@@ -473,6 +473,7 @@ class MuonH:
         out.memory.record_stream(self.torch.cuda.current_stream(self.device))
         _on_device(self.torch, self.device, get_lib().muonh_fp8_weights, self.plan.handle,
                    self._ptr_array("W", weights), *out.arrays)
+        _written(out.memory)
 
     def read_update(self, index: int):
         """The update O of matrix `index` from the last step (fp32, rows x cols)."""
@@ -743,6 +744,13 @@ def _on_device(torch, dev, fn, *args) -> None:
             check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
 
 
+def _written(*tensors) -> None:
+    """Tells autograd that the library wrote into the tensors, so that a
+    backward pass that saved one of them before refuses to use it."""
+    from torch.autograd.graph import increment_version
+    increment_version(tensors)
+
+
 def fp8_quantize(x, block: str = "rows", forms: str = "plain",
                  out: Optional[Fp8Matrix] = None, out_t: Optional[Fp8Matrix] = None):
     """Quantize x (a 2-d fp32 or bf16 tensor on the GPU whose rows are
@@ -752,6 +760,8 @@ def fp8_quantize(x, block: str = "rows", forms: str = "plain",
     grouped along x's rows) or "both", in one pass. Returns (q, q_t), None in
     the place of a form that was not asked for. out / out_t: matrices to
     write into instead of new ones. Runs on the current stream of x's device.
+    Autograd does not see it: the results carry no gradient to x, and a
+    backward pass is the caller's (fp8_matmul).
     """
     import torch
     if not isinstance(x, torch.Tensor):
@@ -769,6 +779,9 @@ def fp8_quantize(x, block: str = "rows", forms: str = "plain",
     d, t = _NO_FORM if q is None else q.desc, _NO_FORM if qt is None else qt.desc
     _on_device(torch, dev, get_lib().muonh_fp8_quantize, x.data_ptr(), dt, rows, cols, ld,
                FP8_BLOCKS[block], d.codes, d.scales, t.codes, t.scales)
+    for o in (out, out_t):
+        if o is not None:
+            _written(o.codes, o.scales)
     return q, qt
 
 
@@ -806,6 +819,10 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     2^-130 to within 2^-134. fast=True, for bf16 results, takes 8-bit matrix
     instructions instead, up to twice as fast, whose sums hold fewer bits: a
     result is off by up to 15 * 2^-13 * sum_k |a[i][k] * b[j][k]|.
+
+    Autograd does not see the product: its result carries no gradient, and
+    the caller runs the two others in the backward pass of a
+    torch.autograd.Function, say. Only the version of a given `out` moves on.
     """
     import torch
     for name, m in (("a", a), ("b", b)):
@@ -823,8 +840,9 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
             raise ValueError("accumulate=True needs out")
         out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
         dt = _fp8_dt(torch, out_dtype)
-        out = torch.empty(shape, device=dev, dtype=out_dtype)
+        out, given = torch.empty(shape, device=dev, dtype=out_dtype), False
     else:
+        given = True
         if not isinstance(out, torch.Tensor):
             raise TypeError("out must be a torch tensor")
         dt = _fp8_dt(torch, out.dtype)
@@ -844,4 +862,6 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _on_device(torch, dev, lib.muonh_fp8_matmul, da, db, out.data_ptr(), dt, ld,
                1 if accumulate else 0, None if ws is None else ws.data_ptr(), nbytes)
+    if given:
+        _written(out)
     return out

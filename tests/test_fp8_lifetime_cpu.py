@@ -60,7 +60,8 @@ def test_every_quantization_records_its_stream(monkeypatch):
     opt.torch = SimpleNamespace(cuda=SimpleNamespace(current_stream=lambda dev: (stream, dev)))
     opt.plan = SimpleNamespace(handle=11)
     opt._ptr_array = lambda name, tensors: 12
-    out = SimpleNamespace(memory=SimpleNamespace(record_stream=lambda s: log.append(("record", s))), arrays=[1, 2, 3, 4])
+    out = SimpleNamespace(memory=torch.zeros(8, dtype=torch.uint8), arrays=[1, 2, 3, 4])
+    out.memory.record_stream = lambda s: log.append(("record", s))
     monkeypatch.setattr(mh, "_on_device", lambda t, dev, fn, *args: log.append(("launch", dev, args)))
     opt._quantize([], out)
     assert log == [("record", (stream, "cuda:1")), ("launch", "cuda:1", (11, 12, 1, 2, 3, 4))]
