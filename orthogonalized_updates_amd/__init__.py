@@ -461,6 +461,8 @@ class MuonH:
         if out.shapes != self.shapes or out.device != self.device or out.order != self.plan_order:
             raise ValueError("the Fp8Weights set has other shapes or another device")
         lo, hi = out.span
+        if not lo <= out.arrays[0] < hi:
+            raise ValueError("the Fp8Weights set's memory was moved, or it is a copy: its pointers are another's")
         for ts in lists:
             for t in ts:
                 p = t.data_ptr()

@@ -52,6 +52,20 @@ def test_pointer_arrays_live_in_the_matrices_memory(on_the_host, transposed):
     assert keep.untyped_storage().data_ptr() == lo
 
 
+def test_a_copied_or_moved_set_is_refused(on_the_host):
+    import copy
+    ws = mh.Fp8Weights([(5, 300)], torch.device("cpu"), True, [0])
+    opt = object.__new__(mh.MuonH)
+    opt.shapes, opt.device, opt.plan_order = [(5, 300)], torch.device("cpu"), [0]
+    opt._check_fp8(ws)
+    opt._check_fp8(copy.copy(ws))  # the same memory
+    with pytest.raises(ValueError, match="moved"):
+        opt._check_fp8(copy.deepcopy(ws))
+    ws.memory.set_(ws.memory.clone())
+    with pytest.raises(ValueError, match="moved"):
+        opt._check_fp8(ws)
+
+
 def test_every_quantization_records_its_stream(monkeypatch):
     log = []
     stream = object()
