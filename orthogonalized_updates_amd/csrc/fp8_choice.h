@@ -35,9 +35,12 @@ struct Choice {
 // then rounds of one tile per CU, each a fixed part (first loads, last stores)
 // and a part per block, which is less where a round leaves CUs idle (power,
 // cache bandwidth). Fitted to times of 130 random products up to 12288 x 8192 x
-// 12288 on the 8-bit path and, widened, with fp32 results (bf16 results of the
-// same products store half the bytes): off by 6 (64-tiles) to 14 % (256-tiles); the
-// kernel taken is on average 0.7 % slower than the fastest, 24 % at worst.
+// 12288 on the 8-bit path and, widened, with fp32 results: off by 6 (64-tiles) to
+// 14 % (256-tiles). On 132 others of these sizes the kernel taken is on average
+// as fast as the best of its kind (8-bit path), 1.3 and 1.1 % slower (widened,
+// bf16 and fp32 results) and 1.3 and 0.7 % where it adds to them, which the
+// estimate does not count; 27 % at worst (10213 x 440 x 94 added to bf16: 15.2
+// us with 192 x 256 tiles, 11.9 with 128).
 struct Cost {
   double fixed, block;
 };
@@ -49,10 +52,12 @@ inline double estimate(const Cost& c, int64_t tiles, double nkb) {
 }
 
 // The kernel for a product: the cheapest by the estimate. Examples (measured
-// us, 8-bit path, tiles of 16, 64, 128, 256): 1x6144x2048: 5.4, 6.6, -, 21;
-// 512x2048x2048: 39, 7.7, 11, 24; 1024x4096x4096: -, 37, 21, 43;
-// 6144x2048x8192: -, 192, 107, 81 (192 x 256: 78); 8192x6144x2048: -, -, 122,
-// 90 (192 x 256: 106).
+// us, tiles of 16, 64, 128, 192 x 256, 256). Widened, bf16 results:
+// 1x6144x2048: 5.5, 7.5, 15, 32, 41; 512x2048x2048: 39, 8.3, 15, 32, 42;
+// 1024x4096x4096: -, 47, 33, 61, 78; 6144x2048x8192: -, 204, 155, 133, 151;
+// 8192x6144x2048: -, 295, 182, 171, 143. 8-bit path: 1x6144x2048: 5.4, 6.6, -, -,
+// 21; 512x2048x2048: 39, 7.7, 11, -, 24; 1024x4096x4096: -, 37, 21, -, 43;
+// 6144x2048x8192: -, 192, 107, 78, 81; 8192x6144x2048: -, -, 122, 106, 90.
 inline Choice choose(int64_t m, int64_t n, int64_t k, bool wide) {
   const int64_t nkb = ceil_div(k, kBlock);
   auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };

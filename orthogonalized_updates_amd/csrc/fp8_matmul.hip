@@ -512,14 +512,15 @@ __global__ __launch_bounds__(512, 2) void k_matmul_tile(MatArgs a) {
 // k block (2 x 64 KB): products with enough tiles for the chip. 192 x 256
 // tiles (FA = 3 instead of 4 fragments of a per half wave tile) where they
 // fill the chip better: 6144 x 2048 x 8192, 192 tiles or 256 for 256 CUs, takes
-// 139 instead of 154 us with fp32 results and 78 instead of 80.5 on the 8-bit
-// path (fewer active CUs clock higher). 256 x 192 tiles gained 3-7 % there.
-// 8192^3 takes 374 us on the 8-bit path (2940 TFLOP/s) and 721 with fp32
-// results (1525): power is what bounds both (about 2 GHz).
+// 139 instead of 154 us with fp32 results, 133 instead of 151 with bf16 ones and
+// 78 instead of 80.5 on the 8-bit path (fewer active CUs clock higher). 256 x 192
+// tiles gained 3-7 % there. 8192^3 takes 721 us with fp32 results (1525 TFLOP/s),
+// 683 with bf16 ones (1610) and 374 on the 8-bit path (2940): power is what bounds
+// all of them (about 2 GHz).
 //
 // The waves form two groups of 4, one wave of each per SIMD, that take turns
-// phase by phase: one group's 16 MFMAs run while the other reads LDS and
-// issues DMA, so the matrix cores see no gap and MFMA waves issue no memory
+// phase by phase: one group's 16 MFMAs (64 widened ones) run while the other
+// reads LDS and issues DMA, so the matrix cores see no gap and MFMA waves issue no memory
 // instruction. A wave's block of k takes two turns, 64 of its 128 rows each
 // (A0, A1), which keeps the fragments at 64 registers beside 128
 // accumulators. Phases of block s, group 0 | group 1:
