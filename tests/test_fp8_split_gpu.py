@@ -68,3 +68,43 @@ def test_split_products_keep_nan_in_its_rows(m, n, k, dtype, fast):
         v = fo.values(*host(a), (m, k)) @ fo.values(*host(b), (n, k)).T
     assert np.array_equal(np.isnan(out), np.isnan(v)) and np.isfinite(out[~np.isnan(v)]).all()
     assert np.isnan(v).sum() == 2 * n + m - 2
+
+
+def test_two_captured_graphs_keep_their_workspaces_apart():
+    """A split product's partial sums live in a workspace of the call's own:
+    two graphs with one each, replayed in turn and on two streams at once with
+    eager products between them, all bit for bit the eager results."""
+    m, n, k = 200, 300, 8192
+    ops = [(operand(m, k, 50 + i, spread=False)[0], operand(n, k, 60 + i, spread=False)[0]) for i in range(3)]
+    want = [mh().fp8_matmul(a, b, out_dtype=torch.float32) for a, b in ops]
+    outs = [torch.zeros(m, n, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for (a, b), out in zip(ops, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mh().fp8_matmul(a, b, out=out)
+            mh().fp8_matmul(a, b, out=out, accumulate=True)
+        graphs.append(graph)
+    twice = []
+    for (a, b), w in zip(ops, want):
+        twice.append(mh().fp8_matmul(a, b, out=w.clone(), accumulate=True))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, out in zip(graphs, outs):
+            out.fill_(float("nan"))
+            graph.replay()
+            assert torch.equal(mh().fp8_matmul(*ops[2], out_dtype=torch.float32), want[2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, t) for out, t in zip(outs, twice))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for out in outs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for stream, graph in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        assert torch.equal(mh().fp8_matmul(*ops[2], out_dtype=torch.float32), want[2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, t) for out, t in zip(outs, twice))
