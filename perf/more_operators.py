@@ -41,7 +41,7 @@ def listed():
         dict(name="norm token", op="norm", rows=1, cols=2048, dtype="bf16", residual=True, forms="plain"),
         # a layer's input in training: the new residual stream, and the operand
         # of the forward products and of the weight gradients
-        dict(name="norm with residual, 8 bits", op="norm", rows=TOKENS, cols=2048, dtype="bf16", residual=True, forms="both"),
+        dict(name="norm with residual in 8 bits", op="norm", rows=TOKENS, cols=2048, dtype="bf16", residual=True, forms="both"),
         # the norm of 16 heads of 128 for each token
         dict(name="norm of heads", op="norm", rows=16 * TOKENS, cols=128, dtype="bf16", residual=False, forms="none"),
         # its way back, joined with the residual's gradient
