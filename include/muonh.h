@@ -81,7 +81,7 @@ enum {
   MUONH_EWORKSPACE = -3, /* workspace missing, too small or misaligned */
   MUONH_EHIP = -4,       /* a HIP runtime call failed (see muonh_last_error) */
   MUONH_ENOMEM = -5,     /* host allocation failed */
-  MUONH_EALIAS = -6      /* two of the W, G, M matrices (or an fp8 call's arrays) overlap */
+  MUONH_EALIAS = -6      /* two of the W, G, M matrices (or another call's arrays) overlap */
 };
 
 /* Newton-Schulz plan flags (at most one). Default: operands in bf16, bf16
@@ -438,6 +438,56 @@ size_t muonh_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t
 int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* out,
                      int32_t out_dtype, int64_t out_ld, int32_t accumulate, void* workspace,
                      size_t workspace_bytes, void* stream);
+
+/*
+ * RMS norm with the residual's addition, before a block's linear layers (the
+ * norms' weights belong to the AdamW group):
+ *   h = x + residual, in fp32, rounded to h's type;  r = 1 / sqrt(mean(h^2) + eps)
+ *   y = (h * r) * weight, along the cols entries of each row.
+ * The norm is of the stored h, which the backward pass takes too. Sums and
+ * factors are fp32 (a mean square beyond fp32's range gives r = 0), y is rounded once,
+ * to its type or to 8 bits.
+ * x: DEVICE, rows x cols of x_dtype, element (i, j) at i*x_ld + j, x_ld >= cols;
+ * residual (or NULL: h = x, and h must be NULL), h: the same with h_dtype and
+ * pitches of their own; h may be x or residual itself (the same pointer, type and
+ * pitch). weight: cols floats; eps: finite, >= 0; rstd: rows floats, receives r. Output, one
+ * of
+ *   y (y_dtype, y_ld), or
+ *   codes and scales and/or codes_t and scales_t: y and/or its transpose as
+ *   MUONH_FP8_ROWS matrices (muonh_fp8_quantize's forms of the unrounded y): what
+ *   muonh_fp8_matmul reads for the forward product and the weight gradient.
+ * Rows do not depend on each other; results are deterministic for a size and set of
+ * outputs. Asynchronous on `stream`, capturable.
+ * Errors: MUONH_EINVAL (NULL or misaligned argument, bad dtype, pitch or eps, half-given
+ * pair, both or neither kind of output, residual without h), MUONH_ESHAPE (rows out
+ * of [0, MUONH_MAX_FP8_DIM], cols out of [1, MUONH_MAX_FP8_DIM], or 2^24 tiles of 128 x 128 or
+ * more with codes_t),
+ * MUONH_EALIAS (an output overlaps an input or another output), MUONH_EHIP.
+ */
+int muonh_rms_norm(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t x_ld,
+                   const void* residual, int32_t h_dtype, int64_t residual_ld, void* h, int64_t h_ld,
+                   const float* weight, float eps, float* rstd, void* y, int32_t y_dtype, int64_t y_ld,
+                   void* codes, void* scales, void* codes_t, void* scales_t, void* stream);
+
+/*
+ * Its gradient: with n = h * r and g = dy * weight,
+ *   dh = r * (g - n * mean(g * n)) + dresidual, rounded once to h's type (the
+ *   gradient of x and of residual alike), and
+ *   dweight = sum over rows of dy * n, plus its old values if `accumulate`.
+ * dy (dy_dtype), h, dresidual (or NULL), dh (h_dtype): DEVICE, rows x cols with
+ * pitches of their own; h and rstd from muonh_rms_norm. dh may be dy or dresidual itself.
+ * Sums are fp32 in a fixed order: deterministic for a size. Without rows dweight is zero (or left as it
+ * is). workspace: DEVICE, 256-byte aligned, at least
+ * muonh_rms_norm_backward_workspace_bytes(rows, cols) bytes; calls in flight at
+ * once need workspaces of their own. Asynchronous on `stream`, capturable.
+ * Errors: as muonh_rms_norm, and MUONH_EWORKSPACE.
+ */
+size_t muonh_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, const void* h,
+                            int32_t h_dtype, int64_t rows, int64_t cols, int64_t h_ld,
+                            const float* weight, const float* rstd, const void* dresidual,
+                            int64_t dresidual_ld, void* dh, int64_t dh_ld, float* dweight,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* muonh_status_string(int status);

@@ -135,6 +135,11 @@ def _load_library() -> ctypes.CDLL:
         "muonh_fp8_matmul_workspace_bytes": (sz, [i64, i64, i64, i32]),
         "muonh_fp8_matmul": (ctypes.c_int, [ctypes.POINTER(Fp8Desc), ctypes.POINTER(Fp8Desc), vp,
                                             i32, i64, i32, vp, sz, vp]),
+        "muonh_rms_norm": (ctypes.c_int, [vp, i32, i64, i64, i64, vp, i32, i64, vp, i64, vp, f32, vp, vp,
+                                          i32, i64, vp, vp, vp, vp, vp]),
+        "muonh_rms_norm_backward_workspace_bytes": (sz, [i64, i64]),
+        "muonh_rms_norm_backward": (ctypes.c_int, [vp, i32, i64, vp, i32, i64, i64, i64, vp, vp, vp, i64,
+                                                   vp, i64, vp, i32, vp, sz, vp]),
         "muonh_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "muonh_last_error": (ctypes.c_char_p, []),
     }
@@ -504,7 +509,7 @@ __all__ = ["MuonH", "Plan", "MuonHError", "GroupDesc", "get_lib", "check", "LIB_
            "MUONH_NOALLOC_WORKSPACE_BYTES", "AdamW",
            "PTR_CACHE_ENTRIES", "Fp8Matrix", "Fp8Weights", "fp8_quantize", "fp8_matmul",
            "MUONH_FP8_ROWS", "MUONH_FP8_TILES", "MUONH_FP8_FAST", "MUONH_DT_FP32", "MUONH_DT_BF16",
-           "MUONH_MAX_FP8_DIM"]
+           "MUONH_MAX_FP8_DIM", "rms_norm", "rms_norm_fp8", "rms_norm_backward"]
 
 
 class AdamW:
@@ -867,3 +872,144 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     if given:
         _written(out)
     return out
+
+
+# -- RMS norm ------------------------------------------------------------------
+def _rows(name: str, t, dev, shape=None, dtype=None):
+    """(dtype code, row pitch) of a 2-d fp32 or bf16 tensor whose rows are
+    contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dt = _fp8_dt(torch, t.dtype)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name} must be a 2-d tensor on {dev if dev.type == 'cuda' else 'a ROCm GPU'}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return dt, _row_pitch(t, name)
+
+
+def _floats(name: str, t, dev, n: int) -> None:
+    """A contiguous fp32 vector of n entries."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 torch tensor")
+    if t.shape != (n,) or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous vector of {n} entries on {dev}")
+
+
+def _norm_inputs(x, weight, residual, residual_out):
+    """Checks what both forms of the norm take: (x's dtype code and pitch, h's
+    dtype code, residual's pitch, h or None, its pitch, rstd)."""
+    import torch
+    dt, ld = _rows("x", x, getattr(x, "device", None))
+    dev, shape = x.device, x.shape
+    _floats("weight", weight, dev, shape[1])
+    rstd = torch.empty(shape[0], dtype=torch.float32, device=dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without residual")
+        return dt, ld, dt, 0, None, 0, rstd
+    hdt, rld = _rows("residual", residual, dev, shape)
+    if residual_out is None:
+        h = torch.empty(shape, dtype=residual.dtype, device=dev)
+        return dt, ld, hdt, rld, h, max(shape[1], 1), rstd
+    _, hld = _rows("residual_out", residual_out, dev, shape, residual.dtype)
+    return dt, ld, hdt, rld, residual_out, hld, rstd
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, out_dtype=None, residual_out=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight along each row
+    (muonh_rms_norm). Returns (y, h, rstd): h is x itself without a residual,
+    rstd (rows, fp32) and h are what rms_norm_backward takes.
+
+    x, residual: 2-d fp32 or bf16 tensors whose rows are contiguous, any row
+    stride, each of its own type; h has the residual's, and y is the norm of h as
+    stored. weight: fp32 vector. residual_out: a tensor for h, which may be
+    `residual` or `x` itself. out: a tensor for y; otherwise a new one of out_dtype
+    (default: h's type). Runs on the current stream of x's device, outside
+    autograd: rms_norm_backward is the gradient.
+    """
+    import torch
+    dt, ld, hdt, rld, h, hld, rstd = _norm_inputs(x, weight, residual, residual_out)
+    dev, shape = x.device, tuple(x.shape)
+    y = out
+    if y is None:
+        y = torch.empty(shape, dtype=(x if h is None else h).dtype if out_dtype is None else out_dtype, device=dev)
+    ydt, yld = _rows("out", y, dev, shape, out_dtype)
+    _on_device(torch, dev, get_lib().muonh_rms_norm, x.data_ptr(), dt, shape[0], shape[1], ld,
+               None if h is None else residual.data_ptr(), hdt, rld, None if h is None else h.data_ptr(), hld,
+               weight.data_ptr(), float(eps), rstd.data_ptr(), y.data_ptr(), ydt, yld, None, None, None, None)
+    for o in (out, residual_out):
+        if o is not None:
+            _written(o)
+    return y, x if h is None else h, rstd
+
+
+def rms_norm_fp8(x, weight, residual=None, eps: float = 1e-6, forms: str = "plain",
+                 out: Optional[Fp8Matrix] = None, out_t: Optional[Fp8Matrix] = None, residual_out=None):
+    """rms_norm with y quantized to block-scaled e4m3 as fp8_quantize(...,
+    block="rows") does, from its unrounded values. Returns (q, q_t, h, rstd);
+    forms, out and out_t as for fp8_quantize, the rest as for rms_norm."""
+    import torch
+    if forms not in FP8_FORMS:
+        raise ValueError(f"forms must be one of {FP8_FORMS}, got {forms!r}")
+    dt, ld, hdt, rld, h, hld, rstd = _norm_inputs(x, weight, residual, residual_out)
+    dev = x.device
+    rows, cols = x.shape
+    q = _form("out", out, forms != "transposed", rows, cols, "rows", dev)
+    qt = _form("out_t", out_t, forms != "plain", cols, rows, "rows", dev)
+    d, t = _NO_FORM if q is None else q.desc, _NO_FORM if qt is None else qt.desc
+    _on_device(torch, dev, get_lib().muonh_rms_norm, x.data_ptr(), dt, rows, cols, ld,
+               None if h is None else residual.data_ptr(), hdt, rld, None if h is None else h.data_ptr(), hld,
+               weight.data_ptr(), float(eps), rstd.data_ptr(), None, 0, 0, d.codes, d.scales, t.codes, t.scales)
+    for o in (out, out_t):
+        if o is not None:
+            _written(o.codes, o.scales)
+    if residual_out is not None:
+        _written(residual_out)
+    return q, qt, x if h is None else h, rstd
+
+
+def rms_norm_backward(dy, h, weight, rstd, dresidual=None, out=None, dweight=None, accumulate: bool = False):
+    """The gradient of rms_norm (muonh_rms_norm_backward): (dh, dweight). dh, of
+    h's type, is the gradient of x and of residual alike; dresidual, the gradient that
+    reaches h past the norm, is added to it.
+
+    dy: gradient of y, fp32 or bf16; h, rstd: from the forward call; dresidual: of
+    h's type. out: a tensor for dh, which may be `dresidual` or `dy` itself. dweight: an fp32
+    vector to write into (new otherwise), with accumulate=True to add to.
+    Deterministic. Runs on the current stream of h's device.
+    """
+    import torch
+    hdt, hld = _rows("h", h, getattr(h, "device", None))
+    dev = h.device
+    rows, cols = shape = tuple(h.shape)
+    ddt, dld = _rows("dy", dy, dev, shape)
+    _floats("weight", weight, dev, cols)
+    _floats("rstd", rstd, dev, rows)
+    rld = 0
+    if dresidual is not None:
+        _, rld = _rows("dresidual", dresidual, dev, shape, h.dtype)
+    dh = torch.empty(shape, dtype=h.dtype, device=dev) if out is None else out
+    _, old = _rows("out", dh, dev, shape, h.dtype)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs dweight")
+        dw = torch.empty(cols, dtype=torch.float32, device=dev)
+    else:
+        _floats("dweight", dweight, dev, cols)
+        dw = dweight
+    lib = get_lib()
+    nbytes = lib.muonh_rms_norm_backward_workspace_bytes(rows, cols)
+    # from torch's allocator on the current stream, as fp8_matmul's
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _on_device(torch, dev, lib.muonh_rms_norm_backward, dy.data_ptr(), ddt, dld, h.data_ptr(), hdt, rows, cols, hld,
+               weight.data_ptr(), rstd.data_ptr(), None if dresidual is None else dresidual.data_ptr(), rld,
+               dh.data_ptr(), old, dw.data_ptr(), 1 if accumulate else 0, None if ws is None else ws.data_ptr(), nbytes)
+    for o in (out, dweight):
+        if o is not None:
+            _written(o)
+    return dh, dw

@@ -37,6 +37,17 @@ inline int fail(int code, const char* fmt, ...) {
 
 inline bool bad_dim(int64_t v) { return v < 0 || v > MUONH_MAX_FP8_DIM; }
 
+// 128 x 128 tiles of a matrix, one workgroup each: a launch has fewer than 2^32
+// threads.
+constexpr int64_t kMaxBlocks = (1 << 24) - 8;
+bool tiles_fit(int64_t rows, int64_t cols);
+
+// codes, scales, codes_t, scales_t (MUONH_FP8_ROWS; codes and scales may be
+// nullptr) of the matrix (src[r][c] * rstd[r]) * weight[c]. Arguments are the
+// caller's to check.
+int quantize_normed(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t src_ld, const float* rstd,
+                    const float* weight, void* codes, void* scales, void* codes_t, void* scales_t, hipStream_t s);
+
 // A byte range of device memory, for the overlap checks of a call.
 struct Span {
   const char* name;

@@ -13,7 +13,7 @@
 // it, rounds once (to nearest, ties to even).
 #include <type_traits>
 
-#include "fp8_internal.h"
+#include "fp8_codes.h"
 
 namespace muonh {
 namespace fp8 {
@@ -21,78 +21,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 16;
-// Blocks of one launch: a launch has fewer than 2^32 threads.
-constexpr int64_t kMaxBlocks = (1 << 24) - 8;
-
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
-// 4 values over a scale 2^e (exact) to 4 codes, the first in the low byte.
-typedef short s16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s) {
-  s16x2 v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(s16x2{0, 0}, a, b, s, false);
-  v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, s, true);
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-// Magnitudes order like their bits, compared as integers: a floating-point
-// maximum answers a signaling NaN with a NaN and forgets what came before. A
-// scale's exponent depends on the upper 16 bits of the maximum, rounded up, so
-// maxima are handled in pairs of 16 bits, two in one packed instruction, and
-// bf16 entries stay in pairs throughout.
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pmax(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(
-      uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
-}
-__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
-  return __builtin_amdgcn_perm(b, a, 0x05040100);
-}
-__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
-  return __builtin_amdgcn_perm(b, a, 0x07060302);
-}
-// Two magnitudes with those that are not finite as zero.
-__device__ __forceinline__ uint32_t finite2(uint32_t m) {
-  return ((m & 0xffffu) < 0x7f80u ? m & 0xffffu : 0u) | (m < 0x7f800000u ? m & 0xffff0000u : 0u);
-}
-// Upper halves of two fp32 magnitudes, rounded up.
-__device__ __forceinline__ uint32_t upper2(uint32_t a, uint32_t b) {
-  return high_halves(a + 0xffffu, b + 0xffffu);
-}
-// Maxima over the 16 lanes of a DPP row, in all of them.
-template <int CTRL>
-__device__ __forceinline__ uint32_t pmax_dpp(uint32_t v) {
-  return pmax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ uint32_t pmax_row16(uint32_t v) {
-  v = pmax_dpp<0xB1>(v);   // quad [1,0,3,2]
-  v = pmax_dpp<0x4E>(v);   // quad [2,3,0,1]
-  v = pmax_dpp<0x141>(v);  // mirrored halves: the other quad of 8
-  return pmax_dpp<0x140>(v);  // mirrored row: the other 8
-}
-// Maxima over finite entries -> scale bytes e + 127, e >= -126: with a = 1.f *
-// 2^E and 448 = 1.75 * 2^8, e = E - 8 where 1.f <= 1.75 (0x60 of the 7 bits),
-// else E - 7.
-__device__ __forceinline__ uint32_t scale_bytes2(uint32_t m) {
-  const u16x2 e = (__builtin_bit_cast(u16x2, m) + u16x2{0x1f, 0x1f}) >> u16x2{7, 7};
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(e, u16x2{9, 9}) - u16x2{8, 8});
-}
-// The scale 2^e of a pair's byte in [1, 247], a normal number.
-__device__ __forceinline__ float scale_lo(uint32_t b) { return __uint_as_float(b << 23); }
-__device__ __forceinline__ float scale_hi(uint32_t b) { return __uint_as_float((b << 7) & 0x7f800000u); }
-// The bytes of 8 scales from 4 pairs.
-__device__ __forceinline__ uint2 bytes8(const uint32_t (&b)[4]) {
-  return make_uint2(__builtin_amdgcn_perm(b[1], b[0], 0x06040200), __builtin_amdgcn_perm(b[3], b[2], 0x06040200));
-}
-// 8 entries (4 pairs) over a scale to 8 codes.
-__device__ __forceinline__ uint2 codes8(uint32_t a, uint32_t b, uint32_t c, uint32_t d, float s) {
-  auto two = [&](s16x2 v, uint32_t x, auto hi) {
-    return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2, x), s, decltype(hi)::value);
-  };
-  const s16x2 x = two(two(s16x2{0, 0}, a, std::false_type{}), b, std::true_type{});
-  const s16x2 y = two(two(s16x2{0, 0}, c, std::false_type{}), d, std::true_type{});
-  return make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
-}
 
 struct Group {
   int64_t rows, cols, src_ld;
@@ -107,6 +35,7 @@ struct Args {
   int ptrs;
   const void* src;
   void *codes, *scales, *codes_t, *scales_t;
+  const float *rstd, *weight;  // NORM: a factor for each row and for each column
 };
 
 // 8 consecutive entries from i, at any multiple of the entry's size (gfx950
@@ -164,17 +93,6 @@ __device__ __forceinline__ void load_patch(const uint16_t* p, int64_t ld, int64_
   }
 }
 
-// The scale byte of block column kb of one scale row; the block of the last
-// column also writes the row's zero padding.
-__device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, int64_t cols,
-                                          uint32_t byte) {
-  const int64_t ld = scale_ld(cols), nb = ceil_div(cols, kBlock);
-  uint8_t* p = s + row * ld;
-  p[kb] = (uint8_t)byte;
-  if (kb == nb - 1)
-    for (int64_t j = nb; j < ld; ++j) p[j] = 0;
-}
-
 // Thread (ty, tx) = (tid / 16, tid % 16) holds rows 8 ty .. +7, columns
 // 8 tx .. +7 of the tile. PLAIN, TRANS: the forms written; TILES: one scale.
 //
@@ -188,7 +106,10 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t row, int64_t kb, i
 // Measured with inputs from memory, a copy of as many bytes in parentheses:
 // bf16 in both forms 8192 x 2048 17.7 us (14.6), x 4096 33.1 (27.5), x 14336
 // 103 (91).
-template <bool BF, bool TILES, bool PLAIN, bool TRANS>
+//
+// NORM: entry (r, c) is src's times rstd[r] times weight[c], in that order, in
+// fp32: RMS norm's output, whose row sums are there already (rms_norm.hip).
+template <bool BF, bool TILES, bool PLAIN, bool TRANS, bool NORM>
 __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   __shared__ __attribute__((aligned(16))) uint32_t red[4][kBlock / 2];  // maxima by wave
   __shared__ __attribute__((aligned(8))) uint8_t byte_of[2][kBlock];  // scale bytes of rows, columns
@@ -219,11 +140,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
 
   // the entries (bf16: pairs of them), and the maxima of magnitudes of rows
   // 2k, 2k + 1 and of columns 2k, 2k + 1
-  constexpr bool kRows = PLAIN && !TILES, kCols = TRANS || TILES;
-  float v[BF ? 1 : 8][8];
+  constexpr bool kRows = PLAIN && !TILES, kCols = TRANS || TILES, kPairs = BF && !NORM;
+  float v[kPairs ? 1 : 8][8];
   u32x4_a2 w[BF ? 8 : 1];
   uint32_t rmax[4], cmax[4];
-  if constexpr (BF) {
+  if constexpr (kPairs) {
     load_patch(static_cast<const uint16_t*>(src), g.src_ld, r0, c0, rows, cols, w);
     auto maxima = [&](auto clean) {
       uint32_t r[8];
@@ -245,7 +166,35 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
     const uint32_t all = pmax(pmax(any[0], any[1]), pmax(any[2], any[3]));
     if (finite2(all) != all) maxima(std::true_type{});
   } else {
-    load_patch(static_cast<const float*>(src), g.src_ld, r0, c0, rows, cols, v);
+    if constexpr (BF) {
+      load_patch(static_cast<const uint16_t*>(src), g.src_ld, r0, c0, rows, cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i][j] = __uint_as_float(j & 1 ? w[i][j >> 1] & 0xffff0000u : w[i][j >> 1] << 16);
+    } else {
+      load_patch(static_cast<const float*>(src), g.src_ld, r0, c0, rows, cols, v);
+    }
+    if constexpr (NORM) {
+      float by_row[8], by_col[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        by_row[i] = a.rstd[r0 + i < rows ? r0 + i : rows - 1];
+        by_col[i] = a.weight[c0 + i < cols ? c0 + i : cols - 1];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = (v[i][j] * by_row[i]) * by_col[j];
+      // past the matrix: zeros, whatever the factors are
+      if (r0 + 8 > rows || c0 + 8 > cols)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (r0 + i >= rows || c0 + j >= cols) v[i][j] = 0.f;
+    }
     uint32_t r[8], c[8];
     auto maxima = [&](auto clean) {
 #pragma unroll
@@ -303,7 +252,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
     for (int i = 0; i < 8; ++i) {
       const float s = TILES ? scale : i & 1 ? scale_hi(pair[i >> 1]) : scale_lo(pair[i >> 1]);
       uint2 q;
-      if constexpr (BF) {
+      if constexpr (kPairs) {
         q = codes8(w[i][0], w[i][1], w[i][2], w[i][3], s);
       } else {
         q.x = codes4(v[i][0], v[i][1], v[i][2], v[i][3], s);
@@ -348,7 +297,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       uint2 q;
-      if constexpr (BF) {
+      if constexpr (kPairs) {
         auto rows2 = [&](int i) {
           return j & 1 ? high_halves(w[i][j >> 1], w[i + 1][j >> 1]) : low_halves(w[i][j >> 1], w[i + 1][j >> 1]);
         };
@@ -383,15 +332,15 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   }
 }
 
-template <bool BF, bool TILES>
+template <bool BF, bool TILES, bool NORM = false>
 void launch_forms(const Args& a, bool plain, bool trans, hipStream_t s) {
   const dim3 grid((unsigned)(8 * ceil_div(a.tiles, 8))), thr(kThreads);
   if (plain && trans)
-    hipLaunchKernelGGL((k_quantize<BF, TILES, true, true>), grid, thr, 0, s, a);
+    hipLaunchKernelGGL((k_quantize<BF, TILES, true, true, NORM>), grid, thr, 0, s, a);
   else if (plain)
-    hipLaunchKernelGGL((k_quantize<BF, TILES, true, false>), grid, thr, 0, s, a);
+    hipLaunchKernelGGL((k_quantize<BF, TILES, true, false, NORM>), grid, thr, 0, s, a);
   else
-    hipLaunchKernelGGL((k_quantize<BF, TILES, false, true>), grid, thr, 0, s, a);
+    hipLaunchKernelGGL((k_quantize<BF, TILES, false, true, NORM>), grid, thr, 0, s, a);
 }
 
 int launched(const char* what) {
@@ -403,6 +352,28 @@ int launched(const char* what) {
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 }  // namespace
+
+bool tiles_fit(int64_t rows, int64_t cols) { return ceil_div(rows, kBlock) * ceil_div(cols, kBlock) <= kMaxBlocks; }
+
+int quantize_normed(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t src_ld, const float* rstd,
+                    const float* weight, void* codes, void* scales, void* codes_t, void* scales_t, hipStream_t s) {
+  const int64_t tr = ceil_div(rows, kBlock), tc = ceil_div(cols, kBlock);
+  Args a{};
+  a.ngroups = 1;
+  a.g[0] = Group{rows, cols, src_ld, 0, (uint32_t)tc, (uint32_t)(tr * tc), 0};
+  a.tiles = (uint32_t)(tr * tc);
+  a.src = src;
+  a.codes = codes;
+  a.scales = scales;
+  a.codes_t = codes_t;
+  a.scales_t = scales_t;
+  a.rstd = rstd;
+  a.weight = weight;
+  if (dtype == MUONH_DT_BF16) launch_forms<true, false, true>(a, codes != nullptr, codes_t != nullptr, s);
+  else launch_forms<false, false, true>(a, codes != nullptr, codes_t != nullptr, s);
+  return launched("rms norm in 8 bits");
+}
+
 }  // namespace fp8
 }  // namespace muonh
 
@@ -445,7 +416,7 @@ int muonh_fp8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t col
   if (misaligned(codes, 16) || misaligned(codes_t, 16) || misaligned(scales, 4) || misaligned(scales_t, 4))
     return fail(MUONH_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
   const int64_t tr = ceil_div(rows, kBlock), tc = ceil_div(cols, kBlock);
-  if (tr * tc > kMaxBlocks) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more");
+  if (!tiles_fit(rows, cols)) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more");
   const Span spans[5] = {
       span("src", src, ((rows - 1) * src_ld + cols) * esize),
       span("codes", codes, rows * code_ld(cols)),

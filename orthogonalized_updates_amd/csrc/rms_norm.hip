@@ -1,0 +1,777 @@
+// RMS norm with the residual's addition on gfx950, forward and backward (contract:
+// include/muonh.h; the norms' weights are among the parameters that the AdamW
+// step updates, model card "Puro", section "Training").
+//
+//   h = x + residual (rounded to h's type), r = rsqrt(mean(h^2) + eps), y = (h r) w
+//   n = h r, g = dy w:  dh = r (g - n mean(g n)) + dresidual,  dw = sum over rows of dy n
+//
+// Both are bound by memory: every entry is read and written once, and a row
+// stays in the registers of the lanes that share it between the two uses that
+// its sum separates. The norm is of the h that is stored, so that y, the 8-bit
+// forms and the backward pass see one h.
+#include <algorithm>
+
+#include "fp8_codes.h"
+
+namespace muonh {
+namespace norm {
+namespace {
+
+using fp8::ceil_div;
+using fp8::code_ld;
+using fp8::fail;
+using fp8::kBlock;
+using fp8::overlap;
+using fp8::Span;
+using fp8::span;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+// at any multiple of the entry's size (gfx950 takes vector accesses at any address)
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// ---- 8 consecutive entries -----------------------------------------------------
+// As loaded; n: how many of them there are (below 8 only in a row's last vector).
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__bf16> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const __bf16* p) { v = *reinterpret_cast<const u32x4_a2*>(p); }
+  __device__ __forceinline__ void load(const __bf16* p, int n) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    v = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) v[j >> 1] |= (uint32_t)q[j] << (16 * (j & 1));
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16);
+  }
+};
+template <>
+struct Raw<float> {
+  f32x4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = *reinterpret_cast<const f32x4_a4*>(p);
+    v[1] = *reinterpret_cast<const f32x4_a4*>(p + 4);
+  }
+  __device__ __forceinline__ void load(const float* p, int n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = j < n ? p[j] : 0.f;
+  }
+  __device__ __forceinline__ float at(int j) const { return v[j >> 2][j & 3]; }
+};
+
+// Stores the first n of 8 values, each rounded once.
+__device__ __forceinline__ void store8(__bf16* p, const float (&v)[8], int n) {
+  const bf16x8 b = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3],
+                    (__bf16)v[4], (__bf16)v[5], (__bf16)v[6], (__bf16)v[7]};
+  if (n >= 8) {
+    *reinterpret_cast<u32x4_a2*>(p) = __builtin_bit_cast(u32x4, b);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = b[j];
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], int n) {
+  if (n >= 8) {
+    *reinterpret_cast<f32x4_a4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4_a4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = v[j];
+  }
+}
+__device__ __forceinline__ float rounded(float v, float) { return v; }
+__device__ __forceinline__ float rounded(float v, __bf16) { return (float)(__bf16)v; }
+
+// A lane's NV vectors of a row: vector v at column (v LPR + lane) 8. Zeros past
+// the row's end. Where the columns are whole vectors, lanes past the end reload the
+// last one, so that no load waits in a branch.
+template <int LPR, int NV, typename T>
+__device__ __forceinline__ void load_row(const T* p, int lane, int cols, Raw<T> (&raw)[NV]) {
+  if ((cols & 7) == 0) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) raw[v].load(p + min((v * LPR + lane) * 8, cols - 8));
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      if (c + 8 <= cols) raw[v].load(p + c);
+      else raw[v].load(p + c, cols - c);
+    }
+  }
+}
+
+// ---- sums over the lanes of a row, in all of them --------------------------------
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float sum_row16(float v) {
+  v = add_dpp<0xB1>(v);     // quad [1,0,3,2]
+  v = add_dpp<0x4E>(v);     // quad [2,3,0,1]
+  v = add_dpp<0x141>(v);    // mirrored halves: the other quad of 8
+  return add_dpp<0x140>(v); // mirrored row: the other 8
+}
+__device__ __forceinline__ float sum_wave(float v) {
+  v = sum_row16(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+// LPR lanes; above 64 through `part` (one float per wave; the caller alternates
+// between two of them from row to row, so that one barrier is enough).
+template <int LPR>
+__device__ __forceinline__ float sum_lanes(float v, float* part) {
+  if constexpr (LPR == 16) return sum_row16(v);
+  v = sum_wave(v);
+  if constexpr (LPR > 64) {
+    constexpr int W = LPR / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[wave] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += part[w];
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t umax_row16(uint32_t v) {
+  auto other = [](uint32_t a, auto ctrl) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)a, decltype(ctrl)::value, 0xF, 0xF, false);
+  };
+  v = fp8::umax(v, other(v, std::integral_constant<int, 0xB1>{}));
+  v = fp8::umax(v, other(v, std::integral_constant<int, 0x4E>{}));
+  v = fp8::umax(v, other(v, std::integral_constant<int, 0x141>{}));
+  return fp8::umax(v, other(v, std::integral_constant<int, 0x140>{}));
+}
+
+// ---- forward ----------------------------------------------------------------------
+enum Out { kNone, kPlain, kCodes };  // beside h and r: nothing, y, y's 8-bit rows
+struct FwdArgs {
+  const void* x;
+  const void* res;  // or nullptr: h = x, not stored
+  void* h;
+  const float* w;
+  float* rstd;
+  void* y;
+  uint8_t *codes, *scales;
+  int64_t rows, x_ld, res_ld, h_ld, y_ld;
+  int cols, y_bf;
+  float inv_cols, eps;
+};
+
+// One vector of y: columns c .. c + 7 of a row. In the kCodes form 16
+// neighbouring lanes hold a block of 128, all of them call.
+template <int OUT>
+__device__ __forceinline__ void emit(const FwdArgs& a, int64_t row, int c, bool live, float (&y)[8]) {
+  const int n = a.cols - c;
+  if constexpr (OUT == kPlain) {
+    if (!live || n <= 0) return;
+    if (a.y_bf) store8(static_cast<__bf16*>(a.y) + row * a.y_ld + c, y, n);
+    else store8(static_cast<float*>(a.y) + row * a.y_ld + c, y, n);
+  } else if constexpr (OUT == kCodes) {
+    if (n < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= n) y[j] = 0.f;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = __float_as_uint(y[j]) & 0x7fffffffu;
+      m = fp8::umax(m, b < 0x7f800000u ? b : 0u);
+    }
+    m = umax_row16(m);
+    const uint32_t byte = fp8::scale_bytes2((m + 0xffffu) >> 16) & 0xffffu;
+    const float s = fp8::scale_lo(byte);
+    const int64_t ld = code_ld(a.cols);
+    if (live && c < ld) {
+      const uint2 q = make_uint2(fp8::codes4(y[0], y[1], y[2], y[3], s), fp8::codes4(y[4], y[5], y[6], y[7], s));
+      *reinterpret_cast<uint2*>(a.codes + row * ld + c) = q;
+      if ((c & (kBlock - 1)) == 0) fp8::put_scale(a.scales, row, c / kBlock, a.cols, byte);
+    }
+  }
+}
+
+// LPR lanes share a row, NV vectors of 8 each: a row is read once and stays in
+// registers. A workgroup goes on to further rows with the weights it holds.
+template <typename TX, typename TH, int LPR, int NV, int OUT>
+__global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void k_norm(FwdArgs a) {
+  constexpr int kRows = LPR < 256 ? 256 / LPR : 1;
+  __shared__ float part[2][LPR > 64 ? LPR / 64 : 1];
+  const int lane = threadIdx.x & (LPR - 1);
+  Raw<float> w[NV];
+  if constexpr (OUT != kNone) load_row<LPR, NV>(a.w, lane, a.cols, w);
+  int turn = 0;
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += (int64_t)gridDim.x * kRows) {
+    const int64_t mine = first + threadIdx.x / LPR;
+    const bool live = mine < a.rows;
+    const int64_t row = live ? mine : a.rows - 1;
+    Raw<TX> x[NV];
+    Raw<TH> res[NV];
+    load_row<LPR, NV>(static_cast<const TX*>(a.x) + row * a.x_ld, lane, a.cols, x);
+    if (a.res) load_row<LPR, NV>(static_cast<const TH*>(a.res) + row * a.res_ld, lane, a.cols, res);
+    float h[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        h[v][j] = x[v].at(j);
+        if (a.res) h[v][j] = rounded(h[v][j] + res[v].at(j), TH{});
+      }
+      if (c < a.cols) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = __builtin_fmaf(h[v][j], h[v][j], s);
+        ss += s;
+        if (a.res && live) store8(static_cast<TH*>(a.h) + row * a.h_ld + c, h[v], a.cols - c);
+      }
+    }
+    ss = sum_lanes<LPR>(ss, part[turn]);
+    turn ^= 1;
+    const float r = rsqrtf(ss * a.inv_cols + a.eps);
+    if (live && lane == 0) a.rstd[row] = r;
+    if constexpr (OUT != kNone) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (h[v][j] * r) * w[v].at(j);
+        emit<OUT>(a, row, (v * LPR + lane) * 8, live, y);
+      }
+    }
+  }
+}
+
+// Rows of any length: a workgroup to a row, which it reads twice.
+template <typename TX, typename TH, int OUT>
+__global__ __launch_bounds__(1024) void k_norm_long(FwdArgs a) {
+  __shared__ float part[2][16];
+  int turn = 0;
+  const int width = (int)ceil_div(a.cols, kBlock) * kBlock;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const TX* px = static_cast<const TX*>(a.x) + row * a.x_ld;
+    TH* ph = static_cast<TH*>(a.h) + row * a.h_ld;
+    float ss = 0.f;
+    for (int c = threadIdx.x * 8; c < a.cols; c += 8192) {
+      const int n = a.cols - c;
+      Raw<TX> x;
+      if (n >= 8) x.load(px + c);
+      else x.load(px + c, n);
+      float h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = x.at(j);
+      if (a.res) {
+        const TH* pr = static_cast<const TH*>(a.res) + row * a.res_ld + c;
+        Raw<TH> res;
+        if (n >= 8) res.load(pr);
+        else res.load(pr, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = rounded(h[j] + res.at(j), TH{});
+        store8(ph + c, h, n);
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = __builtin_fmaf(h[j], h[j], s);
+      ss += s;
+    }
+    ss = sum_lanes<1024>(ss, part[turn]);
+    turn ^= 1;
+    const float r = rsqrtf(ss * a.inv_cols + a.eps);
+    if (threadIdx.x == 0) a.rstd[row] = r;
+    if constexpr (OUT != kNone) {
+      // whole rows of 16 lanes stay together: blocks of 128 columns
+      for (int c = threadIdx.x * 8; c < width; c += 8192) {
+        const int n = a.cols - c;
+        float y[8];
+        Raw<float> w;
+        if (n >= 8) w.load(a.w + c);
+        else w.load(a.w + c, n);
+        auto scaled = [&](const auto& raw) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = (raw.at(j) * r) * w.at(j);
+        };
+        if (a.res) {  // what this thread stored above
+          Raw<TH> q;
+          if (n >= 8) q.load(ph + c);
+          else q.load(ph + c, n);
+          scaled(q);
+        } else {
+          Raw<TX> q;
+          if (n >= 8) q.load(px + c);
+          else q.load(px + c, n);
+          scaled(q);
+        }
+        emit<OUT>(a, row, c, true, y);
+      }
+    }
+  }
+}
+
+constexpr int kMaxGrid = 1 << 20;  // workgroups of up to 1024 threads: below 2^32 threads
+
+template <typename TX, typename TH, int OUT>
+void launch_norm(const FwdArgs& a, hipStream_t s) {
+  auto grid = [&](int per) { return dim3((unsigned)std::min<int64_t>(ceil_div(a.rows, per), kMaxGrid)); };
+  const int vecs = (int)ceil_div(a.cols, 8);
+#define MUONH_NORM(LPR, NV)                                                                              \
+  hipLaunchKernelGGL((k_norm<TX, TH, LPR, NV, OUT>), grid(LPR < 256 ? 256 / LPR : 1), dim3(LPR < 256 ? 256 : LPR), \
+                     0, s, a)
+  if (vecs <= 16) MUONH_NORM(16, 1);
+  else if (vecs <= 256 && a.rows <= 256) MUONH_NORM(256, 1);
+  else if (vecs <= 64) MUONH_NORM(64, 1);
+  else if (vecs <= 128) MUONH_NORM(64, 2);
+  else if (vecs <= 192) MUONH_NORM(64, 3);
+  else if (vecs <= 256) MUONH_NORM(64, 4);
+  else if (vecs <= 512) MUONH_NORM(256, 2);
+  else if (vecs <= 1024) MUONH_NORM(256, 4);
+  else if (vecs <= 2048) MUONH_NORM(1024, 2);
+  else if (vecs <= 4096) MUONH_NORM(1024, 4);
+  else hipLaunchKernelGGL((k_norm_long<TX, TH, OUT>), grid(1), dim3(1024), 0, s, a);
+#undef MUONH_NORM
+}
+template <typename TX, typename TH>
+void launch_norm(const FwdArgs& a, Out out, hipStream_t s) {
+  if (out == kNone) launch_norm<TX, TH, kNone>(a, s);
+  else if (out == kPlain) launch_norm<TX, TH, kPlain>(a, s);
+  else launch_norm<TX, TH, kCodes>(a, s);
+}
+
+// ---- backward ---------------------------------------------------------------------
+struct BwdArgs {
+  const void* dy;
+  const void* h;
+  const float *w, *rstd;
+  const void* dres;  // or nullptr
+  void* dh;
+  float* part;       // [groups][cols]: sums of dy n over each group's rows
+  float* mean;       // [rows]: mean(g n), of k_norm_dots
+  int64_t rows, dy_ld, h_ld, dres_ld, dh_ld;
+  int cols, groups;
+  float inv_cols;
+};
+
+// As k_norm: LPR lanes share a row, whose dy and h they hold. Each workgroup
+// takes every gridDim-th set of rows and keeps its lanes' columns of dw in
+// registers, one partial sum per workgroup at the end.
+template <typename TD, typename TH, int LPR, int NV>
+__global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void k_norm_back(BwdArgs a) {
+  constexpr int kRows = LPR < 256 ? 256 / LPR : 1;
+  __shared__ float part[2][LPR > 64 ? LPR / 64 : 1];
+  __shared__ float sums[kRows > 1 ? kRows : 1][kRows > 1 ? LPR * NV * 8 : 1];
+  const int lane = threadIdx.x & (LPR - 1), group = threadIdx.x / LPR;
+  Raw<float> w[NV];
+  load_row<LPR, NV>(a.w, lane, a.cols, w);
+  float dw[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[v][j] = 0.f;
+  int turn = 0;
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += (int64_t)gridDim.x * kRows) {
+    const bool live = first + group < a.rows;
+    const int64_t row = live ? first + group : a.rows - 1;
+    Raw<TD> dy[NV];
+    Raw<TH> h[NV], res[NV];
+    load_row<LPR, NV>(static_cast<const TD*>(a.dy) + row * a.dy_ld, lane, a.cols, dy);
+    load_row<LPR, NV>(static_cast<const TH*>(a.h) + row * a.h_ld, lane, a.cols, h);
+    if (a.dres) load_row<LPR, NV>(static_cast<const TH*>(a.dres) + row * a.dres_ld, lane, a.cols, res);
+    const float r = a.rstd[row];
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if ((v * LPR + lane) * 8 < a.cols && live) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float t = dy[v].at(j) * (h[v].at(j) * r);
+          dw[v][j] += t;
+          s += t * w[v].at(j);
+        }
+        dot += s;
+      }
+    }
+    const float mean = sum_lanes<LPR>(dot, part[turn]) * a.inv_cols;
+    turn ^= 1;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      if (c >= a.cols || !live) continue;
+      float d[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        d[j] = (dy[v].at(j) * w[v].at(j) - (h[v].at(j) * r) * mean) * r;
+        if (a.dres) d[j] += res[v].at(j);
+      }
+      store8(static_cast<TH*>(a.dh) + row * a.dh_ld + c, d, a.cols - c);
+    }
+  }
+  float* out = a.part + (int64_t)blockIdx.x * a.cols;
+  if constexpr (kRows > 1) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[group][(v * LPR + lane) * 8 + j] = dw[v][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      float s = sums[0][c];
+#pragma unroll
+      for (int k = 1; k < kRows; ++k) s += sums[k][c];
+      out[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      if (c < a.cols) store8(out + c, dw[v], a.cols - c);
+    }
+  }
+}
+
+// Rows of any length: mean(g n) of each row first, then the rest by slabs of
+// 2048 columns, in which a thread has 8 columns of every row of its group.
+template <typename TD, typename TH>
+__global__ __launch_bounds__(1024) void k_norm_dots(BwdArgs a) {
+  __shared__ float part[2][16];
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const TD* pd = static_cast<const TD*>(a.dy) + row * a.dy_ld;
+    const TH* ph = static_cast<const TH*>(a.h) + row * a.h_ld;
+    const float r = a.rstd[row];
+    float dot = 0.f;
+    for (int c = threadIdx.x * 8; c < a.cols; c += 8192) {
+      const int n = a.cols - c;
+      Raw<TD> dy;
+      Raw<TH> h;
+      Raw<float> w;
+      if (n >= 8) {
+        dy.load(pd + c);
+        h.load(ph + c);
+        w.load(a.w + c);
+      } else {
+        dy.load(pd + c, n);
+        h.load(ph + c, n);
+        w.load(a.w + c, n);
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) s += (dy.at(j) * (h.at(j) * r)) * w.at(j);
+      dot += s;
+    }
+    dot = sum_lanes<1024>(dot, part[turn]);
+    turn ^= 1;
+    if (threadIdx.x == 0) a.mean[row] = dot * a.inv_cols;
+  }
+}
+template <typename TD, typename TH>
+__global__ __launch_bounds__(256) void k_norm_back_long(BwdArgs a) {
+  const int c = ((int)blockIdx.x * 256 + threadIdx.x) * 8, n = a.cols - c;
+  if (n <= 0) return;
+  Raw<float> w;
+  if (n >= 8) w.load(a.w + c);
+  else w.load(a.w + c, n);
+  float dw[8] = {};
+  for (int64_t row = blockIdx.y; row < a.rows; row += a.groups) {
+    const TD* pd = static_cast<const TD*>(a.dy) + row * a.dy_ld + c;
+    const TH* ph = static_cast<const TH*>(a.h) + row * a.h_ld + c;
+    Raw<TD> dy;
+    Raw<TH> h, res;
+    if (n >= 8) {
+      dy.load(pd);
+      h.load(ph);
+    } else {
+      dy.load(pd, n);
+      h.load(ph, n);
+    }
+    if (a.dres) {
+      const TH* pr = static_cast<const TH*>(a.dres) + row * a.dres_ld + c;
+      if (n >= 8) res.load(pr);
+      else res.load(pr, n);
+    }
+    const float r = a.rstd[row], mean = a.mean[row];
+    float d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float nh = h.at(j) * r;
+      dw[j] += dy.at(j) * nh;
+      d[j] = (dy.at(j) * w.at(j) - nh * mean) * r;
+      if (a.dres) d[j] += res.at(j);
+    }
+    store8(static_cast<TH*>(a.dh) + row * a.dh_ld + c, d, n);
+  }
+  store8(a.part + (int64_t)blockIdx.y * a.cols + c, dw, n);
+}
+
+// dw[c] (+)= the groups' partial sums, in a fixed order: 32 columns per
+// workgroup, 32 lanes of groups each, then those 32 sums.
+__global__ __launch_bounds__(1024) void k_norm_join(const float* part, int groups, int cols, float* dw, int accumulate) {
+  __shared__ float sums[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = (int)blockIdx.x * 32 + x;
+  float s = 0.f;
+  if (c < cols)
+    for (int g = y; g < groups; g += 32) s += part[(int64_t)g * cols + c];
+  sums[y][x] = s;
+  __syncthreads();
+  if (y == 0 && c < cols) {
+    s = sums[0][x];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) s += sums[k][x];
+    dw[c] = accumulate ? dw[c] + s : s;
+  }
+}
+
+constexpr int kBackCols = 8192;  // longer rows go through k_norm_dots
+// Workgroups, and so partial sums of dw.
+int back_groups(int64_t rows, int64_t cols) {
+  if (cols > kBackCols) return (int)std::min<int64_t>(rows, 64);
+  const int per = cols <= 128 ? 16 : cols <= 2048 ? 4 : 1;  // rows at a time
+  return (int)std::min<int64_t>(ceil_div(rows, per), 512);
+}
+size_t back_bytes(int64_t rows, int64_t cols) {
+  const size_t part = (size_t)back_groups(rows, cols) * (size_t)cols * sizeof(float);
+  return part + (cols > kBackCols ? (size_t)rows * sizeof(float) : 0);
+}
+
+template <typename TD, typename TH>
+void launch_back(BwdArgs a, hipStream_t s) {
+  const int vecs = (int)ceil_div(a.cols, 8);
+  const dim3 grid((unsigned)a.groups);
+#define MUONH_NORM(LPR, NV) \
+  hipLaunchKernelGGL((k_norm_back<TD, TH, LPR, NV>), grid, dim3(LPR < 256 ? 256 : LPR), 0, s, a)
+  if (vecs <= 16) MUONH_NORM(16, 1);
+  else if (vecs <= 64) MUONH_NORM(64, 1);
+  else if (vecs <= 128) MUONH_NORM(64, 2);
+  else if (vecs <= 192) MUONH_NORM(64, 3);
+  else if (vecs <= 256) MUONH_NORM(64, 4);
+  else if (vecs <= 512) MUONH_NORM(256, 2);
+  else if (vecs <= 1024) MUONH_NORM(256, 4);
+  else {
+    hipLaunchKernelGGL((k_norm_dots<TD, TH>), dim3((unsigned)std::min<int64_t>(a.rows, kMaxGrid)), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((k_norm_back_long<TD, TH>), dim3((unsigned)ceil_div(vecs, 256), (unsigned)a.groups), dim3(256),
+                       0, s, a);
+  }
+#undef MUONH_NORM
+}
+
+bool bad_dtype(int32_t d) { return d != MUONH_DT_FP32 && d != MUONH_DT_BF16; }
+int size_of(int32_t d) { return d == MUONH_DT_BF16 ? 2 : 4; }
+
+// A mean over no columns is no number: refused.
+int check_shape(int64_t rows, int64_t cols) {
+  if (fp8::bad_dim(rows) || fp8::bad_dim(cols) || cols == 0)
+    return fail(MUONH_ESHAPE, "%lld x %lld: rows out of [0, %d] or columns out of [1, %d]", (long long)rows,
+                (long long)cols, MUONH_MAX_FP8_DIM, MUONH_MAX_FP8_DIM);
+  return MUONH_OK;
+}
+
+// A 2-d argument: rows of `cols` entries, ld apart.
+struct Mat {
+  const char* name;
+  const void* p;
+  int32_t dtype;
+  int64_t ld;
+};
+int check_mat(const Mat& m, int64_t cols) {
+  if (!m.p) return fail(MUONH_EINVAL, "%s is NULL", m.name);
+  if (reinterpret_cast<uintptr_t>(m.p) & (uintptr_t)(size_of(m.dtype) - 1))
+    return fail(MUONH_EINVAL, "%s is not aligned to its type", m.name);
+  if (m.ld < cols || m.ld > (1LL << 36))
+    return fail(MUONH_EINVAL, "%s's row pitch %lld out of [cols=%lld, 2^36]", m.name, (long long)m.ld, (long long)cols);
+  return MUONH_OK;
+}
+Span span_of(const Mat& m, int64_t rows, int64_t cols) {
+  return span(m.name, m.p, m.p ? ((rows - 1) * m.ld + cols) * size_of(m.dtype) : 0);
+}
+bool same(const Mat& a, const Mat& b) { return a.p == b.p && a.ld == b.ld && a.dtype == b.dtype; }
+
+int launched(const char* what) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(MUONH_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
+  return MUONH_OK;
+}
+
+}  // namespace
+}  // namespace norm
+}  // namespace muonh
+
+extern "C" {
+
+int muonh_rms_norm(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t x_ld, const void* residual,
+                   int32_t h_dtype, int64_t residual_ld, void* h, int64_t h_ld, const float* weight, float eps,
+                   float* rstd, void* y, int32_t y_dtype, int64_t y_ld, void* codes, void* scales, void* codes_t,
+                   void* scales_t, void* stream) {
+  using namespace muonh;
+  using namespace muonh::norm;
+  if (bad_dtype(x_dtype)) return fail(MUONH_EINVAL, "x_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", x_dtype);
+  if (residual && bad_dtype(h_dtype))
+    return fail(MUONH_EINVAL, "h_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", h_dtype);
+  if (y && bad_dtype(y_dtype)) return fail(MUONH_EINVAL, "y_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", y_dtype);
+  if (const int err = check_shape(rows, cols)) return err;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return fail(MUONH_EINVAL, "eps=%g must be finite and >= 0", (double)eps);
+  if (rows == 0) return MUONH_OK;
+  if (!codes != !scales || !codes_t != !scales_t)
+    return fail(MUONH_EINVAL, "codes and scales (codes_t and scales_t) go together");
+  if (!y == !(codes || codes_t)) return fail(MUONH_EINVAL, "either y or 8-bit forms");
+  if (!residual != !h) return fail(MUONH_EINVAL, "residual and h go together");
+  const Mat in = {"x", x, x_dtype, x_ld}, res = {"residual", residual, h_dtype, residual_ld}, sum = {"h", h, h_dtype, h_ld},
+            out = {"y", y, y_dtype, y_ld};
+  if (const int err = check_mat(in, cols)) return err;
+  if (residual) {
+    if (const int err = check_mat(res, cols)) return err;
+    if (const int err = check_mat(sum, cols)) return err;
+  }
+  if (y)
+    if (const int err = check_mat(out, cols)) return err;
+  auto off = [](const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; };
+  if (!weight || off(weight, 4)) return fail(MUONH_EINVAL, "weight must be a 4-byte aligned array of cols floats");
+  if (!rstd || off(rstd, 4)) return fail(MUONH_EINVAL, "rstd must be a 4-byte aligned array of rows floats");
+  if (off(codes, 16) || off(codes_t, 16) || off(scales, 4) || off(scales_t, 4))
+    return fail(MUONH_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
+  if (codes_t && !fp8::tiles_fit(rows, cols)) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more");
+  const Span read[3] = {span_of(in, rows, cols), span_of(res, rows, cols), span("weight", weight, cols * 4)};
+  const Span written[7] = {span_of(sum, rows, cols),
+                           span_of(out, rows, cols),
+                           span("rstd", rstd, rows * 4),
+                           span("codes", codes, rows * code_ld(cols)),
+                           span("scales", scales, rows * fp8::scale_ld(cols)),
+                           span("codes_t", codes_t, cols * code_ld(rows)),
+                           span("scales_t", scales_t, cols * fp8::scale_ld(rows))};
+  for (int i = 0; i < 7; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      // h may take the place of x or of the residual, entry by entry
+      if (i == 0 && ((j == 0 && same(sum, in)) || (j == 1 && same(sum, res)))) continue;
+      if (overlap(written[i], read[j])) return fail(MUONH_EALIAS, "%s overlaps %s", written[i].name, read[j].name);
+    }
+    for (int j = i + 1; j < 7; ++j)
+      if (overlap(written[i], written[j]))
+        return fail(MUONH_EALIAS, "%s overlaps %s", written[j].name, written[i].name);
+  }
+
+  FwdArgs a{};
+  a.x = x;
+  a.res = residual;
+  a.h = h;
+  a.w = weight;
+  a.rstd = rstd;
+  a.y = y;
+  a.rows = rows;
+  a.x_ld = x_ld;
+  a.res_ld = residual_ld;
+  a.h_ld = h_ld;
+  a.y_ld = y_ld;
+  a.cols = (int)cols;
+  a.y_bf = y_dtype == MUONH_DT_BF16;
+  a.inv_cols = (float)(1.0 / (double)cols);
+  a.eps = eps;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = static_cast<uint8_t*>(scales);
+  // The transposed form groups along rows, so it needs whole 128 x 128 tiles
+  // after the rows' sums: a second pass over h writes the 8-bit forms.
+  const Out form = y ? kPlain : codes_t ? kNone : kCodes;
+  const int32_t hd = residual ? h_dtype : x_dtype;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (x_dtype == MUONH_DT_BF16) {
+    if (hd == MUONH_DT_BF16) launch_norm<__bf16, __bf16>(a, form, s);
+    else launch_norm<__bf16, float>(a, form, s);
+  } else {
+    if (hd == MUONH_DT_BF16) launch_norm<float, __bf16>(a, form, s);
+    else launch_norm<float, float>(a, form, s);
+  }
+  if (const int err = launched("rms norm")) return err;
+  if (!codes_t) return MUONH_OK;
+  return fp8::quantize_normed(residual ? h : x, hd, rows, cols, residual ? h_ld : x_ld, rstd, weight, codes, scales,
+                              codes_t, scales_t, s);
+}
+
+size_t muonh_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  using namespace muonh;
+  if (fp8::bad_dim(rows) || fp8::bad_dim(cols) || rows == 0 || cols == 0) return 0;
+  return norm::back_bytes(rows, cols);
+}
+
+int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, const void* h, int32_t h_dtype,
+                            int64_t rows, int64_t cols, int64_t h_ld, const float* weight, const float* rstd,
+                            const void* dresidual, int64_t dresidual_ld, void* dh, int64_t dh_ld, float* dweight,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace muonh;
+  using namespace muonh::norm;
+  if (bad_dtype(dy_dtype)) return fail(MUONH_EINVAL, "dy_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", dy_dtype);
+  if (bad_dtype(h_dtype)) return fail(MUONH_EINVAL, "h_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", h_dtype);
+  if (const int err = check_shape(rows, cols)) return err;
+  auto off = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; };
+  if (!dweight || off(dweight)) return fail(MUONH_EINVAL, "dweight must be a 4-byte aligned array of cols floats");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const dim3 join((unsigned)ceil_div(cols, 32));
+  if (rows == 0) {  // the sum over no rows
+    if (!accumulate) hipLaunchKernelGGL(k_norm_join, join, dim3(1024), 0, s, nullptr, 0, (int)cols, dweight, 0);
+    return launched("rms norm backward");
+  }
+  const Mat d = {"dy", dy, dy_dtype, dy_ld}, x = {"h", h, h_dtype, h_ld}, res = {"dresidual", dresidual, h_dtype, dresidual_ld},
+            out = {"dh", dh, h_dtype, dh_ld};
+  if (const int err = check_mat(d, cols)) return err;
+  if (const int err = check_mat(x, cols)) return err;
+  if (dresidual)
+    if (const int err = check_mat(res, cols)) return err;
+  if (const int err = check_mat(out, cols)) return err;
+  if (!weight || off(weight)) return fail(MUONH_EINVAL, "weight must be a 4-byte aligned array of cols floats");
+  if (!rstd || off(rstd)) return fail(MUONH_EINVAL, "rstd must be a 4-byte aligned array of rows floats");
+  const size_t need = back_bytes(rows, cols);
+  if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the call needs %zu bytes", need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MUONH_EWORKSPACE, "workspace must be 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(MUONH_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
+  const Span read[5] = {span_of(d, rows, cols), span_of(x, rows, cols), span_of(res, rows, cols),
+                        span("weight", weight, cols * 4), span("rstd", rstd, rows * 4)};
+  const Span written[3] = {span_of(out, rows, cols), span("dweight", dweight, cols * 4),
+                           span("workspace", workspace, (int64_t)need)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j) {
+      // dh may take the place of dy or of dresidual, entry by entry
+      if (i == 0 && ((j == 0 && same(out, d)) || (j == 2 && same(out, res)))) continue;
+      if (overlap(written[i], read[j])) return fail(MUONH_EALIAS, "%s overlaps %s", written[i].name, read[j].name);
+    }
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(written[i], written[j]))
+        return fail(MUONH_EALIAS, "%s overlaps %s", written[j].name, written[i].name);
+  }
+
+  BwdArgs a{};
+  a.dy = dy;
+  a.h = h;
+  a.w = weight;
+  a.rstd = rstd;
+  a.dres = dresidual;
+  a.dh = dh;
+  a.rows = rows;
+  a.dy_ld = dy_ld;
+  a.h_ld = h_ld;
+  a.dres_ld = dresidual_ld;
+  a.dh_ld = dh_ld;
+  a.cols = (int)cols;
+  a.groups = back_groups(rows, cols);
+  a.inv_cols = (float)(1.0 / (double)cols);
+  a.part = static_cast<float*>(workspace);
+  a.mean = a.part + (size_t)a.groups * (size_t)cols;
+  if (dy_dtype == MUONH_DT_BF16) {
+    if (h_dtype == MUONH_DT_BF16) launch_back<__bf16, __bf16>(a, s);
+    else launch_back<__bf16, float>(a, s);
+  } else {
+    if (h_dtype == MUONH_DT_BF16) launch_back<float, __bf16>(a, s);
+    else launch_back<float, float>(a, s);
+  }
+  hipLaunchKernelGGL(k_norm_join, join, dim3(1024), 0, s, a.part, a.groups, (int)cols, dweight, accumulate != 0);
+  return launched("rms norm backward");
+}
+
+}  // extern "C"
