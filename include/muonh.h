@@ -489,6 +489,41 @@ int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, con
                             int64_t dresidual_ld, void* dh, int64_t dh_ld, float* dweight,
                             int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Embedding lookup: out[t] = scale * table[ids[t] - first], rounded once, for
+ * t < n; an id that is no row (below `first`, or first + rows or above: padding,
+ * or a row of another part of a table split by rows) gives zeros.
+ * ids: DEVICE, n integers of id_bytes (4 or 8) bytes, signed; n in [0,
+ * MUONH_MAX_FP8_DIM]. table: DEVICE, rows x cols of table_dtype, pitch table_ld;
+ * out: n x cols of out_dtype, pitch out_ld. first >= 0, scale finite.
+ * Asynchronous on `stream`, capturable.
+ * Errors: MUONH_EINVAL (NULL or misaligned argument, bad dtype, id_bytes, pitch, scale
+ * or first), MUONH_ESHAPE (n or a dim out of range, a table of no rows), MUONH_EALIAS
+ * (out overlaps an input), MUONH_EHIP.
+ */
+int muonh_embedding(const void* ids, int32_t id_bytes, int64_t n, int64_t first, const void* table,
+                    int32_t table_dtype, int64_t rows, int64_t cols, int64_t table_ld, float scale,
+                    void* out, int32_t out_dtype, int64_t out_ld, void* stream);
+
+/*
+ * Its gradient: grad[v] = scale * (sum of dy[t] over the t with ids[t] - first = v), zeros
+ * where there is none, or added to grad's old values if `accumulate`, which then reads and
+ * writes the rows that occur only. Ids that are no row have no part in it. grad: DEVICE, rows x cols
+ * fp32, pitch grad_ld (the gradient that muonh_adamw_step reads); dy: n x cols of dy_dtype.
+ * The tokens are sorted by their rows, stably, and each row's sum is taken in
+ * fp32 in an order that n, cols and the ids fix: deterministic, no atomics.
+ * workspace: DEVICE, 256-byte aligned, at least
+ * muonh_embedding_backward_workspace_bytes(n, cols) bytes; calls in flight at once
+ * need workspaces of their own. Asynchronous on `stream`, capturable.
+ * Errors: as muonh_embedding (rows may be 0), MUONH_ESHAPE also where dy has more than 2^38
+ * entries, MUONH_EWORKSPACE.
+ */
+size_t muonh_embedding_backward_workspace_bytes(int64_t n, int64_t cols);
+int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64_t first,
+                             const void* dy, int32_t dy_dtype, int64_t dy_ld, float scale, float* grad,
+                             int64_t rows, int64_t cols, int64_t grad_ld, int32_t accumulate,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* muonh_status_string(int status);
 

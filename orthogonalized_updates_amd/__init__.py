@@ -140,6 +140,10 @@ def _load_library() -> ctypes.CDLL:
         "muonh_rms_norm_backward_workspace_bytes": (sz, [i64, i64]),
         "muonh_rms_norm_backward": (ctypes.c_int, [vp, i32, i64, vp, i32, i64, i64, i64, vp, vp, vp, i64,
                                                    vp, i64, vp, i32, vp, sz, vp]),
+        "muonh_embedding": (ctypes.c_int, [vp, i32, i64, i64, vp, i32, i64, i64, i64, f32, vp, i32, i64, vp]),
+        "muonh_embedding_backward_workspace_bytes": (sz, [i64, i64]),
+        "muonh_embedding_backward": (ctypes.c_int, [vp, i32, i64, i64, vp, i32, i64, f32, vp, i64, i64, i64,
+                                                    i32, vp, sz, vp]),
         "muonh_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "muonh_last_error": (ctypes.c_char_p, []),
     }
@@ -509,7 +513,8 @@ __all__ = ["MuonH", "Plan", "MuonHError", "GroupDesc", "get_lib", "check", "LIB_
            "MUONH_NOALLOC_WORKSPACE_BYTES", "AdamW",
            "PTR_CACHE_ENTRIES", "Fp8Matrix", "Fp8Weights", "fp8_quantize", "fp8_matmul",
            "MUONH_FP8_ROWS", "MUONH_FP8_TILES", "MUONH_FP8_FAST", "MUONH_DT_FP32", "MUONH_DT_BF16",
-           "MUONH_MAX_FP8_DIM", "rms_norm", "rms_norm_fp8", "rms_norm_backward"]
+           "MUONH_MAX_FP8_DIM", "rms_norm", "rms_norm_fp8", "rms_norm_backward",
+           "embedding", "embedding_backward"]
 
 
 class AdamW:
@@ -1013,3 +1018,82 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual=None, out=None, dweight=Non
         if o is not None:
             _written(o)
     return dh, dw
+
+
+# -- embedding -------------------------------------------------------------------
+def _ids(ids, dev) -> int:
+    """Bytes per id of a contiguous int32 or int64 tensor."""
+    import torch
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be an int32 or int64 torch tensor")
+    if ids.device != dev or not ids.is_contiguous():
+        raise ValueError(f"ids must be contiguous and on {dev}")
+    return ids.element_size()
+
+
+def _by_token(name: str, t, ids, cols: int):
+    """A tensor of shape ids.shape + (cols,) as one row per token."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if tuple(t.shape) != (*ids.shape, cols):
+        raise ValueError(f"{name} must have shape {(*ids.shape, cols)}, got {tuple(t.shape)}")
+    try:
+        return t.view(ids.numel(), cols)
+    except RuntimeError:
+        raise ValueError(f"{name}'s tokens must lie at one distance from each other") from None
+
+
+def embedding(ids, table, scale: float = 1.0, out=None, out_dtype=None, first: int = 0):
+    """out[...] = scale * table[ids[...] - first] (muonh_embedding); an id that is
+    no row of the table (padding, or a row of another part of it) gives zeros.
+
+    ids: a contiguous int32 or int64 tensor of any shape; table: a 2-d fp32 or
+    bf16 tensor whose rows are contiguous; out: a tensor of shape ids.shape +
+    (columns,), otherwise a new one of out_dtype (default: the table's type). Runs on the
+    current stream of the table's device, outside autograd: embedding_backward is
+    the gradient.
+    """
+    import torch
+    dt, ld = _rows("table", table, getattr(table, "device", None))
+    dev = table.device
+    nbytes = _ids(ids, dev)
+    rows, cols = table.shape
+    y = out
+    if y is None:
+        y = torch.empty((*ids.shape, cols), dtype=table.dtype if out_dtype is None else out_dtype, device=dev)
+    flat = _by_token("out", y, ids, cols)
+    odt, old = _rows("out", flat, dev, None, out_dtype)
+    _on_device(torch, dev, get_lib().muonh_embedding, ids.data_ptr(), nbytes, ids.numel(), int(first), table.data_ptr(),
+               dt, rows, cols, ld, float(scale), flat.data_ptr(), odt, old)
+    if out is not None:
+        _written(out)
+    return y
+
+
+def embedding_backward(ids, dy, out, scale: float = 1.0, accumulate: bool = False, first: int = 0):
+    """out[v] = scale * (sum of dy over the tokens with ids - first = v), zeros
+    where there is none, or added to out's old values with accumulate=True
+    (muonh_embedding_backward). Returns out.
+
+    ids: as for embedding; dy: fp32 or bf16, shape ids.shape + (columns,); out: the
+    table's gradient, 2-d fp32 with contiguous rows (AdamW.step reads it). Deterministic. Runs on the
+    current stream of out's device.
+    """
+    import torch
+    _, ld = _rows("out", out, getattr(out, "device", None), None, torch.float32)
+    dev = out.device
+    nbytes = _ids(ids, dev)
+    rows, cols = out.shape
+    flat = _by_token("dy", dy, ids, cols)
+    ddt, dld = _rows("dy", flat, dev)
+    lib = get_lib()
+    n = ids.numel()
+    size = lib.muonh_embedding_backward_workspace_bytes(n, cols)
+    # from torch's allocator on the current stream, as fp8_matmul's
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _on_device(torch, dev, lib.muonh_embedding_backward, ids.data_ptr(), nbytes, n, int(first), flat.data_ptr(), ddt, dld,
+               float(scale), out.data_ptr(), rows, cols, ld, 1 if accumulate else 0, None if ws is None else ws.data_ptr(),
+               size)
+    _written(out)
+    return out

@@ -15,7 +15,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libmuonh.so"
 SOURCES = ["muonh_abi.hip", "ns_gemm.hip", "elementwise.hip", "adamw.hip", "fp8_quantize.hip",
-           "fp8_matmul.hip", "rms_norm.hip"]
+           "fp8_matmul.hip", "rms_norm.hip", "embedding.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,629 @@
+// Embedding lookup with scaling and its gradient on gfx950 (contract:
+// include/muonh.h; the table is the largest of the parameters that the AdamW step
+// updates, model card "Puro", section "Training").
+//
+//   out[t] = scale * table[ids[t]];   G[v] (+)= scale * sum of dy[t] over ids[t] = v
+//
+// Both are bound by memory. The gradient sorts the tokens by id, stably, so
+// that a row of G is read and written once, by whom is known, and its sum has a fixed
+// order: no atomics, the same bits every time.
+#include <algorithm>
+
+#include "fp8_internal.h"
+#include "rows.h"
+
+namespace muonh {
+namespace embed {
+namespace {
+
+using fp8::ceil_div;
+using fp8::overlap;
+using namespace rows;
+
+constexpr int kMaxGrid = 1 << 20;
+// of dy: k_sums' launches stay below 2^32 threads
+constexpr int64_t kMaxEntries = 1LL << 38;
+
+struct Ids {
+  const void* p;
+  int wide;  // int64, else int32
+  int64_t first, rows;
+};
+// The row of token t's id; `rows` for an id that is no row.
+__device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t t) {
+  const int64_t id = ids.wide ? static_cast<const int64_t*>(ids.p)[t] : (int64_t) static_cast<const int32_t*>(ids.p)[t];
+  // as unsigned, so that ids below `first`, and differences past 2^63, are past the end too
+  const uint64_t r = (uint64_t)id - (uint64_t)ids.first;
+  return r < (uint64_t)ids.rows ? (uint32_t)r : (uint32_t)ids.rows;
+}
+
+// ---- lookup -------------------------------------------------------------------
+struct LookArgs {
+  Ids ids;
+  const void* table;
+  void* out;
+  int64_t n, table_ld, out_ld;
+  int cols, vecs;
+  float scale;
+};
+
+// A thread takes kPer vectors of 8 entries, one after the other in the list of
+// all tokens' vectors in the workgroup's stretch of it; their loads run together.
+constexpr int kPer = 4;
+template <typename TT, typename TO>
+__global__ __launch_bounds__(256) void k_lookup(LookArgs a) {
+  const uint64_t total = (uint64_t)a.n * (uint32_t)a.vecs;
+  const uint64_t stretch = (uint64_t)gridDim.x * (256 * kPer);
+  for (uint64_t base = (uint64_t)blockIdx.x * (256 * kPer); base < total; base += stretch) {
+    const uint64_t t0 = base / (uint32_t)a.vecs;
+    const uint32_t rest = (uint32_t)(base - t0 * (uint32_t)a.vecs);  // of the first vector in its row
+    int64_t t[kPer];
+    int c[kPer];
+    uint32_t r[kPer];
+    Raw<TT> raw[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const uint32_t i = rest + k * 256 + threadIdx.x, q = i / (uint32_t)a.vecs;
+      t[k] = (int64_t)t0 + q;
+      c[k] = (int)(i - q * (uint32_t)a.vecs) * 8;
+      r[k] = t[k] < a.n ? row_of(a.ids, t[k]) : (uint32_t)a.ids.rows;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const bool found = r[k] < (uint32_t)a.ids.rows;
+      const TT* p = static_cast<const TT*>(a.table) + (found ? (int64_t)r[k] * a.table_ld : 0) + c[k];
+      if (c[k] + 8 <= a.cols) raw[k].load(p);
+      else raw[k].load(p, a.cols - c[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (t[k] >= a.n) continue;
+      const bool found = r[k] < (uint32_t)a.ids.rows;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = found ? raw[k].at(j) * a.scale : 0.f;
+      store8(static_cast<TO*>(a.out) + t[k] * a.out_ld + c[k], v, a.cols - c[k]);
+    }
+  }
+}
+
+// ---- tokens in the order of their rows ---------------------------------------------
+// Zeros over rows x cols floats, ld apart, by blocks `block` of `blocks`.
+struct FillArgs {
+  float* p;
+  int64_t rows, cols, ld;
+};
+__device__ __forceinline__ void fill(const FillArgs& f, int64_t block, int64_t blocks) {
+  const int64_t vecs = (f.cols + 3) >> 2, step = blocks * blockDim.x;
+  const float zero[4] = {};
+  for (int64_t i = block * blockDim.x + threadIdx.x; i < f.rows * vecs; i += step) {
+    const int64_t r = f.rows == 1 ? 0 : i / vecs, c = (i - r * vecs) * 4;
+    float* p = f.p + r * f.ld + c;
+    if (c + 4 <= f.cols) *reinterpret_cast<f32x4_a4*>(p) = f32x4{0.f, 0.f, 0.f, 0.f};
+    else
+      for (int j = 0; c + j < f.cols; ++j) p[j] = zero[j];
+  }
+}
+__global__ __launch_bounds__(1024) void k_fill(FillArgs f) { fill(f, blockIdx.x, gridDim.x); }
+
+struct Sorted {
+  uint32_t *key, *tok;  // rows in ascending order, and whose they are
+};
+
+// Up to kCountMax tokens: a token's place is the number of tokens before it,
+// counted over all of them, n^2 comparisons in one launch. Thread (x, y) of a
+// workgroup counts for token x of its kTok the tokens of slice y of all; waves read
+// the slice's rows from LDS as broadcasts. The workgroups past the first `sorting` fill G with zeros.
+//
+// (To be measured against the passes below.)
+constexpr int kCountMax = 16384, kTok = 32, kSlices = 1024 / kTok;
+__global__ __launch_bounds__(1024) void k_count(Ids ids, int n, Sorted out, int sorting, FillArgs f) {
+  // n rounded up to 4 kSlices, then the counts
+  __shared__ __attribute__((aligned(16))) uint32_t keys[kCountMax + 1024];
+  if ((int)blockIdx.x >= sorting) {
+    fill(f, blockIdx.x - sorting, gridDim.x - sorting);
+    return;
+  }
+  const int per = (int)ceil_div(n, 4 * kSlices) * 4, all = per * kSlices;
+  for (int t = threadIdx.x; t < all; t += 1024) keys[t] = t < n ? row_of(ids, t) : 0xffffffffu;
+  __syncthreads();
+  const int x = threadIdx.x & (kTok - 1), y = threadIdx.x / kTok;
+  const int t = (int)blockIdx.x * kTok + x;
+  const uint32_t mine = t < n ? keys[t] : 0u;
+  // rows equal to mine count where their token comes first
+  int count = 0;
+  const int end = (y + 1) * per;
+  for (int i = y * per; i < end; i += 4) {
+    const u32x4 k = *reinterpret_cast<const u32x4*>(keys + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) count += k[j] < mine + (i + j < t ? 1u : 0u) ? 1 : 0;
+  }
+  uint32_t* sums = keys + all;
+  sums[y * kTok + x] = (uint32_t)count;
+  __syncthreads();
+  if (threadIdx.x < kTok && t < n) {
+    uint32_t place = 0;
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) place += sums[s * kTok + x];
+    out.key[place] = mine;
+    out.tok[place] = (uint32_t)t;
+  }
+}
+static_assert(kCountMax % (4 * kSlices) == 0, "rounded up, n fits keys");
+
+// More tokens: by 8 bits of the row at a time, from the lowest. A pass counts
+// each tile's digits, sums the counts up over digits and tiles, and moves the tokens.
+constexpr int kTile = 4096, kDigits = 256;
+struct PassArgs {
+  Ids ids;
+  Sorted in, out;  // in.key == nullptr: the ids themselves
+  uint32_t* counts;  // [digit][tile]
+  int n, tiles, shift;
+};
+__device__ __forceinline__ uint32_t key_at(const PassArgs& a, int i) { return a.in.key ? a.in.key[i] : row_of(a.ids, i); }
+
+__global__ __launch_bounds__(256) void k_digits(PassArgs a) {
+  __shared__ uint32_t hist[kDigits];
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  const int lo = (int)blockIdx.x * kTile, hi = min(lo + kTile, a.n);
+  for (int i = lo + threadIdx.x; i < hi; i += 256) atomicAdd(&hist[key_at(a, i) >> a.shift & 255], 1u);
+  __syncthreads();
+  a.counts[(int64_t)threadIdx.x * a.tiles + blockIdx.x] = hist[threadIdx.x];
+}
+
+// counts[i] <- the sum of those before it; one workgroup, 4096 at a time.
+__global__ __launch_bounds__(1024) void k_sum_up(uint32_t* counts, int total) {
+  __shared__ uint32_t part[2][1024];
+  uint32_t before = 0;
+  for (int base = 0; base < total; base += 4096) {
+    const int i = base + threadIdx.x * 4;
+    uint32_t v[4], s = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = i + k < total ? counts[i + k] : 0;
+      s += v[k];
+    }
+    int cur = 0;
+    part[0][threadIdx.x] = s;
+    __syncthreads();
+    for (int d = 1; d < 1024; d <<= 1) {
+      part[cur ^ 1][threadIdx.x] = part[cur][threadIdx.x] + ((int)threadIdx.x >= d ? part[cur][threadIdx.x - d] : 0);
+      cur ^= 1;
+      __syncthreads();
+    }
+    uint32_t at = before + part[cur][threadIdx.x] - s;
+    before += part[cur][1023];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k < total) counts[i + k] = at;
+      at += v[k];
+    }
+    __syncthreads();
+  }
+}
+
+// Each of the 4 waves takes a quarter of the tile, 64 tokens at a time in their
+// order; those with equal digits find each other by ballots.
+__global__ __launch_bounds__(256) void k_move(PassArgs a) {
+  __shared__ uint32_t at[4][kDigits];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kQuarter = kTile / 4;
+  const int lo = (int)blockIdx.x * kTile + wave * kQuarter;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) at[w][threadIdx.x] = 0;
+  __syncthreads();
+  uint32_t key[kQuarter / 64];
+#pragma unroll
+  for (int k = 0; k < kQuarter / 64; ++k) {
+    const int i = lo + k * 64 + lane;
+    key[k] = i < a.n ? key_at(a, i) : 0;
+    if (i < a.n) atomicAdd(&at[wave][key[k] >> a.shift & 255], 1u);
+  }
+  __syncthreads();
+  {  // the waves' counts to their first places
+    uint32_t p = a.counts[(int64_t)threadIdx.x * a.tiles + blockIdx.x];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t c = at[w][threadIdx.x];
+      at[w][threadIdx.x] = p;
+      p += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kQuarter / 64; ++k) {
+    const int i = lo + k * 64 + lane;
+    const bool live = i < a.n;
+    const uint32_t digit = key[k] >> a.shift & 255;
+    uint64_t same = __ballot(live);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const uint64_t set = __ballot(digit >> b & 1);
+      same &= digit >> b & 1 ? set : ~set;
+    }
+    const int before = __popcll(same & ((1ull << lane) - 1));
+    if (live) {
+      const uint32_t to = at[wave][digit] + before;
+      a.out.key[to] = key[k];
+      a.out.tok[to] = a.in.key ? a.in.tok[i] : (uint32_t)i;
+    }
+    // the wave's places move on before its next 64 (its own lanes only: LDS operations of a wave are in order)
+    __builtin_amdgcn_wave_barrier();
+    if (live && before == 0) at[wave][digit] += (uint32_t)__popcll(same);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---- the sums -----------------------------------------------------------------------
+// The sorted tokens are cut into chunks of `chunk`. The chunk in which a row's
+// tokens begin sums them to the end of the next chunk and, if that is all of them,
+// stores the row; what lies in later chunks is summed there (`head`) and joined to
+// the first sum (`tail`) by k_join. So most rows are stored at once, and a frequent token's
+// sum is shared out.
+struct SumArgs {
+  Sorted s;
+  const void* dy;
+  float* g;
+  float *tail, *head;  // [chunk][cols]
+  int64_t dy_ld, g_ld;
+  int n, chunk, chunks, slabs, cols, accumulate;
+  uint32_t rows;
+  float scale;
+};
+
+// LPR lanes take a chunk's LPR * 8 columns, kRows tokens at a time.
+template <typename TD, int LPR>
+__global__ __launch_bounds__(256) void k_sums(SumArgs a) {
+  constexpr int kRows = 4;
+  int64_t g = (int64_t)blockIdx.x * (256 / LPR);
+  if constexpr (LPR == 64) g += __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  else g += threadIdx.x / LPR;
+  if (g >= (int64_t)a.chunks * a.slabs) return;
+  const int c = (int)(g / a.slabs), slab = (int)(g - (int64_t)c * a.slabs);
+  const int col = (slab * LPR + (int)(threadIdx.x & (LPR - 1))) * 8, left = a.cols - col;
+  const int p0 = c * a.chunk, p1 = min(p0 + a.chunk, a.n), lim = min(p1 + a.chunk, a.n);
+  const uint32_t* key = a.s.key;
+  const uint32_t first = key[p0], last = key[p1 - 1];
+  if (first >= a.rows) return;
+  // first's tokens began before this chunk: in the one before, which sums them (skip), or earlier (head)
+  const bool cont = p0 > 0 && key[p0 - 1] == first;
+  const bool head = cont && p0 - a.chunk > 0 && key[p0 - a.chunk - 1] == first;
+  const bool skip = cont && !head;
+  float acc[8] = {};
+  bool open = head, pending = false;
+  for (int p = p0; p < lim; p += kRows) {
+    uint32_t k[kRows + 1];
+    bool valid[kRows], end[kRows], store[kRows];
+    Raw<TD> raw[kRows];
+    Raw<float> old[kRows];
+#pragma unroll
+    for (int i = 0; i <= kRows; ++i) k[i] = p + i < a.n ? key[p + i] : 0xffffffffu;
+    bool any = false, still = open;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      valid[i] = p + i < lim && k[i] < a.rows && !(skip && k[i] == first) &&
+                 (p + i < p1 || (k[i] == last && !(cont && last == first)));
+      end[i] = valid[i] && k[i + 1] != k[i];
+      store[i] = end[i] && !still;
+      if (end[i]) still = false;
+      any |= valid[i];
+      if (valid[i]) {
+        const TD* q = static_cast<const TD*>(a.dy) + (int64_t)a.s.tok[p + i] * a.dy_ld + col;
+        if (left >= 8) raw[i].load(q);
+        else raw[i].load(q, left);
+        if (store[i] && a.accumulate) {
+          const float* o = a.g + (int64_t)k[i] * a.g_ld + col;
+          if (left >= 8) old[i].load(o);
+          else old[i].load(o, left);
+        }
+      }
+    }
+    if (!any && p >= p1) break;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (!valid[i]) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += raw[i].at(j);
+      pending = !end[i];
+      if (!end[i]) continue;
+      if (store[i]) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = a.accumulate ? __builtin_fmaf(acc[j], a.scale, old[i].at(j)) : acc[j] * a.scale;
+        if (left > 0) store8(a.g + (int64_t)k[i] * a.g_ld + col, v, left);
+      } else if (left > 0) {
+        store8(a.head + (int64_t)c * a.cols + col, acc, left);
+      }
+      open = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    }
+  }
+  if (pending && left > 0) store8((open ? a.head : a.tail) + (int64_t)c * a.cols + col, acc, left);
+}
+
+// Rows whose tokens go on past the chunk after the one they begin in: the tail
+// and the heads, each of 4 waves a quarter of them, then the quarters in order. A
+// workgroup looks through 64 chunks.
+template <int LPR>
+__global__ __launch_bounds__(256) void k_join(SumArgs a) {
+  __shared__ float sums[4][64 * 8 + 8];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c0 = (int)(blockIdx.x / a.slabs) * 64, slab = (int)(blockIdx.x % a.slabs);
+  const int col = (slab * LPR + (lane & (LPR - 1))) * 8, left = lane < LPR ? a.cols - col : 0;
+  const uint32_t* key = a.s.key;
+  auto key_of = [&](int64_t chunk) { return key[chunk * a.chunk]; };
+  bool mine = false;
+  {
+    const int c = c0 + lane;
+    if (c + 2 < a.chunks) {
+      const uint32_t k = key[(int64_t)(c + 1) * a.chunk - 1];
+      mine = k < a.rows && key_of(c + 2) == k && (c == 0 || key[(int64_t)c * a.chunk - 1] != k);
+    }
+  }
+  for (uint64_t todo = __ballot(mine); todo; todo &= todo - 1) {
+    const int c = c0 + __builtin_ctzll(todo);
+    const uint32_t k = key[(int64_t)(c + 1) * a.chunk - 1];
+    int heads = 0;  // chunks c + 2 .. c + 1 + heads
+    for (;;) {
+      const int64_t q = (int64_t)c + 2 + heads + lane;
+      const uint64_t eq = __ballot(q < a.chunks && key_of(q) == k);
+      const int run = ~eq ? __builtin_ctzll(~eq) : 64;
+      heads += run;
+      if (run < 64) break;
+    }
+    const int lo = (int)((int64_t)wave * heads >> 2), hi = (int)((int64_t)(wave + 1) * heads >> 2);
+    float acc[8] = {};
+    if (left > 0) {
+      const float* p = a.head + ((int64_t)c + 2) * a.cols + col;
+      if (wave == 0) {
+        Raw<float> t;
+        const float* q = a.tail + (int64_t)c * a.cols + col;
+        if (left >= 8) t.load(q);
+        else t.load(q, left);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = t.at(j);
+      }
+      int h = lo;
+      for (; h + 4 <= hi; h += 4) {
+        Raw<float> t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* q = p + (int64_t)(h + i) * a.cols;
+          if (left >= 8) t[i].load(q);
+          else t[i].load(q, left);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] += t[i].at(j);
+      }
+      for (; h < hi; ++h) {
+        Raw<float> t;
+        const float* q = p + (int64_t)h * a.cols;
+        if (left >= 8) t.load(q);
+        else t.load(q, left);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += t.at(j);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = acc[j];
+    __syncthreads();
+    if (wave == 0 && left > 0) {
+      float v[8];
+      float* o = a.g + (int64_t)k * a.g_ld + col;
+      Raw<float> old;
+      if (a.accumulate) {
+        if (left >= 8) old.load(o);
+        else old.load(o, left);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = acc[j] + sums[1][lane * 8 + j] + sums[2][lane * 8 + j] + sums[3][lane * 8 + j];
+        v[j] = a.accumulate ? __builtin_fmaf(s, a.scale, old.at(j)) : s * a.scale;
+      }
+      store8(o, v, left);
+    }
+    __syncthreads();
+  }
+}
+
+// ---- host side ----------------------------------------------------------------------
+// Where things are in the workspace, and how the tokens are cut.
+struct Plan {
+  int64_t n;
+  int lpr, slabs, chunk, chunks, tiles;
+  size_t key[2], tok[2], counts, tail, head, bytes;
+};
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+Plan plan_of(int64_t n, int64_t cols) {
+  Plan p{};
+  p.n = n;
+  p.lpr = cols <= 128 ? 16 : 64;
+  p.slabs = (int)ceil_div(cols, p.lpr * 8);
+  // about 4096 waves, 16 a CU; each chunk pays for its ends
+  p.chunk = 4;
+  while (p.chunk < 256 && n * p.slabs * (p.lpr / 16) > (int64_t)p.chunk * 16384) p.chunk *= 2;
+  p.chunks = (int)ceil_div(n, p.chunk);
+  p.tiles = (int)ceil_div(n, kTile);
+  const bool count = n <= kCountMax;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = up256(at + bytes);
+    return here;
+  };
+  for (int i = 0; i < (count ? 1 : 2); ++i) {
+    p.key[i] = take((size_t)n * 4);
+    p.tok[i] = take((size_t)n * 4);
+  }
+  p.counts = count ? 0 : take((size_t)kDigits * p.tiles * 4);
+  p.tail = take((size_t)p.chunks * cols * 4);
+  p.head = take((size_t)p.chunks * cols * 4);
+  p.bytes = at;
+  return p;
+}
+
+int check_ids(const void* ids, int32_t id_bytes, int64_t n, int64_t rows, int64_t cols, int64_t first) {
+  if (id_bytes != 4 && id_bytes != 8) return fail(MUONH_EINVAL, "id_bytes=%d is neither 4 nor 8", id_bytes);
+  if (fp8::bad_dim(n)) return fail(MUONH_ESHAPE, "%lld ids out of [0, %d]", (long long)n, MUONH_MAX_FP8_DIM);
+  if (fp8::bad_dim(rows) || fp8::bad_dim(cols))
+    return fail(MUONH_ESHAPE, "shape %lld x %lld out of [0, %d]", (long long)rows, (long long)cols, MUONH_MAX_FP8_DIM);
+  if (first < 0) return fail(MUONH_EINVAL, "first=%lld must be >= 0", (long long)first);
+  if (n > 0 && cols > 0) {
+    if (!ids) return fail(MUONH_EINVAL, "ids is NULL");
+    if (reinterpret_cast<uintptr_t>(ids) & (uintptr_t)(id_bytes - 1))
+      return fail(MUONH_EINVAL, "ids is not aligned to its type");
+  }
+  return MUONH_OK;
+}
+
+}  // namespace
+}  // namespace embed
+}  // namespace muonh
+
+extern "C" {
+
+int muonh_embedding(const void* ids, int32_t id_bytes, int64_t n, int64_t first, const void* table, int32_t table_dtype,
+                    int64_t rows, int64_t cols, int64_t table_ld, float scale, void* out, int32_t out_dtype,
+                    int64_t out_ld, void* stream) {
+  using namespace muonh;
+  using namespace muonh::embed;
+  if (bad_dtype(table_dtype))
+    return fail(MUONH_EINVAL, "table_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", table_dtype);
+  if (bad_dtype(out_dtype)) return fail(MUONH_EINVAL, "out_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", out_dtype);
+  if (const int err = check_ids(ids, id_bytes, n, rows, cols, first)) return err;
+  if (!(scale - scale == 0.f)) return fail(MUONH_EINVAL, "scale=%g must be finite", (double)scale);
+  if (n == 0 || cols == 0) return MUONH_OK;
+  if (rows == 0) return fail(MUONH_ESHAPE, "a table of no rows");
+  const Mat from = {"table", table, table_dtype, table_ld}, to = {"out", out, out_dtype, out_ld};
+  if (const int err = check_mat(from, cols)) return err;
+  if (const int err = check_mat(to, cols)) return err;
+  const Span written = span_of(to, n, cols);
+  if (overlap(written, span_of(from, rows, cols))) return fail(MUONH_EALIAS, "out overlaps table");
+  if (overlap(written, span("ids", ids, n * id_bytes))) return fail(MUONH_EALIAS, "out overlaps ids");
+  LookArgs a{};
+  a.ids = Ids{ids, id_bytes == 8, first, rows};
+  a.table = table;
+  a.out = out;
+  a.n = n;
+  a.table_ld = table_ld;
+  a.out_ld = out_ld;
+  a.cols = (int)cols;
+  a.vecs = (int)ceil_div(cols, 8);
+  a.scale = scale;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(n * a.vecs, 256 * kPer), kMaxGrid));
+  const bool tb = table_dtype == MUONH_DT_BF16, ob = out_dtype == MUONH_DT_BF16;
+  if (tb && ob) hipLaunchKernelGGL((k_lookup<__bf16, __bf16>), grid, dim3(256), 0, s, a);
+  else if (tb) hipLaunchKernelGGL((k_lookup<__bf16, float>), grid, dim3(256), 0, s, a);
+  else if (ob) hipLaunchKernelGGL((k_lookup<float, __bf16>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_lookup<float, float>), grid, dim3(256), 0, s, a);
+  return launched("embedding");
+}
+
+size_t muonh_embedding_backward_workspace_bytes(int64_t n, int64_t cols) {
+  using namespace muonh;
+  if (fp8::bad_dim(n) || fp8::bad_dim(cols) || n == 0 || cols == 0 ||
+      n * cols > embed::kMaxEntries)
+    return 0;
+  return embed::plan_of(n, cols).bytes;
+}
+
+int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64_t first, const void* dy, int32_t dy_dtype,
+                             int64_t dy_ld, float scale, float* grad, int64_t rows, int64_t cols, int64_t grad_ld,
+                             int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace muonh;
+  using namespace muonh::embed;
+  if (bad_dtype(dy_dtype)) return fail(MUONH_EINVAL, "dy_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", dy_dtype);
+  if (const int err = check_ids(ids, id_bytes, n, rows, cols, first)) return err;
+  if (!(scale - scale == 0.f)) return fail(MUONH_EINVAL, "scale=%g must be finite", (double)scale);
+  if (rows == 0 || cols == 0) return MUONH_OK;
+  const Mat to = {"grad", grad, MUONH_DT_FP32, grad_ld}, from = {"dy", dy, dy_dtype, dy_ld};
+  if (const int err = check_mat(to, cols)) return err;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  // whole rows without gaps are one long row of zeros
+  FillArgs f = grad_ld == cols ? FillArgs{grad, 1, rows * cols, rows * cols} : FillArgs{grad, rows, cols, grad_ld};
+  if (accumulate) f.rows = 0;
+  const int fills = accumulate ? 0 : (int)std::min<int64_t>(ceil_div(f.rows * ceil_div(f.cols, 4), 1024), 2048);
+  if (n == 0) {
+    if (!fills) return MUONH_OK;
+    hipLaunchKernelGGL(k_fill, dim3((unsigned)fills), dim3(1024), 0, s, f);
+    return launched("embedding backward");
+  }
+  if (const int err = check_mat(from, cols)) return err;
+  if (n * cols > kMaxEntries) return fail(MUONH_ESHAPE, "dy has more than 2^38 entries");
+  const Plan p = plan_of(n, cols);
+  if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the call needs %zu bytes", p.bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MUONH_EWORKSPACE, "workspace must be 256-byte aligned");
+  if (workspace_bytes < p.bytes)
+    return fail(MUONH_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, p.bytes);
+  const Span read[2] = {span_of(from, n, cols), span("ids", ids, n * id_bytes)};
+  const Span written[2] = {span_of(to, rows, cols), span("workspace", workspace, (int64_t)p.bytes)};
+  for (const Span& w : written)
+    for (const Span& r : read)
+      if (overlap(w, r)) return fail(MUONH_EALIAS, "%s overlaps %s", w.name, r.name);
+  if (overlap(written[0], written[1])) return fail(MUONH_EALIAS, "grad overlaps the workspace");
+
+  char* ws = static_cast<char*>(workspace);
+  auto sorted = [&](int i) {
+    return Sorted{reinterpret_cast<uint32_t*>(ws + p.key[i]), reinterpret_cast<uint32_t*>(ws + p.tok[i])};
+  };
+  const Ids which{ids, id_bytes == 8, first, rows};
+  SumArgs a{};
+  if (n <= kCountMax) {
+    const int sorting = (int)ceil_div(n, kTok);
+    hipLaunchKernelGGL(k_count, dim3((unsigned)(sorting + fills)), dim3(1024), 0, s, which, (int)n,
+                       sorted(0), sorting, f);
+    a.s = sorted(0);
+  } else {
+    if (fills) hipLaunchKernelGGL(k_fill, dim3((unsigned)fills), dim3(1024), 0, s, f);
+    PassArgs b{};
+    b.ids = which;
+    b.counts = reinterpret_cast<uint32_t*>(ws + p.counts);
+    b.n = (int)n;
+    b.tiles = p.tiles;
+    int side = 0;
+    for (b.shift = 0; b.shift == 0 || rows >> b.shift; b.shift += 8) {
+      b.out = sorted(side);
+      hipLaunchKernelGGL(k_digits, dim3((unsigned)p.tiles), dim3(256), 0, s, b);
+      hipLaunchKernelGGL(k_sum_up, dim3(1), dim3(1024), 0, s, b.counts, kDigits * p.tiles);
+      hipLaunchKernelGGL(k_move, dim3((unsigned)p.tiles), dim3(256), 0, s, b);
+      b.in = b.out;
+      side ^= 1;
+    }
+    a.s = b.in;
+  }
+  a.dy = dy;
+  a.g = grad;
+  a.tail = reinterpret_cast<float*>(ws + p.tail);
+  a.head = reinterpret_cast<float*>(ws + p.head);
+  a.dy_ld = dy_ld;
+  a.g_ld = grad_ld;
+  a.n = (int)n;
+  a.chunk = p.chunk;
+  a.chunks = p.chunks;
+  a.slabs = p.slabs;
+  a.cols = (int)cols;
+  a.accumulate = accumulate != 0;
+  a.rows = (uint32_t)rows;
+  a.scale = scale;
+  const int64_t groups = (int64_t)p.chunks * p.slabs;
+  const dim3 sums((unsigned)ceil_div(groups, 256 / p.lpr)), join((unsigned)(ceil_div(p.chunks, 64) * p.slabs));
+  auto run = [&](auto type) {
+    using T = decltype(type);
+    if (p.lpr == 16) hipLaunchKernelGGL((k_sums<T, 16>), sums, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_sums<T, 64>), sums, dim3(256), 0, s, a);
+  };
+  if (dy_dtype == MUONH_DT_BF16) run(__bf16{});
+  else run(float{});
+  if (p.chunks > 2) {
+    if (p.lpr == 16) hipLaunchKernelGGL((k_join<16>), join, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_join<64>), join, dim3(256), 0, s, a);
+  }
+  return launched("embedding backward");
+}
+
+}  // extern "C"

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "fp8_codes.h"
+#include "rows.h"
 
 namespace muonh {
 namespace norm {
@@ -24,69 +25,8 @@ using fp8::kBlock;
 using fp8::overlap;
 using fp8::Span;
 using fp8::span;
+using namespace rows;
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-// at any multiple of the entry's size (gfx950 takes vector accesses at any address)
-typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// ---- 8 consecutive entries -----------------------------------------------------
-// As loaded; n: how many of them there are (below 8 only in a row's last vector).
-template <typename T>
-struct Raw;
-template <>
-struct Raw<__bf16> {
-  u32x4 v;
-  __device__ __forceinline__ void load(const __bf16* p) { v = *reinterpret_cast<const u32x4_a2*>(p); }
-  __device__ __forceinline__ void load(const __bf16* p, int n) {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-    v = u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) v[j >> 1] |= (uint32_t)q[j] << (16 * (j & 1));
-  }
-  __device__ __forceinline__ float at(int j) const {
-    return __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16);
-  }
-};
-template <>
-struct Raw<float> {
-  f32x4 v[2];
-  __device__ __forceinline__ void load(const float* p) {
-    v[0] = *reinterpret_cast<const f32x4_a4*>(p);
-    v[1] = *reinterpret_cast<const f32x4_a4*>(p + 4);
-  }
-  __device__ __forceinline__ void load(const float* p, int n) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = j < n ? p[j] : 0.f;
-  }
-  __device__ __forceinline__ float at(int j) const { return v[j >> 2][j & 3]; }
-};
-
-// Stores the first n of 8 values, each rounded once.
-__device__ __forceinline__ void store8(__bf16* p, const float (&v)[8], int n) {
-  const bf16x8 b = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3],
-                    (__bf16)v[4], (__bf16)v[5], (__bf16)v[6], (__bf16)v[7]};
-  if (n >= 8) {
-    *reinterpret_cast<u32x4_a2*>(p) = __builtin_bit_cast(u32x4, b);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = b[j];
-  }
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8], int n) {
-  if (n >= 8) {
-    *reinterpret_cast<f32x4_a4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4_a4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = v[j];
-  }
-}
 __device__ __forceinline__ float rounded(float v, float) { return v; }
 __device__ __forceinline__ float rounded(float v, __bf16) { return (float)(__bf16)v; }
 
@@ -564,40 +504,11 @@ void launch_back(BwdArgs a, hipStream_t s) {
 #undef MUONH_NORM
 }
 
-bool bad_dtype(int32_t d) { return d != MUONH_DT_FP32 && d != MUONH_DT_BF16; }
-int size_of(int32_t d) { return d == MUONH_DT_BF16 ? 2 : 4; }
-
 // A mean over no columns is no number: refused.
 int check_shape(int64_t rows, int64_t cols) {
   if (fp8::bad_dim(rows) || fp8::bad_dim(cols) || cols == 0)
     return fail(MUONH_ESHAPE, "%lld x %lld: rows out of [0, %d] or columns out of [1, %d]", (long long)rows,
                 (long long)cols, MUONH_MAX_FP8_DIM, MUONH_MAX_FP8_DIM);
-  return MUONH_OK;
-}
-
-// A 2-d argument: rows of `cols` entries, ld apart.
-struct Mat {
-  const char* name;
-  const void* p;
-  int32_t dtype;
-  int64_t ld;
-};
-int check_mat(const Mat& m, int64_t cols) {
-  if (!m.p) return fail(MUONH_EINVAL, "%s is NULL", m.name);
-  if (reinterpret_cast<uintptr_t>(m.p) & (uintptr_t)(size_of(m.dtype) - 1))
-    return fail(MUONH_EINVAL, "%s is not aligned to its type", m.name);
-  if (m.ld < cols || m.ld > (1LL << 36))
-    return fail(MUONH_EINVAL, "%s's row pitch %lld out of [cols=%lld, 2^36]", m.name, (long long)m.ld, (long long)cols);
-  return MUONH_OK;
-}
-Span span_of(const Mat& m, int64_t rows, int64_t cols) {
-  return span(m.name, m.p, m.p ? ((rows - 1) * m.ld + cols) * size_of(m.dtype) : 0);
-}
-bool same(const Mat& a, const Mat& b) { return a.p == b.p && a.ld == b.ld && a.dtype == b.dtype; }
-
-int launched(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(MUONH_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
   return MUONH_OK;
 }
 
@@ -714,7 +625,8 @@ int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, con
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 join((unsigned)ceil_div(cols, 32));
   if (rows == 0) {  // the sum over no rows
-    if (!accumulate) hipLaunchKernelGGL(k_norm_join, join, dim3(1024), 0, s, nullptr, 0, (int)cols, dweight, 0);
+    if (accumulate) return MUONH_OK;
+    hipLaunchKernelGGL(k_norm_join, join, dim3(1024), 0, s, nullptr, 0, (int)cols, dweight, 0);
     return launched("rms norm backward");
   }
   const Mat d = {"dy", dy, dy_dtype, dy_ld}, x = {"h", h, h_dtype, h_ld}, res = {"dresidual", dresidual, h_dtype, dresidual_ld},
