@@ -524,6 +524,66 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
                              int64_t rows, int64_t cols, int64_t grad_ld, int32_t accumulate,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Microscaled 4-bit matrices (OCP MX, FP4): the operands of linear layers at half the
+ * bytes of the 8-bit ones, and twice their matrix rate. Readings:
+ *   - codes: e2m1 (sign, 2 exponent, 1 mantissa bit): 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *     and their negatives; no NaN, no infinity;
+ *   - scales: E8M0, one byte per 32 consecutive columns of a row (the last group of
+ *     a row may be shorter). A group's scale is the smallest power of two 2^e, e >= -126,
+ *     with max|x| <= 6 * 2^e, so that no entry overflows (as for the 8-bit blocks;
+ *     the MX document's conversion lets the largest entries saturate). x * 2^-e is
+ *     exact, so a code is x / 2^e rounded once, to the nearest e2m1 value, ties to the even
+ *     mantissa. A group with a NaN or an infinity has the scale byte 255, which makes
+ *     all of it NaN, and zero codes.
+ * Storage of a rows x cols matrix: codes, row-major, two to a byte, the first in the
+ * low 4 bits, row pitch muonh_fp4_ld(cols) = cols rounded up to 256, over 2, bytes, zeros past
+ * cols; scales, row-major, row pitch muonh_fp4_scale_ld(cols) = cols rounded up to 512,
+ * over 32, bytes, zeros past ceil(cols/32). Both 16-byte aligned. The quantizing calls write all of
+ * it; an operand of muonh_fp4_matmul from elsewhere needs the zero codes past cols, and scale
+ * bytes there that are not 255. Matrices without rows or columns are allowed.
+ */
+typedef struct {
+  const void* codes;  /* DEVICE, rows x muonh_fp4_ld(cols) bytes */
+  const void* scales; /* DEVICE, rows x muonh_fp4_scale_ld(cols) bytes */
+  int64_t rows, cols; /* in [0, MUONH_MAX_FP8_DIM] */
+} muonh_fp4_matrix;
+
+/* Row pitches in bytes (0 for cols out of [0, MUONH_MAX_FP8_DIM]). Host-only. */
+int64_t muonh_fp4_ld(int64_t cols);
+int64_t muonh_fp4_scale_ld(int64_t cols);
+
+/*
+ * Quantize src (as for muonh_fp8_quantize) into codes and scales, grouped along its
+ * columns, and/or codes_t and scales_t, its transpose (cols x rows), grouped along its rows:
+ * the forms that a forward product and a weight gradient read. One pass over src.
+ * Deterministic; asynchronous on `stream`, capturable. Errors: as muonh_fp8_quantize.
+ */
+int muonh_fp4_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t src_ld,
+                       void* codes, void* scales, void* codes_t, void* scales_t, void* stream);
+
+/*
+ * out[i][j] = the value that x's entry stands for (DEVICE, out_dtype, pitch out_ld): exact in
+ * either type, but for 2^128 and above, which are infinite. Errors: MUONH_EINVAL, MUONH_ESHAPE,
+ * MUONH_EALIAS, MUONH_EHIP.
+ */
+int muonh_fp4_dequantize(const muonh_fp4_matrix* x, void* out, int32_t out_dtype, int64_t out_ld,
+                         void* stream);
+
+/*
+ * out[i][j] = sum_k a[i][k] * b[j][k] over the values that a (m x k) and b (n x k) stand
+ * for, plus out's old value if `accumulate`; out, its types and pitch, workspace, k = 0 and the three products of
+ * a linear layer as for muonh_fp8_matmul (every operand is grouped along k here, so a
+ * weight is quantized in both forms). Products and the sums of a group are exact, other sums fp32; the result
+ * is rounded once to out_dtype. Groups of scale byte 255 give NaN in their row or column of
+ * out. The result does not depend on out_ld or alignment, and is deterministic.
+ * Errors: as muonh_fp8_matmul.
+ */
+size_t muonh_fp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int muonh_fp4_matmul(const muonh_fp4_matrix* a, const muonh_fp4_matrix* b, void* out,
+                     int32_t out_dtype, int64_t out_ld, int32_t accumulate, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* muonh_status_string(int status);
 

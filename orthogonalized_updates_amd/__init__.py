@@ -94,6 +94,12 @@ class Fp8Desc(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("block", ctypes.c_int32)]
 
 
+class Fp4Desc(ctypes.Structure):
+    """muonh_fp4_matrix."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
 class GroupDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("count", ctypes.c_int32)]
 
@@ -135,6 +141,13 @@ def _load_library() -> ctypes.CDLL:
         "muonh_fp8_matmul_workspace_bytes": (sz, [i64, i64, i64, i32]),
         "muonh_fp8_matmul": (ctypes.c_int, [ctypes.POINTER(Fp8Desc), ctypes.POINTER(Fp8Desc), vp,
                                             i32, i64, i32, vp, sz, vp]),
+        "muonh_fp4_ld": (i64, [i64]),
+        "muonh_fp4_scale_ld": (i64, [i64]),
+        "muonh_fp4_quantize": (ctypes.c_int, [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]),
+        "muonh_fp4_dequantize": (ctypes.c_int, [ctypes.POINTER(Fp4Desc), vp, i32, i64, vp]),
+        "muonh_fp4_matmul_workspace_bytes": (sz, [i64, i64, i64]),
+        "muonh_fp4_matmul": (ctypes.c_int, [ctypes.POINTER(Fp4Desc), ctypes.POINTER(Fp4Desc), vp, i32, i64, i32,
+                                            vp, sz, vp]),
         "muonh_rms_norm": (ctypes.c_int, [vp, i32, i64, i64, i64, vp, i32, i64, vp, i64, vp, f32, vp, vp,
                                           i32, i64, vp, vp, vp, vp, vp]),
         "muonh_rms_norm_backward_workspace_bytes": (sz, [i64, i64]),
@@ -514,7 +527,7 @@ __all__ = ["MuonH", "Plan", "MuonHError", "GroupDesc", "get_lib", "check", "LIB_
            "PTR_CACHE_ENTRIES", "Fp8Matrix", "Fp8Weights", "fp8_quantize", "fp8_matmul",
            "MUONH_FP8_ROWS", "MUONH_FP8_TILES", "MUONH_FP8_FAST", "MUONH_DT_FP32", "MUONH_DT_BF16",
            "MUONH_MAX_FP8_DIM", "rms_norm", "rms_norm_fp8", "rms_norm_backward",
-           "embedding", "embedding_backward"]
+           "embedding", "embedding_backward", "Fp4Matrix", "fp4_quantize", "fp4_matmul"]
 
 
 class AdamW:
@@ -602,7 +615,18 @@ def _check_part(name: str, t, dtype, shape) -> None:
         raise ValueError(f"{name} must be a contiguous {shape} tensor")
 
 
-class Fp8Matrix:
+class _BlockMatrix:
+    """Codes and scales in their layout, whose addresses `desc` holds: read-only attributes."""
+    __slots__ = ("codes", "scales", "shape", "device", "desc")
+
+    def __setattr__(self, name, value):
+        kind = type(self).__name__
+        raise AttributeError(f"{kind}.{name} is read-only; make another {kind}")
+
+    __delattr__ = functools.partialmethod(__setattr__, value=None)
+
+
+class Fp8Matrix(_BlockMatrix):
     """A rows x cols matrix held as e4m3 codes with a power-of-two scale per
     block (muonh_fp8_matrix): per 128 columns of a row (block="rows") or per
     128 x 128 entries ("tiles").
@@ -615,12 +639,7 @@ class Fp8Matrix:
     Fp8Matrix. A matrix whose tensors were moved or resized in place is
     refused by the calls that take it.
     """
-    __slots__ = ("codes", "scales", "shape", "block", "device", "desc")
-
-    def __setattr__(self, name, value):
-        raise AttributeError(f"Fp8Matrix.{name} is read-only; make another Fp8Matrix")
-
-    __delattr__ = functools.partialmethod(__setattr__, value=None)
+    __slots__ = ("block",)
 
     def _set(self, codes, scales, shape, block) -> None:
         put = object.__setattr__
@@ -667,11 +686,11 @@ class Fp8Matrix:
         return self.codes[:, :cols].float() * s.repeat_interleave(FP8_BLOCK, 1)[:, :cols]
 
 
-def _held(name: str, m: Fp8Matrix) -> Fp8Desc:
+def _held(name: str, m: _BlockMatrix):
     """m's descriptor, if its tensors are where they were."""
     d = m.desc
     if m.codes.data_ptr() != (d.codes or 0) or m.scales.data_ptr() != (d.scales or 0):
-        raise ValueError(f"{name}'s codes or scales were moved since the Fp8Matrix was made")
+        raise ValueError(f"{name}'s codes or scales were moved since the {type(m).__name__} was made")
     return d
 
 
@@ -874,6 +893,160 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _on_device(torch, dev, lib.muonh_fp8_matmul, da, db, out.data_ptr(), dt, ld,
                1 if accumulate else 0, None if ws is None else ws.data_ptr(), nbytes)
+    if given:
+        _written(out)
+    return out
+
+
+# -- microscaled 4-bit matrices ------------------------------------------------
+FP4_GROUP = 32  # entries per scale along a row (include/muonh.h)
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp4_layout(rows: int, cols: int):
+    """(codes shape, scales shape) of a rows x cols matrix, in bytes."""
+    if not (0 <= rows <= MUONH_MAX_FP8_DIM and 0 <= cols <= MUONH_MAX_FP8_DIM):
+        raise ValueError(f"shape {(rows, cols)} out of [0, {MUONH_MAX_FP8_DIM}]")
+    return (rows, _up(cols, 256) // 2), (rows, _up(cols, 512) // FP4_GROUP)
+
+
+class Fp4Matrix(_BlockMatrix):
+    """A rows x cols matrix held as e2m1 codes with a power-of-two scale per 32
+    columns of a row (muonh_fp4_matrix).
+
+    codes: torch.float4_e2m1fn_x2 (two codes to a byte, the first in the low half),
+    rows x (cols rounded up to 256, over 2), zeros past cols; scales:
+    torch.float8_e8m0fnu, rows x (cols rounded up to 512, over 32); the byte 255 is
+    NaN. Both contiguous, on one GPU. shape: (rows, cols). Read-only attributes, and
+    moved tensors, as for Fp8Matrix.
+    """
+    __slots__ = ()
+
+    def _set(self, codes, scales, shape) -> None:
+        put = object.__setattr__
+        put(self, "codes", codes)
+        put(self, "scales", scales)
+        put(self, "shape", shape)
+        put(self, "device", codes.device)
+        put(self, "desc", Fp4Desc(codes.data_ptr(), scales.data_ptr(), shape[0], shape[1]))
+
+    def __reduce__(self):  # copies and pickles take the addresses of their own tensors
+        return Fp4Matrix, (self.codes, self.scales, self.shape)
+
+    def __init__(self, codes, scales, shape: Tuple[int, int]):
+        import torch
+        rows, cols = int(shape[0]), int(shape[1])
+        c, e = _fp4_layout(rows, cols)
+        _check_part("codes", codes, torch.float4_e2m1fn_x2, c)
+        _check_part("scales", scales, torch.float8_e8m0fnu, e)
+        if codes.device != scales.device or codes.device.type != "cuda":
+            raise ValueError("codes and scales must be on one ROCm GPU")
+        self._set(codes, scales, (rows, cols))
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device=None) -> "Fp4Matrix":
+        """Storage with undefined contents."""
+        import torch
+        c, s = _fp4_layout(rows, cols)
+        dev = device if isinstance(device, torch.device) else torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            raise ValueError("codes and scales must be on one ROCm GPU")
+        # made in its layout, so without __init__'s checks
+        m = cls.__new__(cls)
+        m._set(torch.empty(c, dtype=torch.float4_e2m1fn_x2, device=dev),
+               torch.empty(s, dtype=torch.float8_e8m0fnu, device=dev), (rows, cols))
+        return m
+
+    def dequantize(self, dtype=None):
+        """The values it stands for (muonh_fp4_dequantize), fp32 by default or bf16:
+        both hold them exactly."""
+        import torch
+        dtype = torch.float32 if dtype is None else dtype
+        dt = _fp8_dt(torch, dtype)
+        d = _held("the matrix", self)
+        out = torch.empty(self.shape, dtype=dtype, device=self.device)
+        _on_device(torch, self.device, get_lib().muonh_fp4_dequantize, d, out.data_ptr(), dt, max(self.shape[1], 1))
+        return out
+
+
+_NO_FORM4 = Fp4Desc(None, None, 0, 0)
+
+
+def _form4(name: str, o, wanted: bool, rows: int, cols: int, dev):
+    """The output for one form of fp4_quantize: `o` checked, a new one, or None."""
+    if not wanted:
+        if o is not None:
+            raise ValueError(f"{name} given for a form that was not asked for")
+        return None
+    if o is None:
+        return Fp4Matrix.empty(rows, cols, dev)
+    if not isinstance(o, Fp4Matrix):
+        raise TypeError(f"{name} must be an Fp4Matrix")
+    if o.shape != (rows, cols) or o.device != dev:
+        raise ValueError(f"{name} must be a {(rows, cols)} Fp4Matrix on {dev}")
+    _held(name, o)
+    return o
+
+
+def fp4_quantize(x, forms: str = "plain", out: Optional[Fp4Matrix] = None, out_t: Optional[Fp4Matrix] = None):
+    """Quantize x (a 2-d fp32 or bf16 tensor on the GPU whose rows are
+    contiguous, any row stride) to microscaled 4-bit floats (muonh_fp4_quantize).
+
+    forms: "plain" (x itself, grouped along its columns), "transposed" (its
+    transpose, grouped along x's rows) or "both", in one pass. Returns (q, q_t), None in the
+    place of a form that was not asked for; out / out_t: matrices to write into.
+    Runs on the current stream of x's device, outside autograd, as fp8_quantize.
+    """
+    import torch
+    dt, ld = _rows("x", x, getattr(x, "device", None))
+    dev = x.device
+    if forms not in FP8_FORMS:
+        raise ValueError(f"forms must be one of {FP8_FORMS}, got {forms!r}")
+    rows, cols = x.shape
+    q = _form4("out", out, forms != "transposed", rows, cols, dev)
+    qt = _form4("out_t", out_t, forms != "plain", cols, rows, dev)
+    d, t = _NO_FORM4 if q is None else q.desc, _NO_FORM4 if qt is None else qt.desc
+    _on_device(torch, dev, get_lib().muonh_fp4_quantize, x.data_ptr(), dt, rows, cols, ld, d.codes, d.scales, t.codes,
+               t.scales)
+    for o in (out, out_t):
+        if o is not None:
+            _written(o.codes, o.scales)
+    return q, qt
+
+
+def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=None, accumulate: bool = False):
+    """out[i][j] = sum_k a[i][k] * b[j][k] (muonh_fp4_matmul), plus out's old
+    values with accumulate=True.
+
+    out: a 2-d fp32 or bf16 tensor (a rows x b rows) whose rows are contiguous;
+    otherwise a new one of out_dtype (default bfloat16). Products and the sums of a group of 32
+    are exact, other sums fp32. The products of a linear layer as for fp8_matmul; here
+    a weight's transposed form is a quantization of its own (forms="both"), since groups
+    lie along k. Runs on the current stream of the operands' device, outside autograd.
+    """
+    import torch
+    for name, m in (("a", a), ("b", b)):
+        if not isinstance(m, Fp4Matrix):
+            raise TypeError(f"{name} must be an Fp4Matrix")
+    da, db = _held("a", a), _held("b", b)
+    dev = a.device
+    if dev != b.device:
+        raise ValueError(f"a is on {dev}, b on {b.device}")
+    if a.shape[1] != b.shape[1]:
+        raise ValueError(f"a has {a.shape[1]} columns, b {b.shape[1]}")
+    m, n = shape = (a.shape[0], b.shape[0])
+    given = out is not None
+    if not given:
+        if accumulate:
+            raise ValueError("accumulate=True needs out")
+        out = torch.empty(shape, device=dev, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+    dt, ld = _rows("out", out, dev, shape, out_dtype)
+    lib = get_lib()
+    nbytes = lib.muonh_fp4_matmul_workspace_bytes(m, n, a.shape[1])
+    # from torch's allocator on the current stream, as fp8_matmul's
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _on_device(torch, dev, lib.muonh_fp4_matmul, da, db, out.data_ptr(), dt, ld, 1 if accumulate else 0,
+               None if ws is None else ws.data_ptr(), nbytes)
     if given:
         _written(out)
     return out

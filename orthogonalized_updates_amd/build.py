@@ -15,7 +15,8 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libmuonh.so"
 SOURCES = ["muonh_abi.hip", "ns_gemm.hip", "elementwise.hip", "adamw.hip", "fp8_quantize.hip",
-           "fp8_matmul.hip", "rms_norm.hip", "embedding.hip"]
+           "fp8_matmul.hip", "rms_norm.hip", "embedding.hip",
+           "fp4_quantize.hip", "fp4_matmul.hip"]
 ARCH = "gfx950"
 
 

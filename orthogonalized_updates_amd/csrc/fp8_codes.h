@@ -1,6 +1,6 @@
-// Device code of the block-scaled e4m3 format (include/muonh.h) that its
-// producers share (fp8_quantize.hip, rms_norm.hip): maxima of magnitudes, scale
-// bytes, conversions.
+// Device code that the producers of block-scaled matrices share
+// (fp8_quantize.hip, rms_norm.hip, fp4_quantize.hip): maxima of magnitudes, patches of a tile, and
+// of the e4m3 format (include/muonh.h) scale bytes and conversions.
 #pragma once
 
 #include <type_traits>
@@ -78,6 +78,61 @@ __device__ __forceinline__ uint2 codes8(uint32_t a, uint32_t b, uint32_t c, uint
   const s16x2 x = two(two(s16x2{0, 0}, a, std::false_type{}), b, std::true_type{});
   const s16x2 y = two(two(s16x2{0, 0}, c, std::false_type{}), d, std::true_type{});
   return make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
+}
+
+// 8 consecutive entries from i, at any multiple of the entry's size (gfx950
+// takes vector accesses at any address).
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// A thread's 8 x 8 entries: zeros past the matrix.
+__device__ __forceinline__ void load_patch(const float* p, int64_t ld, int64_t r0, int64_t c0, int64_t rows,
+                                           int64_t cols, float (&v)[8][8]) {
+  if (c0 + 8 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // rows past the end reload the last one, so that no load waits in a branch
+      const int64_t r = r0 + i < rows ? r0 + i : rows - 1;
+      const f32x4_a4* q = reinterpret_cast<const f32x4_a4*>(p + r * ld + c0);
+      const f32x4_a4 a = q[0], b = q[1];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[i][k] = a[k];
+        v[i][4 + k] = b[k];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i >= rows)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = r0 + i < rows && c0 + j < cols ? p[(r0 + i) * ld + c0 + j] : 0.f;
+  }
+}
+__device__ __forceinline__ void load_patch(const uint16_t* p, int64_t ld, int64_t r0, int64_t c0, int64_t rows,
+                                           int64_t cols, u32x4_a2 (&v)[8]) {
+  if (c0 + 8 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + i < rows ? r0 + i : rows - 1;
+      v[i] = *reinterpret_cast<const u32x4_a2*>(p + r * ld + c0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i >= rows) v[i] = u32x4_a2{0, 0, 0, 0};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        auto at = [&](int64_t c) { return r0 + i < rows && c < cols ? (uint32_t)p[(r0 + i) * ld + c] : 0u; };
+        v[i][j] = at(c0 + 2 * j) | at(c0 + 2 * j + 1) << 16;
+      }
+  }
 }
 
 // The scale byte of block column kb of one scale row; the block of the last
