@@ -267,10 +267,15 @@ __device__ __forceinline__ void stage_barrier() {
 
 // A pointer that is the same in all lanes, in scalar registers (the compiler
 // may compute uniform values in vector registers, which the DMA's base cannot be).
+// A memory instruction must not read a scalar register in the 5 cycles after a vector
+// instruction wrote it; the compiler sees to that for its own instructions, not for
+// those in inline asm. So the wait is here, between the reads of the lanes and any use of the
+// pointer: without it a DMA took a stale half of its base (GPU memory fault).
 __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
   const uint64_t u = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+  uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+  uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+  asm volatile("s_nop 4" : "+s"(lo), "+s"(hi));
   return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
 }
 
