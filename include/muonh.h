@@ -538,8 +538,8 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
  *     all of it NaN, and zero codes.
  * Storage of a rows x cols matrix: codes, row-major, two to a byte, the first in the
  * low 4 bits, row pitch muonh_fp4_ld(cols) = cols rounded up to 256, over 2, bytes, zeros past
- * cols; scales, row-major, row pitch muonh_fp4_scale_ld(cols) = cols rounded up to 512,
- * over 32, bytes, zeros past ceil(cols/32). Both 16-byte aligned. The quantizing calls write all of
+ * cols; scales, row-major, row pitch muonh_fp4_scale_ld(cols) = cols rounded up to 256,
+ * over 32, bytes, zeros past ceil(cols/32). codes 16-byte, scales 8-byte aligned. The quantizing calls write all of
  * it; an operand of muonh_fp4_matmul from elsewhere needs the zero codes past cols, and scale
  * bytes there that are not 255. Matrices without rows or columns are allowed.
  */

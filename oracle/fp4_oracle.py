@@ -39,7 +39,7 @@ def quantize(x: np.ndarray):
     """(codes, one to a byte, rows x padded columns; scale bytes, padded)."""
     x = np.asarray(x, np.float64)
     rows, cols = x.shape
-    ld, sld = -(-cols // 256) * 256, -(-cols // 512) * 16
+    ld, sld = -(-cols // 256) * 256, -(-cols // 256) * 8
     codes, scales = np.zeros((rows, ld), np.uint8), np.zeros((rows, sld), np.uint8)
     for r in range(rows):
         for g in range(-(-cols // GROUP)):

@@ -907,7 +907,7 @@ def _fp4_layout(rows: int, cols: int):
     """(codes shape, scales shape) of a rows x cols matrix, in bytes."""
     if not (0 <= rows <= MUONH_MAX_FP8_DIM and 0 <= cols <= MUONH_MAX_FP8_DIM):
         raise ValueError(f"shape {(rows, cols)} out of [0, {MUONH_MAX_FP8_DIM}]")
-    return (rows, _up(cols, 256) // 2), (rows, _up(cols, 512) // FP4_GROUP)
+    return (rows, _up(cols, 256) // 2), (rows, _up(cols, 256) // FP4_GROUP)
 
 
 class Fp4Matrix(_BlockMatrix):
@@ -916,7 +916,7 @@ class Fp4Matrix(_BlockMatrix):
 
     codes: torch.float4_e2m1fn_x2 (two codes to a byte, the first in the low half),
     rows x (cols rounded up to 256, over 2), zeros past cols; scales:
-    torch.float8_e8m0fnu, rows x (cols rounded up to 512, over 32); the byte 255 is
+    torch.float8_e8m0fnu, rows x (cols rounded up to 256, over 32); the byte 255 is
     NaN. Both contiguous, on one GPU. shape: (rows, cols). Read-only attributes, and
     moved tensors, as for Fp8Matrix.
     """

@@ -18,8 +18,7 @@ constexpr int kGroup = 32;   // entries per scale
 constexpr int kStep = 256;   // entries that a product takes at a time: 128 bytes of codes, 8 of scales
 
 __host__ __device__ inline int64_t code_ld(int64_t cols) { return ceil_div(cols, kStep) * (kStep / 2); }
-// two steps' scales are 16 bytes
-__host__ __device__ inline int64_t scale_ld(int64_t cols) { return ceil_div(cols, 2 * kStep) * 16; }
+__host__ __device__ inline int64_t scale_ld(int64_t cols) { return ceil_div(cols, kStep) * (kStep / kGroup); }
 
 inline int check_matrix(const char* name, const muonh_fp4_matrix* x) {
   if (!x) return fail(MUONH_EINVAL, "%s is NULL", name);
@@ -28,8 +27,8 @@ inline int check_matrix(const char* name, const muonh_fp4_matrix* x) {
                 MUONH_MAX_FP8_DIM);
   if (x->rows == 0 || x->cols == 0) return MUONH_OK;
   if (!x->codes || !x->scales) return fail(MUONH_EINVAL, "%s: codes and scales must not be NULL", name);
-  if (reinterpret_cast<uintptr_t>(x->codes) & 15u || reinterpret_cast<uintptr_t>(x->scales) & 15u)
-    return fail(MUONH_EINVAL, "%s: codes and scales must be 16-byte aligned", name);
+  if (reinterpret_cast<uintptr_t>(x->codes) & 15u || reinterpret_cast<uintptr_t>(x->scales) & 7u)
+    return fail(MUONH_EINVAL, "%s: codes must be 16-byte and scales 8-byte aligned", name);
   return MUONH_OK;
 }
 

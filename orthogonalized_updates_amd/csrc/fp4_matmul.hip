@@ -55,10 +55,22 @@ __device__ __forceinline__ void mma_block(const Frag (&x)[NX], const Frag (&y)[N
 // A lane's two of a row's 8 scale bytes.
 __device__ __forceinline__ Scales scales_of(u32x2 b, int shift) { return Scales{(int)(b[0] >> shift), (int)(b[1] >> shift)}; }
 
+// A block's scales in LDS: for each 64 rows bytes 0-3 of them all, then bytes 4-7, as two DMAs write them
+// (there is none of 8 bytes per lane).
+__device__ __forceinline__ void dma_scales(const uint8_t* p, uint32_t off, uint32_t m0) {
+  dma4s(p, off, m0);
+  dma4s(p + 4, off, m0 + 256);
+}
+// Row `first` + r's, first a multiple of 16.
+__device__ __forceinline__ u32x2 row_scales(const char* lds, int first, int r) {
+  const char* p = lds + (first >> 6) * 512 + ((first & 63) + r) * 4;
+  return u32x2{*reinterpret_cast<const unsigned int*>(p), *reinterpret_cast<const unsigned int*>(p + 256)};
+}
+
 // ---- 128 x 128 tiles: two groups of 4 waves that take the blocks in turn, a ring of 4 stages ----
 constexpr int kOpStage = kT * kRow;        // 16 KB
 constexpr int kStageBytes = 2 * kOpStage;  // A, then B
-constexpr int kScaleBytes = 2 * kT * 16;   // 16 bytes of each row of both operands: two blocks' scales
+constexpr int kScaleBytes = 2 * kT * 8;    // of both operands' rows: bytes 0-3 of 64 rows, bytes 4-7 of them, ...
 constexpr int kRing = 4;
 
 template <typename T>
@@ -92,19 +104,19 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
   const uint8_t* codes = op.codes + first * op.ld;
   const uint8_t* scales = op.scales + first * op.sld;
   const uint32_t dst = base + (is_a ? 0 : kOpStage) + (w4 & 1) * 64 * kRow;
-  const uint32_t sdst = base + kRing * kStageBytes + w4 * 1024;
+  const uint32_t sdst = base + kRing * kStageBytes + w4 * 512;
   auto fetch_part = [&](int s, int c) {  // quarter c
     const int slot = s & (kRing - 1);
     const int64_t k = (int64_t)s * kRow;
 #pragma unroll
     for (int q = 2 * c; q < 2 * c + 2; ++q) dma16s(codes + k, off[q], dst + slot * kStageBytes + q * 1024);
-    if (c == 3) dma16s(scales + (int64_t)(s >> 1) * 16, soff, sdst + slot * kScaleBytes);
+    if (c == 3) dma_scales(scales + (int64_t)s * 8, soff, sdst + slot * kScaleBytes);
   };
   auto fetch = [&](int s) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) fetch_part(s, c);
   };
-  constexpr int kOps = 9;  // memory operations of fetch()
+  constexpr int kOps = 10;  // memory operations of fetch()
 
   const int wm = w4 >> 1, wn = w4 & 1, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kRow + ((g ^ (r16 & 7)) << 4);
@@ -116,7 +128,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
   auto block = [&](int s, auto more) {
     constexpr bool kMore = decltype(more)::value;
     const char* st = lds + (s & (kRing - 1)) * kStageBytes;
-    const char* ss = lds + kRing * kStageBytes + (s & (kRing - 1)) * kScaleBytes + (s & 1) * 8;
+    const char* ss = lds + kRing * kStageBytes + (s & (kRing - 1)) * kScaleBytes;
     auto frag = [&](const char* p) {
       return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
     };
@@ -126,8 +138,8 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(st + (64 * wm + 16 * f) * kRow);
       fb[f] = frag(st + kOpStage + (64 * wn + 16 * f) * kRow);
-      ba[f] = *reinterpret_cast<const u32x2*>(ss + (64 * wm + 16 * f + r16) * 16);
-      bb[f] = *reinterpret_cast<const u32x2*>(ss + (kT + 64 * wn + 16 * f + r16) * 16);
+      ba[f] = row_scales(ss, 64 * wm + 16 * f, r16);
+      bb[f] = row_scales(ss, kT + 64 * wn + 16 * f, r16);
       if constexpr (kMore) fetch_part(s + 3, f);
     }
     stage_barrier<(kMore ? kOps : 0)>();
@@ -178,7 +190,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
 // ---- 256 x 256 and 192 x 256 tiles: two groups of 4 waves, four phases per block, two stages ----
 constexpr int kBigOp = kB * kRow;       // 32 KB
 constexpr int kBigStage = 2 * kBigOp;   // A, then B
-constexpr int kBigScales = 2 * kB * 16; // a's rows, then b's: 2 blocks each
+constexpr int kBigScales = 2 * kB * 8;  // a's rows, then b's
 
 template <typename T, int FA, int G>
 __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const uint8_t* pa, const uint8_t* pb,
@@ -193,29 +205,29 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
     return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
   };
   auto bytes = [&](int s, int row) {
-    const char* q = lds + 2 * kBigStage + (s & 1) * kBigScales + (s & 1) * 8;
-    return *reinterpret_cast<const u32x2*>(q + (row + r16) * 16);
+    return row_scales(lds + 2 * kBigStage + (s & 1) * kBigScales, row, r16);
   };
   constexpr int kA1 = 2 * FA - 3;         // a's rows by a wave of group 0, 8 per instruction
-  constexpr int kOps[2] = {6, kA1 + 1};   // memory operations of a part
+  constexpr int kOps[2] = {G == 1 ? 6 : 7, kA1 + 2};  // memory operations of a part
+  constexpr int kCalls[2] = {6, kA1 + 1};             // calls of fetch() for it
   auto fetch = [&](int s, int part, int q) {
     const uint32_t st = base + (s & 1) * kBigStage;
-    const uint32_t sc = base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 1024;
-    const int64_t k = (int64_t)s * kRow, ks = (int64_t)(s >> 1) * 16;
+    const uint32_t sc = base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 512;
+    const int64_t k = (int64_t)s * kRow, ks = (int64_t)s * 8;
     if (G == 1) {
       if (q < 3) dma16s(pb + k, off[q], st + kBigOp + (20 + 3 * w4 + q) * 1024);
       else dma16s(pa + k, off[q], st + (3 * w4 + q - 3) * 1024);
     } else if (part == 0) {
       if (q < 5) dma16s(pb + k, off[q], st + kBigOp + (5 * w4 + q) * 1024);
-      else dma16s(scb + ks, sob, sc + kB * 16);
+      else dma_scales(scb + ks, sob, sc + kB * 8);
     } else {
       if (q < kA1) dma16s(pa + k, off[5 + q], st + (12 + kA1 * w4 + q) * 1024);
-      else dma16s(sca + ks, soa, sc);
+      else dma_scales(sca + ks, soa, sc);
     }
   };
   auto fetch_all = [&](int s, int part) {
 #pragma unroll
-    for (int q = 0; q < kOps[part]; ++q) fetch(s, part, q);
+    for (int q = 0; q < kCalls[part]; ++q) fetch(s, part, q);
   };
   auto load_a = [&](int s, int half, auto dma, int t) {
     const char* p = lds + (s & 1) * kBigStage + (2 * G + half) * 16 * FA * kRow;
@@ -225,7 +237,7 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
       ba[f] = bytes(s, (2 * G + half) * 16 * FA + 16 * f);
       if constexpr (decltype(dma)::value)
 #pragma unroll
-        for (int q = kOps[0] * f / FA; q < kOps[0] * (f + 1) / FA; ++q) fetch(t, 0, q);
+        for (int q = kCalls[0] * f / FA; q < kCalls[0] * (f + 1) / FA; ++q) fetch(t, 0, q);
     }
   };
   auto load_b = [&](int s, auto dma, int t) {
@@ -236,7 +248,7 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
       bb[f] = bytes(s, kB + 64 * w4 + 16 * f);
       if constexpr (decltype(dma)::value)
 #pragma unroll
-        for (int q = kOps[1] * f / 4; q < kOps[1] * (f + 1) / 4; ++q) fetch(t, 1, q);
+        for (int q = kCalls[1] * f / 4; q < kCalls[1] * (f + 1) / 4; ++q) fetch(t, 1, q);
     }
   };
   auto mul = [&](int half) {
@@ -388,7 +400,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_matmul4_direct(MatArgs a) {
 
 // ---- 64 x 64 tiles: an LDS stage per wave, the waves share out the blocks ----
 constexpr int kSmallOp = kS * kRow;                      // 8 KB
-constexpr int kSmallStage = 2 * kSmallOp + 2 * kS * 16;  // both operands, then 16 bytes of scales per row
+constexpr int kSmallStage = 2 * kSmallOp + 2 * kS * 8;   // both operands, then their scales
 
 template <typename T>
 __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
@@ -416,14 +428,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
   const uint8_t *sa = a.a.scales + i0 * a.a.sld, *sb = a.b.scales + j0 * a.b.sld;
   char* st = lds + wave * kSmallStage;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds + wave * kSmallStage;
-  auto fetch = [&](int kb, bool first) {
+  auto fetch = [&](int kb) {
     const int64_t k = (int64_t)kb * kRow;
 #pragma unroll
     for (int q = 0; q < 16; ++q) dma16s((q < 8 ? pa : pb) + k, off[q], base + q * 1024);
-    if (first || (kb & 1) == 0) {
-      dma16s(sa + (int64_t)(kb >> 1) * 16, soa, base + 2 * kSmallOp);
-      dma16s(sb + (int64_t)(kb >> 1) * 16, sob, base + 2 * kSmallOp + kS * 16);
-    }
+    dma_scales(sa + (int64_t)kb * 8, soa, base + 2 * kSmallOp);
+    dma_scales(sb + (int64_t)kb * 8, sob, base + 2 * kSmallOp + kS * 8);
   };
   const int foff = r16 * kRow + ((g ^ (r16 & 7)) << 4);
   f32x4 acc[4][4];
@@ -435,7 +445,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
   const int order = 2 * (wave & 3) + (wave >> 2), nk = max(kb1 - kb0, 0);
   int kb = kb0 + (int)((int64_t)order * nk >> 3);
   const int end = kb0 + (int)((int64_t)(order + 1) * nk >> 3);
-  if (kb < end) fetch(kb, true);
+  if (kb < end) fetch(kb);
   for (; kb < end; ++kb) {
     // this wave's block has landed; the empty asm keeps the reads below the wait
     __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xF << 8));  // vmcnt(0)
@@ -445,20 +455,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
     auto frag = [&](const char* p) {
       return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
     };
-    const char* ss = st + 2 * kSmallOp + (kb & 1) * 8;
+    const char* ss = st + 2 * kSmallOp;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(st + 16 * f * kRow);
       fb[f] = frag(st + kSmallOp + 16 * f * kRow);
-      ba[f] = *reinterpret_cast<const u32x2*>(ss + (16 * f + r16) * 16);
-      bb[f] = *reinterpret_cast<const u32x2*>(ss + (kS + 16 * f + r16) * 16);
+      ba[f] = row_scales(ss, 16 * f, r16);
+      bb[f] = row_scales(ss, kS + 16 * f, r16);
     }
     if (kb + 1 < end) {
       // the reads have retired before the stage is refilled
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4) | (0 << 8));  // lgkmcnt(0)
       asm volatile("" ::: "memory");
-      fetch(kb + 1, false);
+      fetch(kb + 1);
     }
     Scales ea[4], eb[4];
 #pragma unroll

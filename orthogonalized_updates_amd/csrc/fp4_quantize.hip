@@ -277,8 +277,8 @@ int muonh_fp4_quantize(const void* src, int32_t dtype, int64_t rows, int64_t col
   if (!codes && !codes_t) return fail(MUONH_EINVAL, "no output given");
   const int esize = dtype == MUONH_DT_BF16 ? 2 : 4;
   if (misaligned(src, esize)) return fail(MUONH_EINVAL, "src is not aligned to its type");
-  if (misaligned(codes, 16) || misaligned(codes_t, 16) || misaligned(scales, 16) || misaligned(scales_t, 16))
-    return fail(MUONH_EINVAL, "codes and scales must be 16-byte aligned");
+  if (misaligned(codes, 16) || misaligned(codes_t, 16) || misaligned(scales, 8) || misaligned(scales_t, 8))
+    return fail(MUONH_EINVAL, "codes must be 16-byte and scales 8-byte aligned");
   if (!fp8::tiles_fit(rows, cols)) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more");
   const Span spans[5] = {span("src", src, ((rows - 1) * src_ld + cols) * esize), span("codes", codes, rows * code_ld(cols)),
                          span("scales", scales, rows * scale_ld(cols)), span("codes_t", codes_t, cols * code_ld(rows)),

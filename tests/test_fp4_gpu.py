@@ -184,7 +184,7 @@ def matrix(codes, scales, shape):
 def random_matrix(rows, cols, seed, spread=0):
     """(Fp4Matrix, its fp64 values): any codes; scales of one power per row, or spread along it."""
     rng = np.random.default_rng((seed, rows, cols))
-    ld, sld = -(-cols // 256) * 256, -(-cols // 512) * 16
+    ld, sld = -(-cols // 256) * 256, -(-cols // 256) * 8
     codes = np.zeros((rows, ld), np.uint8)
     codes[:, :cols] = rng.integers(0, 16, (rows, cols))
     scales = np.zeros((rows, sld), np.uint8)
@@ -241,7 +241,7 @@ def test_small_sums_survive_large_products_that_cancel(m, n, k):
     rng = np.random.default_rng(5)
     ca, cb = rng.integers(0, 16, (m, k)).astype(np.uint8), rng.integers(0, 16, (n, k)).astype(np.uint8)
     ca[:, 160:192], cb[:, 160:192] = ca[:, :32] ^ 8, cb[:, :32]
-    sld = -(-k // 512) * 16
+    sld = -(-k // 256) * 8
     sa, sb = np.full((m, sld), 127, np.uint8), np.full((n, sld), 127, np.uint8)
     sa[:, [0, 5]] = 127 + 12
     want = reference(fo.values(fo.pack(ca), sa, (m, k)), fo.values(fo.pack(cb), sb, (n, k)))
@@ -270,7 +270,7 @@ def test_ends_of_the_range():
     codes = lambda r: np.pad(rng.integers(0, 16, (r, k)).astype(np.uint8), ((0, 0), (0, 192)))  # noqa: E731
     ca, cb = codes(m), codes(n)
     for ea, eb in ((-70, -72), (-126, -14), (-60, -60), (-127, 100), (60, 56), (127, -20), (-127, 127)):
-        sa, sb = np.full((m, 16), 127 + ea, np.uint8), np.full((n, 16), 127 + eb, np.uint8)
+        sa, sb = np.full((m, 8), 127 + ea, np.uint8), np.full((n, 8), 127 + eb, np.uint8)
         va, vb = fo.values(fo.pack(ca), sa, (m, k)), fo.values(fo.pack(cb), sb, (n, k))
         out = mh().fp4_matmul(matrix(ca, sa, (m, k)), matrix(cb, sb, (n, k)), out_dtype=torch.float32)
         want = reference(va, vb)
