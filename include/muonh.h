@@ -513,8 +513,8 @@ int muonh_embedding(const void* ids, int32_t id_bytes, int64_t n, int64_t first,
  * The tokens are sorted by their rows, stably, and each row's sum is taken in
  * fp32 in an order that n, cols and the ids fix: deterministic, no atomics.
  * workspace: DEVICE, 256-byte aligned, at least
- * muonh_embedding_backward_workspace_bytes(n, cols) bytes; calls in flight at once
- * need workspaces of their own. Asynchronous on `stream`, capturable.
+ * muonh_embedding_backward_workspace_bytes(n, cols) bytes (NULL if that is 0); calls in flight
+ * at once need workspaces of their own. Asynchronous on `stream`, capturable.
  * Errors: as muonh_embedding (rows may be 0), MUONH_ESHAPE also where dy has more than 2^38
  * entries, MUONH_EWORKSPACE.
  */

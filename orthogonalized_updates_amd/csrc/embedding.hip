@@ -21,7 +21,7 @@ using fp8::overlap;
 using namespace rows;
 
 constexpr int kMaxGrid = 1 << 20;
-// of dy: k_sums' launches stay below 2^32 threads
+// of dy: the launches of k_sums and k_few stay below 2^32 threads
 constexpr int64_t kMaxEntries = 1LL << 38;
 
 struct Ids {
@@ -87,6 +87,136 @@ __global__ __launch_bounds__(256) void k_lookup(LookArgs a) {
   }
 }
 
+// ---- the gradient of few tokens ------------------------------------------------------
+// Up to kFewMax tokens, in one launch: a workgroup to each token and 512 columns,
+// which does nothing unless its token is the first of its row, and else sums the row's tokens in their order:
+// up to 8 of them by one wave, more by 4, a quarter each, joined in order. Where G starts
+// at zero, the workgroups past `summing` clear the rows that do not occur.
+constexpr int kFewMax = 1024;
+struct FewArgs {
+  Ids ids;
+  const void* dy;
+  float* g;
+  int64_t dy_ld, g_ld;
+  int n, cols, slabs, summing, accumulate;
+  float scale;
+};
+
+// Zeros in the rows that no token has, in stretches of kStretch rows: flags in LDS, then
+// the lanes' rows, as many lanes to a row as it has vectors of 4, up to 64.
+constexpr int kStretch = 512;
+__device__ __forceinline__ void clear_others(const FewArgs& a, int64_t block, int64_t blocks, uint32_t* flags) {
+  const int vecs = (a.cols + 3) >> 2;
+  const int lanes = vecs >= 64 ? 64 : vecs > 1 ? 1 << (32 - __builtin_clz((unsigned)vecs - 1)) : 1;
+  const int at = threadIdx.x & (lanes - 1), first = threadIdx.x / lanes, step = 256 / lanes;
+  // equal stretches, so that all workgroups have one where rows are few
+  const int64_t per = min((int64_t)kStretch, max((int64_t)1, ceil_div(a.ids.rows, blocks)));
+  for (int64_t r0 = block * per; r0 < a.ids.rows; r0 += blocks * per) {
+    const int count = (int)min(per, a.ids.rows - r0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kStretch / 32; i += 256) flags[i] = 0;
+    __syncthreads();
+    for (int t = threadIdx.x; t < a.n; t += 256) {
+      const int64_t r = (int64_t)row_of(a.ids, t) - r0;
+      if (r >= 0 && r < count) atomicOr(&flags[r >> 5], 1u << (r & 31));
+    }
+    __syncthreads();
+    for (int r = first; r < count; r += step) {
+      if (flags[r >> 5] >> (r & 31) & 1) continue;
+      float* p = a.g + (r0 + r) * a.g_ld;
+      for (int v = at; v < vecs; v += lanes) {
+        if (4 * v + 4 <= a.cols) *reinterpret_cast<f32x4_a4*>(p + 4 * v) = f32x4{0.f, 0.f, 0.f, 0.f};
+        else
+          for (int j = 4 * v; j < a.cols; ++j) p[j] = 0.f;
+      }
+    }
+  }
+}
+
+template <typename TD>
+__global__ __launch_bounds__(256) void k_few(FewArgs a) {
+  __shared__ uint64_t masks[kFewMax / 64];  // the tokens of this row, t itself and after
+  __shared__ float sums[4][64 * 8 + 8];
+  static_assert(sizeof masks >= kStretch / 8, "the masks also hold the flags");
+  if ((int)blockIdx.x >= a.summing) {
+    clear_others(a, blockIdx.x - a.summing, gridDim.x - a.summing, reinterpret_cast<uint32_t*>(masks));
+    return;
+  }
+  const int t = (int)blockIdx.x / a.slabs, slab = (int)blockIdx.x - t * a.slabs;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t mine = row_of(a.ids, t);
+  if (mine >= (uint32_t)a.ids.rows) return;
+  int earlier = 0;
+  for (int i = 0; i < a.n; i += 256) {
+    const int u = i + (int)threadIdx.x;
+    const bool same = u < a.n && row_of(a.ids, u) == mine;
+    earlier |= same && u < t;
+    const uint64_t mask = __ballot(same && u >= t);
+    if (lane == 0) masks[i / 64 + wave] = mask;
+  }
+  if (__syncthreads_or(earlier)) return;
+  const int words = (a.n + 63) / 64;
+  int count = 0;
+  for (int i = t >> 6; i < words; ++i) count += __popcll(masks[i]);
+  const bool shared = count > 8;
+  if (!shared && wave) return;
+  const int lo = shared ? wave * count >> 2 : 0, hi = shared ? (wave + 1) * count >> 2 : count;
+  const int col = (slab * 64 + lane) * 8, left = a.cols - col;
+  float* o = a.g + (int64_t)mine * a.g_ld + col;
+  Raw<float> old;
+  if (a.accumulate && wave == 0) {
+    if (left >= 8) old.load(o);
+    else old.load(o, left);
+  }
+  float acc[8] = {};
+  int at = 0;  // of the next token among the row's
+  int next[4], have = 0;
+  auto add = [&](int m) {
+    Raw<TD> raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= m) continue;
+      const TD* q = static_cast<const TD*>(a.dy) + (int64_t)next[i] * a.dy_ld + col;
+      if (left >= 8) raw[i].load(q);
+      else raw[i].load(q, left);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < m)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += raw[i].at(j);
+  };
+  for (int i = t >> 6; i < words && at < hi; ++i) {
+    uint64_t mask = masks[i];
+    for (; mask && at < hi; mask &= mask - 1, ++at) {
+      if (at < lo) continue;
+      const int u = 64 * i + __builtin_ctzll(mask);
+      next[3] = have == 3 ? u : next[3];
+      next[2] = have == 2 ? u : next[2];
+      next[1] = have == 1 ? u : next[1];
+      next[0] = have == 0 ? u : next[0];
+      if (++have == 4) {
+        add(4);
+        have = 0;
+      }
+    }
+  }
+  if (have) add(have);
+  if (shared) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = acc[j];
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = acc[j] + sums[1][lane * 8 + j] + sums[2][lane * 8 + j] + sums[3][lane * 8 + j];
+  }
+  if (left <= 0) return;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = a.accumulate ? __builtin_fmaf(acc[j], a.scale, old.at(j)) : acc[j] * a.scale;
+  store8(o, v, left);
+}
+
 // ---- tokens in the order of their rows ---------------------------------------------
 // Zeros over rows x cols floats, ld apart, by blocks `block` of `blocks`.
 struct FillArgs {
@@ -130,14 +260,18 @@ __global__ __launch_bounds__(1024) void k_count(Ids ids, int n, Sorted out, int 
   const int x = threadIdx.x & (kTok - 1), y = threadIdx.x / kTok;
   const int t = (int)blockIdx.x * kTok + x;
   const uint32_t mine = t < n ? keys[t] : 0u;
-  // rows equal to mine count where their token comes first
+  // rows equal to mine count where their token comes first: all of the 4 before t's own 4, and of those some
   int count = 0;
-  const int end = (y + 1) * per;
+  const int end = (y + 1) * per, own = t & ~3;
+#pragma unroll 4
   for (int i = y * per; i < end; i += 4) {
     const u32x4 k = *reinterpret_cast<const u32x4*>(keys + i);
+    const uint32_t below = mine + (i < own ? 1u : 0u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) count += k[j] < mine + (i + j < t ? 1u : 0u) ? 1 : 0;
+    for (int j = 0; j < 4; ++j) count += k[j] < below ? 1 : 0;
   }
+  if (y * per <= own && own < end)
+    for (int i = own; i < t; ++i) count += keys[i] == mine ? 1 : 0;
   uint32_t* sums = keys + all;
   sums[y * kTok + x] = (uint32_t)count;
   __syncthreads();
@@ -345,26 +479,18 @@ __global__ __launch_bounds__(256) void k_sums(SumArgs a) {
 
 // Rows whose tokens go on past the chunk after the one they begin in: the tail
 // and the heads, each of 4 waves a quarter of them, then the quarters in order. A
-// workgroup looks through 64 chunks.
+// workgroup to each chunk and slab; most of them have nothing to do.
 template <int LPR>
 __global__ __launch_bounds__(256) void k_join(SumArgs a) {
   __shared__ float sums[4][64 * 8 + 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c0 = (int)(blockIdx.x / a.slabs) * 64, slab = (int)(blockIdx.x % a.slabs);
+  const int c = (int)(blockIdx.x / a.slabs), slab = (int)(blockIdx.x % a.slabs);
   const int col = (slab * LPR + (lane & (LPR - 1))) * 8, left = lane < LPR ? a.cols - col : 0;
   const uint32_t* key = a.s.key;
   auto key_of = [&](int64_t chunk) { return key[chunk * a.chunk]; };
-  bool mine = false;
+  const uint32_t k = key[(int64_t)(c + 1) * a.chunk - 1];
+  if (k >= a.rows || key_of((int64_t)c + 2) != k || (c > 0 && key[(int64_t)c * a.chunk - 1] == k)) return;
   {
-    const int c = c0 + lane;
-    if (c + 2 < a.chunks) {
-      const uint32_t k = key[(int64_t)(c + 1) * a.chunk - 1];
-      mine = k < a.rows && key_of(c + 2) == k && (c == 0 || key[(int64_t)c * a.chunk - 1] != k);
-    }
-  }
-  for (uint64_t todo = __ballot(mine); todo; todo &= todo - 1) {
-    const int c = c0 + __builtin_ctzll(todo);
-    const uint32_t k = key[(int64_t)(c + 1) * a.chunk - 1];
     int heads = 0;  // chunks c + 2 .. c + 1 + heads
     for (;;) {
       const int64_t q = (int64_t)c + 2 + heads + lane;
@@ -426,7 +552,6 @@ __global__ __launch_bounds__(256) void k_join(SumArgs a) {
       }
       store8(o, v, left);
     }
-    __syncthreads();
   }
 }
 
@@ -437,10 +562,13 @@ struct Plan {
   int lpr, slabs, chunk, chunks, tiles;
   size_t key[2], tok[2], counts, tail, head, bytes;
 };
+// Whether k_few takes the call: a launch has fewer than 2^32 threads.
+bool few(int64_t n, int64_t cols) { return n <= kFewMax && n * ceil_div(cols, 512) < (1 << 23); }
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 Plan plan_of(int64_t n, int64_t cols) {
   Plan p{};
   p.n = n;
+  if (few(n, cols)) return p;
   p.lpr = cols <= 128 ? 16 : 64;
   p.slabs = (int)ceil_div(cols, p.lpr * 8);
   // about 4096 waves, 16 a CU; each chunk pays for its ends
@@ -556,22 +684,45 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
   if (const int err = check_mat(from, cols)) return err;
   if (n * cols > kMaxEntries) return fail(MUONH_ESHAPE, "dy has more than 2^38 entries");
   const Plan p = plan_of(n, cols);
-  if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the call needs %zu bytes", p.bytes);
-  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MUONH_EWORKSPACE, "workspace must be 256-byte aligned");
-  if (workspace_bytes < p.bytes)
-    return fail(MUONH_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, p.bytes);
+  if (p.bytes) {
+    if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the call needs %zu bytes", p.bytes);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MUONH_EWORKSPACE, "workspace must be 256-byte aligned");
+    if (workspace_bytes < p.bytes)
+      return fail(MUONH_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, p.bytes);
+  }
   const Span read[2] = {span_of(from, n, cols), span("ids", ids, n * id_bytes)};
-  const Span written[2] = {span_of(to, rows, cols), span("workspace", workspace, (int64_t)p.bytes)};
+  const Span written[2] = {span_of(to, rows, cols), span("workspace", p.bytes ? workspace : nullptr, (int64_t)p.bytes)};
   for (const Span& w : written)
     for (const Span& r : read)
       if (overlap(w, r)) return fail(MUONH_EALIAS, "%s overlaps %s", w.name, r.name);
   if (overlap(written[0], written[1])) return fail(MUONH_EALIAS, "grad overlaps the workspace");
 
+  const Ids which{ids, id_bytes == 8, first, rows};
+  if (few(n, cols)) {
+    FewArgs a{};
+    a.ids = which;
+    a.dy = dy;
+    a.g = grad;
+    a.dy_ld = dy_ld;
+    a.g_ld = grad_ld;
+    a.n = (int)n;
+    a.cols = (int)cols;
+    a.slabs = (int)ceil_div(cols, 512);
+    a.summing = a.n * a.slabs;
+    a.accumulate = accumulate != 0;
+    a.scale = scale;
+    // a workgroup clears 32 KB or more, 2048 of them at most
+    const int clears = accumulate ? 0 : (int)std::min(std::min<int64_t>(ceil_div(rows * cols, 8192), rows), (int64_t)2048);
+    const dim3 grid((unsigned)(a.summing + clears));
+    if (dy_dtype == MUONH_DT_BF16) hipLaunchKernelGGL((k_few<__bf16>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_few<float>), grid, dim3(256), 0, s, a);
+    return launched("embedding backward");
+  }
+
   char* ws = static_cast<char*>(workspace);
   auto sorted = [&](int i) {
     return Sorted{reinterpret_cast<uint32_t*>(ws + p.key[i]), reinterpret_cast<uint32_t*>(ws + p.tok[i])};
   };
-  const Ids which{ids, id_bytes == 8, first, rows};
   SumArgs a{};
   if (n <= kCountMax) {
     const int sorting = (int)ceil_div(n, kTok);
@@ -611,7 +762,7 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
   a.rows = (uint32_t)rows;
   a.scale = scale;
   const int64_t groups = (int64_t)p.chunks * p.slabs;
-  const dim3 sums((unsigned)ceil_div(groups, 256 / p.lpr)), join((unsigned)(ceil_div(p.chunks, 64) * p.slabs));
+  const dim3 sums((unsigned)ceil_div(groups, 256 / p.lpr)), join((unsigned)((int64_t)(p.chunks - 2) * p.slabs));
   auto run = [&](auto type) {
     using T = decltype(type);
     if (p.lpr == 16) hipLaunchKernelGGL((k_sums<T, 16>), sums, dim3(256), 0, s, a);

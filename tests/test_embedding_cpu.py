@@ -51,7 +51,7 @@ def test_lookup_of_nothing_is_a_no_op():
     assert _look(cols=0, ld=0, old=0, ids=None, table=None, out=None) == mh.MUONH_OK
 
 
-def _back(ids=A, nb=8, n=100, first=0, dy=2 * A, dt=0, dld=200, scale=1.0, g=3 * A, rows=50, cols=200, ld=200, acc=1, ws=4 * A,
+def _back(ids=A, nb=8, n=2000, first=0, dy=2 * A, dt=0, dld=200, scale=1.0, g=3 * A, rows=50, cols=200, ld=200, acc=1, ws=4 * A,
           size=1 << 34):
     return mh.lib.muonh_embedding_backward(ids, nb, n, first, dy, dt, dld, scale, g, rows, cols, ld, acc, ws, size, None)
 
@@ -82,7 +82,9 @@ def test_workspace():
     f = mh.lib.muonh_embedding_backward_workspace_bytes
     assert f(0, 5) == f(5, 0) == f(-1, 5) == f(BIG, 5) == f(1 << 24, 1 << 15) == 0
     sizes = [f(n, 2048) for n in (1, 777, 8192, 16384, 16385, 1 << 20)]
-    assert all(0 < s < 160 << 20 for s in sizes)
+    assert sizes[0] == sizes[1] == 0 and all(0 < s < 160 << 20 for s in sizes[2:])
+    assert f(1024, 2048) == 0 < f(1025, 2048)
+    assert _back(n=100, ws=None, size=0, g=2 * A) == mh.MUONH_EALIAS  # no workspace asked for
 
 
 def test_python_refuses():

@@ -104,9 +104,9 @@ def test_values_pass_through():
     assert torch.equal(mh().embedding(torch.tensor([0, 5], device="cuda"), t).view(torch.int32), torch.stack([t[0], torch.zeros(6, device="cuda")]).view(torch.int32))
 
 
-# chunks of 4 to 64 tokens; the counting sort up to 16384 tokens, then passes of 8 bits
+# up to 1024 tokens in one launch; else chunks of 4 to 64 tokens, the counting sort up to 16384 tokens, then passes of 8 bits
 SIZES = [(1, 1, 1), (1, 300, 2048), (2, 3, 5), (4, 4, 64), (5, 7, 128), (9, 2, 129), (13, 300, 520), (100, 257, 1001), (777, 5003, 1001),
-         (1000, 256, 2048), (4099, 1000, 100), (3000, 90, 4096), (16384, 3000, 64), (16385, 3000, 64), (20000, 255, 40), (20000, 256, 40),
+         (1000, 256, 2048), (1024, 300, 520), (1025, 300, 520), (1024, 40000, 6), (4099, 1000, 100), (3000, 90, 4096), (16384, 3000, 64), (16385, 3000, 64), (20000, 255, 40), (20000, 256, 40),
          (20000, 257, 40), (50001, 70000, 24), (140000, 66000, 136), (70000, 1 << 24, 1), (9000, 151936, 8)]
 
 
