@@ -37,6 +37,24 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t t) {
   return r < (uint64_t)ids.rows ? (uint32_t)r : (uint32_t)ids.rows;
 }
 
+// The rows of tokens t, t + step, ... (N of them; `rows` from n on), whose loads run together.
+template <int N>
+__device__ __forceinline__ void rows_of(const Ids& ids, int t, int step, int n, uint32_t (&r)[N]) {
+  int64_t id[N];
+  if (ids.wide) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) id[k] = static_cast<const int64_t*>(ids.p)[min(t + k * step, n - 1)];
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) id[k] = static_cast<const int32_t*>(ids.p)[min(t + k * step, n - 1)];
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint64_t v = (uint64_t)id[k] - (uint64_t)ids.first;
+    r[k] = t + k * step < n && v < (uint64_t)ids.rows ? (uint32_t)v : (uint32_t)ids.rows;
+  }
+}
+
 // ---- lookup -------------------------------------------------------------------
 struct LookArgs {
   Ids ids;
@@ -91,14 +109,14 @@ __global__ __launch_bounds__(256) void k_lookup(LookArgs a) {
 // Up to kFewMax tokens, in one launch: a workgroup to each token and 512 columns,
 // which does nothing unless its token is the first of its row, and else sums the row's tokens in their order:
 // up to 8 of them by one wave, more by 4, a quarter each, joined in order. Where G starts
-// at zero, the workgroups past `summing` clear the rows that do not occur.
+// at zero, the first `clearing` workgroups clear the rows that do not occur.
 constexpr int kFewMax = 1024;
 struct FewArgs {
   Ids ids;
   const void* dy;
   float* g;
   int64_t dy_ld, g_ld;
-  int n, cols, slabs, summing, accumulate;
+  int n, cols, slabs, clearing, accumulate;
   float scale;
 };
 
@@ -116,19 +134,22 @@ __device__ __forceinline__ void clear_others(const FewArgs& a, int64_t block, in
     __syncthreads();
     for (int i = threadIdx.x; i < kStretch / 32; i += 256) flags[i] = 0;
     __syncthreads();
-    for (int t = threadIdx.x; t < a.n; t += 256) {
-      const int64_t r = (int64_t)row_of(a.ids, t) - r0;
+    uint32_t occur[kFewMax / 256];
+    rows_of<kFewMax / 256>(a.ids, threadIdx.x, 256, a.n, occur);
+#pragma unroll
+    for (int k = 0; k < kFewMax / 256; ++k) {
+      const int64_t r = (int64_t)occur[k] - r0;
       if (r >= 0 && r < count) atomicOr(&flags[r >> 5], 1u << (r & 31));
     }
     __syncthreads();
     for (int r = first; r < count; r += step) {
       if (flags[r >> 5] >> (r & 31) & 1) continue;
+      // stores of 16 bytes at multiples of 16: single floats before the first and after the last
       float* p = a.g + (r0 + r) * a.g_ld;
-      for (int v = at; v < vecs; v += lanes) {
-        if (4 * v + 4 <= a.cols) *reinterpret_cast<f32x4_a4*>(p + 4 * v) = f32x4{0.f, 0.f, 0.f, 0.f};
-        else
-          for (int j = 4 * v; j < a.cols; ++j) p[j] = 0.f;
-      }
+      const int head = min((int)((0 - (reinterpret_cast<uintptr_t>(p) >> 2)) & 3), a.cols);
+      const int body = (a.cols - head) >> 2;
+      for (int v = at; v < body; v += lanes) *reinterpret_cast<f32x4*>(p + head + 4 * v) = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = at; j < a.cols - 4 * body; j += lanes) p[j < head ? j : 4 * body + j] = 0.f;
     }
   }
 }
@@ -136,28 +157,43 @@ __device__ __forceinline__ void clear_others(const FewArgs& a, int64_t block, in
 template <typename TD>
 __global__ __launch_bounds__(256) void k_few(FewArgs a) {
   __shared__ uint64_t masks[kFewMax / 64];  // the tokens of this row, t itself and after
+  __shared__ uint16_t list[kFewMax];        // them in their order
   __shared__ float sums[4][64 * 8 + 8];
   static_assert(sizeof masks >= kStretch / 8, "the masks also hold the flags");
-  if ((int)blockIdx.x >= a.summing) {
-    clear_others(a, blockIdx.x - a.summing, gridDim.x - a.summing, reinterpret_cast<uint32_t*>(masks));
+  if ((int)blockIdx.x < a.clearing) {
+    clear_others(a, blockIdx.x, a.clearing, reinterpret_cast<uint32_t*>(masks));
     return;
   }
-  const int t = (int)blockIdx.x / a.slabs, slab = (int)blockIdx.x - t * a.slabs;
+  const int b = (int)blockIdx.x - a.clearing, t = b / a.slabs, slab = b - t * a.slabs;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t mine = row_of(a.ids, t);
   if (mine >= (uint32_t)a.ids.rows) return;
   int earlier = 0;
-  for (int i = 0; i < a.n; i += 256) {
-    const int u = i + (int)threadIdx.x;
-    const bool same = u < a.n && row_of(a.ids, u) == mine;
-    earlier |= same && u < t;
-    const uint64_t mask = __ballot(same && u >= t);
-    if (lane == 0) masks[i / 64 + wave] = mask;
+  constexpr int kMine = kFewMax / 256;
+  uint32_t theirs[kMine];
+  uint64_t mask[kMine];
+  rows_of<kMine>(a.ids, threadIdx.x, 256, a.n, theirs);
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int u = k * 256 + (int)threadIdx.x;
+    earlier |= theirs[k] == mine && u < t;
+    mask[k] = __ballot(theirs[k] == mine && u >= t);
+    if (lane == 0) masks[k * 4 + wave] = mask[k];
   }
   if (__syncthreads_or(earlier)) return;
-  const int words = (a.n + 63) / 64;
-  int count = 0;
-  for (int i = t >> 6; i < words; ++i) count += __popcll(masks[i]);
+  int count = 0, before[kMine] = {};
+#pragma unroll
+  for (int i = 0; i < kFewMax / 64; ++i) {
+    const int c = __popcll(masks[i]);
+    count += c;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) before[k] += i < k * 4 + wave ? c : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kMine; ++k)
+    if (mask[k] >> lane & 1)
+      list[before[k] + __popcll(mask[k] & ((1ull << lane) - 1))] = (uint16_t)(k * 256 + threadIdx.x);
+  __syncthreads();
   const bool shared = count > 8;
   if (!shared && wave) return;
   const int lo = shared ? wave * count >> 2 : 0, hi = shared ? (wave + 1) * count >> 2 : count;
@@ -169,39 +205,22 @@ __global__ __launch_bounds__(256) void k_few(FewArgs a) {
     else old.load(o, left);
   }
   float acc[8] = {};
-  int at = 0;  // of the next token among the row's
-  int next[4], have = 0;
-  auto add = [&](int m) {
-    Raw<TD> raw[4];
+  for (int i = lo; i < hi; i += 8) {
+    Raw<TD> raw[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= m) continue;
-      const TD* q = static_cast<const TD*>(a.dy) + (int64_t)next[i] * a.dy_ld + col;
-      if (left >= 8) raw[i].load(q);
-      else raw[i].load(q, left);
+    for (int k = 0; k < 8; ++k) {
+      if (i + k >= hi) continue;
+      const int u = __builtin_amdgcn_readfirstlane(list[i + k]);
+      const TD* q = static_cast<const TD*>(a.dy) + (int64_t)u * a.dy_ld + col;
+      if (left >= 8) raw[k].load(q);
+      else raw[k].load(q, left);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < m)
+    for (int k = 0; k < 8; ++k)
+      if (i + k < hi)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += raw[i].at(j);
-  };
-  for (int i = t >> 6; i < words && at < hi; ++i) {
-    uint64_t mask = masks[i];
-    for (; mask && at < hi; mask &= mask - 1, ++at) {
-      if (at < lo) continue;
-      const int u = 64 * i + __builtin_ctzll(mask);
-      next[3] = have == 3 ? u : next[3];
-      next[2] = have == 2 ? u : next[2];
-      next[1] = have == 1 ? u : next[1];
-      next[0] = have == 0 ? u : next[0];
-      if (++have == 4) {
-        add(4);
-        have = 0;
-      }
-    }
+        for (int j = 0; j < 8; ++j) acc[j] += raw[k].at(j);
   }
-  if (have) add(have);
   if (shared) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = acc[j];
@@ -255,7 +274,13 @@ __global__ __launch_bounds__(1024) void k_count(Ids ids, int n, Sorted out, int 
     return;
   }
   const int per = (int)ceil_div(n, 4 * kSlices) * 4, all = per * kSlices;
-  for (int t = threadIdx.x; t < all; t += 1024) keys[t] = t < n ? row_of(ids, t) : 0xffffffffu;
+  for (int t = threadIdx.x; t < all; t += 8 * 1024) {
+    uint32_t r[8];
+    rows_of<8>(ids, t, 1024, n, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (t + k * 1024 < all) keys[t + k * 1024] = t + k * 1024 < n ? r[k] : 0xffffffffu;
+  }
   __syncthreads();
   const int x = threadIdx.x & (kTok - 1), y = threadIdx.x / kTok;
   const int t = (int)blockIdx.x * kTok + x;
@@ -406,44 +431,61 @@ struct SumArgs {
   float scale;
 };
 
-// LPR lanes take a chunk's LPR * 8 columns, kRows tokens at a time.
+// LPR lanes take a chunk's LPR * 8 columns, kRows tokens at a time: their keys and places come by one
+// load, a lane each, before the rows of the tokens before them are summed.
 template <typename TD, int LPR>
-__global__ __launch_bounds__(256) void k_sums(SumArgs a) {
-  constexpr int kRows = 4;
+__global__ __launch_bounds__(256, 4) void k_sums(SumArgs a) {
+  constexpr int kRows = sizeof(TD) == 2 && LPR == 64 ? 8 : 4;
+  static_assert(kRows + 1 <= 16, "a group's lanes hold a turn's keys");
   int64_t g = (int64_t)blockIdx.x * (256 / LPR);
   if constexpr (LPR == 64) g += __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   else g += threadIdx.x / LPR;
-  if (g >= (int64_t)a.chunks * a.slabs) return;
+  const bool mine = g < (int64_t)a.chunks * a.slabs;
+  if (!mine) g = 0;
   const int c = (int)(g / a.slabs), slab = (int)(g - (int64_t)c * a.slabs);
-  const int col = (slab * LPR + (int)(threadIdx.x & (LPR - 1))) * 8, left = a.cols - col;
+  const int lane = threadIdx.x & 63, gl = lane & (LPR - 1);
+  const int col = (slab * LPR + gl) * 8, left = a.cols - col;
   const int p0 = c * a.chunk, p1 = min(p0 + a.chunk, a.n), lim = min(p1 + a.chunk, a.n);
   const uint32_t* key = a.s.key;
+  uint32_t kv, tv;  // of tokens p + gl
+  auto fetch = [&](int p) {
+    const int i = min(p + gl, a.n - 1);
+    kv = p + gl < a.n ? key[i] : 0xffffffffu;
+    tv = a.s.tok[i];
+  };
+  auto of = [&](uint32_t v, int i) -> uint32_t {
+    if constexpr (LPR == 64) return (uint32_t)__builtin_amdgcn_readlane((int)v, i);
+    else return (uint32_t)__shfl((int)v, (lane & ~(LPR - 1)) + i, 64);
+  };
+  fetch(p0);
   const uint32_t first = key[p0], last = key[p1 - 1];
-  if (first >= a.rows) return;
   // first's tokens began before this chunk: in the one before, which sums them (skip), or earlier (head)
-  const bool cont = p0 > 0 && key[p0 - 1] == first;
-  const bool head = cont && p0 - a.chunk > 0 && key[p0 - a.chunk - 1] == first;
+  const bool cont = p0 > 0 && key[max(p0 - 1, 0)] == first;
+  const bool head = cont && p0 - a.chunk > 0 && key[max(p0 - a.chunk - 1, 0)] == first;
   const bool skip = cont && !head;
   float acc[8] = {};
   bool open = head, pending = false;
   for (int p = p0; p < lim; p += kRows) {
-    uint32_t k[kRows + 1];
+    uint32_t k[kRows + 1], t[kRows];
     bool valid[kRows], end[kRows], store[kRows];
     Raw<TD> raw[kRows];
     Raw<float> old[kRows];
 #pragma unroll
-    for (int i = 0; i <= kRows; ++i) k[i] = p + i < a.n ? key[p + i] : 0xffffffffu;
+    for (int i = 0; i <= kRows; ++i) k[i] = of(kv, i);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) t[i] = of(tv, i);
+    fetch(p + kRows);
     bool any = false, still = open;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      valid[i] = p + i < lim && k[i] < a.rows && !(skip && k[i] == first) &&
+      valid[i] = mine && p + i < lim && k[i] < a.rows && !(skip && k[i] == first) &&
                  (p + i < p1 || (k[i] == last && !(cont && last == first)));
       end[i] = valid[i] && k[i + 1] != k[i];
       store[i] = end[i] && !still;
       if (end[i]) still = false;
       any |= valid[i];
       if (valid[i]) {
-        const TD* q = static_cast<const TD*>(a.dy) + (int64_t)a.s.tok[p + i] * a.dy_ld + col;
+        const TD* q = static_cast<const TD*>(a.dy) + (int64_t)t[i] * a.dy_ld + col;
         if (left >= 8) raw[i].load(q);
         else raw[i].load(q, left);
         if (store[i] && a.accumulate) {
@@ -453,7 +495,7 @@ __global__ __launch_bounds__(256) void k_sums(SumArgs a) {
         }
       }
     }
-    if (!any && p >= p1) break;
+    if (LPR == 64 && !any && p >= p1) break;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       if (!valid[i]) continue;
@@ -708,12 +750,11 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
     a.n = (int)n;
     a.cols = (int)cols;
     a.slabs = (int)ceil_div(cols, 512);
-    a.summing = a.n * a.slabs;
     a.accumulate = accumulate != 0;
     a.scale = scale;
     // a workgroup clears 32 KB or more, 2048 of them at most
-    const int clears = accumulate ? 0 : (int)std::min(std::min<int64_t>(ceil_div(rows * cols, 8192), rows), (int64_t)2048);
-    const dim3 grid((unsigned)(a.summing + clears));
+    a.clearing = accumulate ? 0 : (int)std::min(std::min<int64_t>(ceil_div(rows * cols, 8192), rows), (int64_t)2048);
+    const dim3 grid((unsigned)(a.clearing + a.n * a.slabs));
     if (dy_dtype == MUONH_DT_BF16) hipLaunchKernelGGL((k_few<__bf16>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_few<float>), grid, dim3(256), 0, s, a);
     return launched("embedding backward");
