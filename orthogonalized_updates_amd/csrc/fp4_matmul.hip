@@ -55,28 +55,34 @@ __device__ __forceinline__ void mma_block(const Frag (&x)[NX], const Frag (&y)[N
 // A lane's two of a row's 8 scale bytes.
 __device__ __forceinline__ Scales scales_of(u32x2 b, int shift) { return Scales{(int)(b[0] >> shift), (int)(b[1] >> shift)}; }
 
-// A block's scales in LDS: for each 64 rows bytes 0-3 of them all, then bytes 4-7, as two DMAs write them
-// (there is none of 8 bytes per lane).
-__device__ __forceinline__ void dma_scales(const uint8_t* p, uint32_t off, uint32_t m0) {
-  dma4s(p, off, m0);
-  dma4s(p + 4, off, m0 + 256);
+// Scales in LDS. A block's 8 bytes per row are too few for a DMA of their own: each lane of it would
+// touch a cache line of its own, as many lines as the codes' DMA touches altogether. So a DMA of 4 bytes per
+// lane brings 8 rows' scales of a quad, 4 blocks: 32 bytes per row, a quarter of a tile's rows
+// with each block. Of LDS row r, block b of the quad lies at 8 (b ^ (r / 8 & 1)), so that the 16 rows
+// of a fragment fall on different banks. Past the row's end the last 4 bytes come again (products of 8192 x 8192 x
+// 8192: 300 us with two DMAs per block, 4 bytes of 64 rows each; QUADS).
+constexpr int kQuadRow = 32;
+// The lane's offset for LDS rows 8 i .. + 7 (i: the parity), lane l: row l / 8, dword l % 8; row: the matrix row
+// from the base, quad: which 4 blocks.
+__device__ __forceinline__ uint32_t quad_off(int row, int quad, int i, int lane, int sld) {
+  const int dw = (((lane & 7) >> 1) ^ (i & 1)) * 2 + (lane & 1);
+  return (uint32_t)row * (uint32_t)sld + (uint32_t)min(quad * kQuadRow + dw * 4, sld - 4);
 }
-// Row `first` + r's, first a multiple of 16.
-__device__ __forceinline__ u32x2 row_scales(const char* lds, int first, int r) {
-  const char* p = lds + (first >> 6) * 512 + ((first & 63) + r) * 4;
-  return u32x2{*reinterpret_cast<const unsigned int*>(p), *reinterpret_cast<const unsigned int*>(p + 256)};
+// Row `first` + r's of block s, first a multiple of 16.
+__device__ __forceinline__ u32x2 row_scales(const char* quad, int first, int r, int s) {
+  return *reinterpret_cast<const u32x2*>(quad + (first + r) * kQuadRow + (((s & 3) ^ (r >> 3)) << 3));
 }
 
 // ---- 128 x 128 tiles: two groups of 4 waves that take the blocks in turn, a ring of 4 stages ----
 constexpr int kOpStage = kT * kRow;        // 16 KB
 constexpr int kStageBytes = 2 * kOpStage;  // A, then B
-constexpr int kScaleBytes = 2 * kT * 8;    // of both operands' rows: bytes 0-3 of 64 rows, bytes 4-7 of them, ...
-constexpr int kRing = 4;
+constexpr int kQuadBytes = 2 * kT * kQuadRow;  // a quad's scales, A's then B's
+constexpr int kRing = 4;                   // of stages, and of quads
 
 template <typename T>
 __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
   constexpr bool kPair = sizeof(T) == 2;
-  __shared__ __attribute__((aligned(1024))) char lds[kRing * (kStageBytes + kScaleBytes)];
+  __shared__ __attribute__((aligned(1024))) char lds[kRing * (kStageBytes + kQuadBytes)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int w4 = wave & 3, group = wave >> 2;
@@ -87,7 +93,8 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
   const int64_t ra = (int64_t)ti * kT, rb = (int64_t)tj * kT;
 
   // DMA of a block by one group: waves 0, 1 fill a's 128 rows, waves 2, 3 b's;
-  // 8 instructions of 8 rows, then the scales of 64 rows
+  // 8 instructions of 8 rows, then with block s a quarter of the scales of the quad that
+  // block s + 3 is in: 16 rows a wave. All of a quad have landed when its first block has.
   const bool is_a = w4 < 2;
   const Operand& op = is_a ? a.a : a.b;
   const int64_t first = is_a ? ra : rb;
@@ -100,23 +107,29 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
     const int lr = 64 * (w4 & 1) + 8 * q + (lane >> 3);
     off[q] = (uint32_t)(row(lr) - first) * (uint32_t)op.ld + (uint32_t)(((lane & 7) ^ (lr & 7)) << 4);
   }
-  const uint32_t soff = (uint32_t)(row(64 * (w4 & 1) + lane) - first) * (uint32_t)op.sld;
+  const int sld = (int)op.sld;
   const uint8_t* codes = op.codes + first * op.ld;
   const uint8_t* scales = op.scales + first * op.sld;
   const uint32_t dst = base + (is_a ? 0 : kOpStage) + (w4 & 1) * 64 * kRow;
-  const uint32_t sdst = base + kRing * kStageBytes + w4 * 512;
+  auto fetch_scales = [&](int s) {
+    const int quad = (s + 3) >> 2, r0 = 32 * ((s + 3) & 3) + 16 * (w4 & 1);
+    const uint32_t to = base + kRing * kStageBytes + (quad & (kRing - 1)) * kQuadBytes + (is_a ? 0 : kT * kQuadRow) + r0 * kQuadRow;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      dma4s(scales, quad_off((int)(row(r0 + 8 * i + (lane >> 3)) - first), quad, i, lane, sld), to + i * 8 * kQuadRow);
+  };
   auto fetch_part = [&](int s, int c) {  // quarter c
     const int slot = s & (kRing - 1);
     const int64_t k = (int64_t)s * kRow;
 #pragma unroll
     for (int q = 2 * c; q < 2 * c + 2; ++q) dma16s(codes + k, off[q], dst + slot * kStageBytes + q * 1024);
-    if (c == 3) dma_scales(scales + (int64_t)s * 8, soff, sdst + slot * kScaleBytes);
+    if (c == 3) fetch_scales(s);
   };
   auto fetch = [&](int s) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) fetch_part(s, c);
   };
-  constexpr int kOps = 10;  // memory operations of fetch()
+  constexpr int kOps = 10;  // memory operations of fetch(): 8 of codes, 2 of scales
 
   const int wm = w4 >> 1, wn = w4 & 1, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kRow + ((g ^ (r16 & 7)) << 4);
@@ -128,7 +141,7 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
   auto block = [&](int s, auto more) {
     constexpr bool kMore = decltype(more)::value;
     const char* st = lds + (s & (kRing - 1)) * kStageBytes;
-    const char* ss = lds + kRing * kStageBytes + (s & (kRing - 1)) * kScaleBytes;
+    const char* ss = lds + kRing * kStageBytes + ((s >> 2) & (kRing - 1)) * kQuadBytes;
     auto frag = [&](const char* p) {
       return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
     };
@@ -138,8 +151,8 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(st + (64 * wm + 16 * f) * kRow);
       fb[f] = frag(st + kOpStage + (64 * wn + 16 * f) * kRow);
-      ba[f] = row_scales(ss, 64 * wm + 16 * f, r16);
-      bb[f] = row_scales(ss, kT + 64 * wn + 16 * f, r16);
+      ba[f] = row_scales(ss, 64 * wm + 16 * f, r16, s);
+      bb[f] = row_scales(ss, kT + 64 * wn + 16 * f, r16, s);
       if constexpr (kMore) fetch_part(s + 3, f);
     }
     stage_barrier<(kMore ? kOps : 0)>();
@@ -152,11 +165,17 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
     mma_block<4, 4>(fb, fa, sb, sa, acc);
     stage_barrier<63>();
   };
+  // the first quad: what blocks -3, -2, -1 and 0 would bring; it is waited for with block 0, by group 1
   if (group == 0) {
     if (nk > 1) fetch(1);
     stage_barrier<63>();
   } else {
-    if (nk > 0) fetch(0);
+    if (nk > 0) {
+      fetch_scales(-3);
+      fetch_scales(-2);
+      fetch_scales(-1);
+      fetch(0);
+    }
     if (nk > 2) {
       fetch(2);
       stage_barrier<kOps>();  // block 0 has landed
@@ -190,13 +209,14 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
 // ---- 256 x 256 and 192 x 256 tiles: two groups of 4 waves, four phases per block, two stages ----
 constexpr int kBigOp = kB * kRow;       // 32 KB
 constexpr int kBigStage = 2 * kBigOp;   // A, then B
-constexpr int kBigScales = 2 * kB * 8;  // a's rows, then b's
+constexpr int kBigQuad = 2 * kB * kQuadRow;  // a quad's scales: a's rows, then b's
 
 template <typename T, int FA, int G>
 __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const uint8_t* pa, const uint8_t* pb,
                                          const uint8_t* sca, const uint8_t* scb, const uint32_t (&off)[10],
-                                         uint32_t soa, uint32_t sob, int nk, int wave, int lane,
+                                         int last_a, int last_b, int sld, int nk, int wave, int lane,
                                          f32x4 (&acc)[4][2 * FA]) {
+  constexpr bool kPair = sizeof(T) == 2;
   const int w4 = wave & 3, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kRow + ((g ^ (r16 & 7)) << 4);
   Frag fa[FA], fb[4];
@@ -205,29 +225,36 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
     return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
   };
   auto bytes = [&](int s, int row) {
-    return row_scales(lds + 2 * kBigStage + (s & 1) * kBigScales, row, r16);
+    return row_scales(lds + 2 * kBigStage + ((s >> 2) & 1) * kBigQuad, row, r16, s);
   };
   constexpr int kA1 = 2 * FA - 3;         // a's rows by a wave of group 0, 8 per instruction
-  constexpr int kOps[2] = {G == 1 ? 6 : 7, kA1 + 2};  // memory operations of a part
-  constexpr int kCalls[2] = {6, kA1 + 1};             // calls of fetch() for it
+  constexpr int kOps[2] = {G == 1 ? 6 : 5, kA1 + 4};  // memory operations of a part
+  // Part 1 of block s, which is sent in the first phase of block s - 1, also brings a quarter of the
+  // scales of the quad after block s - 1's: q = 0, 1 a's, 2, 3 b's, 8 rows a wave each. All of
+  // a quad have landed when its first block has; it takes the place of the quad before block s - 1's, whose last
+  // reads are over.
+  auto fetch_scales = [&](int s, int q) {
+    const int quad = ((s - 1) >> 2) + 1, r0 = 64 * ((s - 1) & 3), i = q & 1, r8 = 8 * i + (lane >> 3);
+    const uint32_t to = base + 2 * kBigStage + (quad & 1) * kBigQuad + (r0 + 16 * w4 + 8 * i) * kQuadRow;
+    if (q < 2) dma4s(sca, quad_off(min(r0 + 16 * w4 + r8, last_a), quad, i, lane, sld), to);
+    else dma4s(scb, quad_off(min(r0 + b_row<kPair>(w4, r8), last_b), quad, i, lane, sld), to + kB * kQuadRow);
+  };
   auto fetch = [&](int s, int part, int q) {
     const uint32_t st = base + (s & 1) * kBigStage;
-    const uint32_t sc = base + 2 * kBigStage + (s & 1) * kBigScales + w4 * 512;
-    const int64_t k = (int64_t)s * kRow, ks = (int64_t)s * 8;
+    const int64_t k = (int64_t)s * kRow;
     if (G == 1) {
       if (q < 3) dma16s(pb + k, off[q], st + kBigOp + (20 + 3 * w4 + q) * 1024);
       else dma16s(pa + k, off[q], st + (3 * w4 + q - 3) * 1024);
     } else if (part == 0) {
-      if (q < 5) dma16s(pb + k, off[q], st + kBigOp + (5 * w4 + q) * 1024);
-      else dma_scales(scb + ks, sob, sc + kB * 8);
+      dma16s(pb + k, off[q], st + kBigOp + (5 * w4 + q) * 1024);
     } else {
       if (q < kA1) dma16s(pa + k, off[5 + q], st + (12 + kA1 * w4 + q) * 1024);
-      else dma_scales(sca + ks, soa, sc);
+      else fetch_scales(s, q - kA1);
     }
   };
   auto fetch_all = [&](int s, int part) {
 #pragma unroll
-    for (int q = 0; q < kCalls[part]; ++q) fetch(s, part, q);
+    for (int q = 0; q < kOps[part]; ++q) fetch(s, part, q);
   };
   auto load_a = [&](int s, int half, auto dma, int t) {
     const char* p = lds + (s & 1) * kBigStage + (2 * G + half) * 16 * FA * kRow;
@@ -237,7 +264,7 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
       ba[f] = bytes(s, (2 * G + half) * 16 * FA + 16 * f);
       if constexpr (decltype(dma)::value)
 #pragma unroll
-        for (int q = kCalls[0] * f / FA; q < kCalls[0] * (f + 1) / FA; ++q) fetch(t, 0, q);
+        for (int q = kOps[0] * f / FA; q < kOps[0] * (f + 1) / FA; ++q) fetch(t, 0, q);
     }
   };
   auto load_b = [&](int s, auto dma, int t) {
@@ -248,7 +275,7 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
       bb[f] = bytes(s, kB + 64 * w4 + 16 * f);
       if constexpr (decltype(dma)::value)
 #pragma unroll
-        for (int q = kCalls[1] * f / 4; q < kCalls[1] * (f + 1) / 4; ++q) fetch(t, 1, q);
+        for (int q = kOps[1] * f / 4; q < kOps[1] * (f + 1) / 4; ++q) fetch(t, 1, q);
     }
   };
   auto mul = [&](int half) {
@@ -272,6 +299,9 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
         c = mma(fb[q].hi, fa[f].hi, c, sb[q].hi, sa[f].hi);
       }
   };
+  if (G == 0)  // the first quad: what blocks -3, -2, -1 and 0 would bring
+#pragma unroll
+    for (int q = 0; q < 12; ++q) fetch_scales(q / 4 - 3, q & 3);
   fetch_all(0, 0);
   if (G == 0) fetch_all(0, 1);
   if (nk > 1) {
@@ -306,7 +336,7 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
 template <typename T, int FA>
 __global__ __launch_bounds__(512, 2) void k_matmul4_big(MatArgs a) {
   constexpr bool kPair = sizeof(T) == 2;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kBigStage + 2 * kBigScales];
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kBigStage + 2 * kBigQuad];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int ti, tj;
@@ -339,15 +369,13 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_big(MatArgs a) {
     for (int q = 0; q < 5; ++q) off[q] = off_b(5 * w4 + q);
 #pragma unroll
     for (int q = 0; q < 2 * FA - 3; ++q) off[5 + q] = off_a(12 + (2 * FA - 3) * w4 + q);
-    const uint32_t soa = (uint32_t)(min(ra + 64 * w4 + lane, a.m - 1) - ra) * (uint32_t)a.a.sld;
-    const uint32_t sob =
-        (uint32_t)(min(rb + 64 * w4 + b_row<kPair>(lane >> 4, lane & 15), a.n - 1) - rb) * (uint32_t)a.b.sld;
+    const int last_a = (int)min(a.m - 1 - ra, (int64_t)kB), last_b = (int)min(a.n - 1 - rb, (int64_t)kB);
     big_loop<T, FA, 0>(lds, base, pa, pb, scalar(a.a.scales + ra * a.a.sld), scalar(a.b.scales + rb * a.b.sld), off,
-                       soa, sob, nk, wave, lane, acc);
+                       last_a, last_b, (int)a.a.sld, nk, wave, lane, acc);
   } else {
 #pragma unroll
     for (int q = 0; q < 6; ++q) off[q] = q < 3 ? off_b(20 + 3 * w4 + q) : off_a(3 * w4 + q - 3);
-    big_loop<T, FA, 1>(lds, base, pa, pb, nullptr, nullptr, off, 0, 0, nk, wave, lane, acc);
+    big_loop<T, FA, 1>(lds, base, pa, pb, nullptr, nullptr, off, 0, 0, 0, nk, wave, lane, acc);
   }
   store_wave<T, 2 * FA>(a, ra + 32 * FA * (wave >> 2), rb + 64 * w4, lane, acc);
 }
@@ -400,7 +428,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_matmul4_direct(MatArgs a) {
 
 // ---- 64 x 64 tiles: an LDS stage per wave, the waves share out the blocks ----
 constexpr int kSmallOp = kS * kRow;                      // 8 KB
-constexpr int kSmallStage = 2 * kSmallOp + 2 * kS * 8;   // both operands, then their scales
+constexpr int kSmallStage = 2 * kSmallOp + 2 * kS * kQuadRow;  // both operands, then a quad's scales
 
 template <typename T>
 __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
@@ -423,17 +451,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
     off[q] = (uint32_t)(q < 8 ? row_a(lr) : row_b(lr)) * (uint32_t)(q < 8 ? a.a.ld : a.b.ld) +
              (uint32_t)(((lane & 7) ^ (lr & 7)) << 4);
   }
-  const uint32_t soa = (uint32_t)row_a(lane) * (uint32_t)a.a.sld, sob = (uint32_t)row_b(lane) * (uint32_t)a.b.sld;
+  const int sld = (int)a.a.sld;
   const uint8_t *pa = a.a.codes + i0 * a.a.ld, *pb = a.b.codes + j0 * a.b.ld;
   const uint8_t *sa = a.a.scales + i0 * a.a.sld, *sb = a.b.scales + j0 * a.b.sld;
   char* st = lds + wave * kSmallStage;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds + wave * kSmallStage;
-  auto fetch = [&](int kb) {
+  auto fetch = [&](int kb, bool first) {
     const int64_t k = (int64_t)kb * kRow;
 #pragma unroll
     for (int q = 0; q < 16; ++q) dma16s((q < 8 ? pa : pb) + k, off[q], base + q * 1024);
-    dma_scales(sa + (int64_t)kb * 8, soa, base + 2 * kSmallOp);
-    dma_scales(sb + (int64_t)kb * 8, sob, base + 2 * kSmallOp + kS * 8);
+    if (first || (kb & 3) == 0) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int r = 8 * (q & 7) + (lane >> 3);
+        dma4s(q < 8 ? sa : sb, quad_off((int)(q < 8 ? row_a(r) : row_b(r)), kb >> 2, q, lane, sld),
+              base + 2 * kSmallOp + q * 8 * kQuadRow);
+      }
+    }
   };
   const int foff = r16 * kRow + ((g ^ (r16 & 7)) << 4);
   f32x4 acc[4][4];
@@ -445,7 +479,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
   const int order = 2 * (wave & 3) + (wave >> 2), nk = max(kb1 - kb0, 0);
   int kb = kb0 + (int)((int64_t)order * nk >> 3);
   const int end = kb0 + (int)((int64_t)(order + 1) * nk >> 3);
-  if (kb < end) fetch(kb);
+  if (kb < end) fetch(kb, true);
   for (; kb < end; ++kb) {
     // this wave's block has landed; the empty asm keeps the reads below the wait
     __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xF << 8));  // vmcnt(0)
@@ -460,15 +494,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(st + 16 * f * kRow);
       fb[f] = frag(st + kSmallOp + 16 * f * kRow);
-      ba[f] = row_scales(ss, 16 * f, r16);
-      bb[f] = row_scales(ss, kS + 16 * f, r16);
+      ba[f] = row_scales(ss, 16 * f, r16, kb);
+      bb[f] = row_scales(ss, kS + 16 * f, r16, kb);
     }
     if (kb + 1 < end) {
       // the reads have retired before the stage is refilled
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4) | (0 << 8));  // lgkmcnt(0)
       asm volatile("" ::: "memory");
-      fetch(kb + 1);
+      fetch(kb + 1, false);
     }
     Scales ea[4], eb[4];
 #pragma unroll
