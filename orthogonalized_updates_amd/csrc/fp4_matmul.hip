@@ -60,7 +60,7 @@ __device__ __forceinline__ Scales scales_of(u32x2 b, int shift) { return Scales{
 // lane brings 8 rows' scales of a quad, 4 blocks: 32 bytes per row, a quarter of a tile's rows
 // with each block. Of LDS row r, block b of the quad lies at 8 (b ^ (r / 8 & 1)), so that the 16 rows
 // of a fragment fall on different banks. Past the row's end the last 4 bytes come again (products of 8192 x 8192 x
-// 8192: 300 us with two DMAs per block, 4 bytes of 64 rows each; QUADS).
+// 8192: 300 us with two DMAs per block, 4 bytes of 64 rows each, 273 so).
 constexpr int kQuadRow = 32;
 // The lane's offset for LDS rows 8 i .. + 7 (i: the parity), lane l: row l / 8, dword l % 8; row: the matrix row
 // from the base, quad: which 4 blocks.

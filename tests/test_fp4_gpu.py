@@ -197,6 +197,8 @@ SIZES = [(1, 1, 1), (1, 6144, 2048), (2, 17, 129), (16, 512, 2048), (17, 130, 10
          (65, 15, 64), (128, 128, 128), (129, 257, 769), (300, 1, 1300), (777, 1003, 501), (1024, 512, 256),
          (200, 300, 16384), (513, 2050, 640), (2100, 1100, 192), (2900, 2900, 100), (2817, 3000, 1301),
          (4096, 2048, 768), (1536, 5400, 2560), (6144, 2048, 4096), (1024, 4096, 8192)]
+# each of the large tiles with 1 to 5 blocks of k, and more
+SIZES += [(m, n, k) for m, n in ((1100, 1300), (2817, 3000), (3900, 4000)) for k in (200, 300, 768, 900, 1200, 1501)]
 
 
 def reference(va, vb):
@@ -235,7 +237,7 @@ def test_product(m, n, k, dtype):
     assert ((got.double() - want).abs() <= tol + U * old64.abs() * 2 + HALF[dtype] * want.abs()).all()
 
 
-@pytest.mark.parametrize("m,n,k", [(40, 60, 1024), (300, 520, 2048), (1100, 1300, 512)])
+@pytest.mark.parametrize("m,n,k", [(1, 60, 1024), (300, 520, 2048), (200, 300, 16384), (1100, 1300, 512), (2817, 3000, 512), (3900, 4000, 768)])
 def test_small_sums_survive_large_products_that_cancel(m, n, k):
     """Group 0 of every row times 2^12 and group 5 its negative: what is left is the rest, exact in quarters."""
     rng = np.random.default_rng(5)
@@ -251,7 +253,7 @@ def test_small_sums_survive_large_products_that_cancel(m, n, k):
     assert ((out.double() - want).abs() <= 1.0).all()
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 40, 300), (70, 90, 600), (300, 300, 2000), (2900, 2900, 100)])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 300), (70, 90, 600), (500, 520, 2000), (200, 300, 16384), (1100, 1300, 300), (2900, 2900, 100), (3900, 4000, 600)])
 def test_nan_groups_stay_in_their_rows(m, n, k):
     a, va = random_matrix(m, k, 1)
     b, vb = random_matrix(n, k, 2)
@@ -279,7 +281,8 @@ def test_ends_of_the_range():
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-@pytest.mark.parametrize("m,n,k,ld,first", [(70, 50, 300, 51, 1), (300, 257, 600, 260, 3), (520, 1030, 512, 1031, 0), (1100, 1300, 512, 1301, 5)])
+@pytest.mark.parametrize("m,n,k,ld,first", [(7, 50, 300, 51, 1), (300, 257, 600, 260, 3), (520, 1030, 512, 1031, 0), (200, 301, 16384, 303, 1), (1100, 1300, 512, 1301, 5),
+                                               (2817, 3000, 300, 3007, 1), (3900, 4000, 300, 4003, 3)])
 def test_output_rows_inside_wider_ones(m, n, k, ld, first, dtype):
     a, va = random_matrix(m, k, 1)
     b, vb = random_matrix(n, k, 2)
