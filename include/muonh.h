@@ -456,6 +456,7 @@ int muonh_fp8_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void*
  *   codes and scales and/or codes_t and scales_t: y and/or its transpose as
  *   MUONH_FP8_ROWS matrices (muonh_fp8_quantize's forms of the unrounded y): what
  *   muonh_fp8_matmul reads for the forward product and the weight gradient.
+ * Matrices of one pitch may lie between each other's rows, as columns of a wider one.
  * Rows do not depend on each other; results are deterministic for a size and set of
  * outputs. Asynchronous on `stream`, capturable.
  * Errors: MUONH_EINVAL (NULL or misaligned argument, bad dtype, pitch or eps, half-given

@@ -775,11 +775,16 @@ def _on_device(torch, dev, fn, *args) -> None:
             check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
 
 
+@functools.lru_cache(maxsize=None)
+def _increment_version():
+    from torch.autograd.graph import increment_version
+    return increment_version
+
+
 def _written(*tensors) -> None:
     """Tells autograd that the library wrote into the tensors, so that a
     backward pass that saved one of them before refuses to use it."""
-    from torch.autograd.graph import increment_version
-    increment_version(tensors)
+    _increment_version()(tensors)
 
 
 def fp8_quantize(x, block: str = "rows", forms: str = "plain",
@@ -1039,8 +1044,11 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=None, accumulate:
     if not given:
         if accumulate:
             raise ValueError("accumulate=True needs out")
-        out = torch.empty(shape, device=dev, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
-    dt, ld = _rows("out", out, dev, shape, out_dtype)
+        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        dt, ld = _fp8_dt(torch, out_dtype), max(n, 1)
+        out = torch.empty(shape, device=dev, dtype=out_dtype)
+    else:
+        dt, ld = _rows("out", out, dev, shape, out_dtype)
     lib = get_lib()
     nbytes = lib.muonh_fp4_matmul_workspace_bytes(m, n, a.shape[1])
     # from torch's allocator on the current stream, as fp8_matmul's
@@ -1053,20 +1061,37 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=None, accumulate:
 
 
 # -- RMS norm ------------------------------------------------------------------
+@functools.lru_cache(maxsize=None)
+def _dt_codes():
+    import torch
+    return {torch.float32: MUONH_DT_FP32, torch.bfloat16: MUONH_DT_BF16}
+
+
 def _rows(name: str, t, dev, shape=None, dtype=None):
     """(dtype code, row pitch) of a 2-d fp32 or bf16 tensor whose rows are
     contiguous."""
+    try:
+        dt, (rows, cols), (ld, step) = _dt_codes()[t.dtype], t.shape, t.stride()
+    except (AttributeError, KeyError, TypeError, ValueError):
+        _refuse_rows(name, t)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name} must be a 2-d tensor on {dev if dev.type == 'cuda' else 'a ROCm GPU'}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if step == 1 and ld >= cols and rows > 1:
+        return dt, ld
+    return dt, _row_pitch(t, name)
+
+
+def _refuse_rows(name: str, t) -> None:
+    """Says why t is no 2-d fp32 or bf16 tensor."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    dt = _fp8_dt(torch, t.dtype)
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.device != dev or dev.type != "cuda":
-        raise ValueError(f"{name} must be a 2-d tensor on {dev if dev.type == 'cuda' else 'a ROCm GPU'}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return dt, _row_pitch(t, name)
+    _fp8_dt(torch, t.dtype)
+    raise ValueError(f"{name} must be a 2-d tensor")
 
 
 def _floats(name: str, t, dev, n: int) -> None:
@@ -1113,10 +1138,13 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, out_dtype=No
     import torch
     dt, ld, hdt, rld, h, hld, rstd = _norm_inputs(x, weight, residual, residual_out)
     dev, shape = x.device, tuple(x.shape)
-    y = out
-    if y is None:
+    if out is None:
+        ydt = hdt if out_dtype is None else _fp8_dt(torch, out_dtype)
         y = torch.empty(shape, dtype=(x if h is None else h).dtype if out_dtype is None else out_dtype, device=dev)
-    ydt, yld = _rows("out", y, dev, shape, out_dtype)
+        yld = shape[1]
+    else:
+        y = out
+        ydt, yld = _rows("out", y, dev, shape, out_dtype)
     _on_device(torch, dev, get_lib().muonh_rms_norm, x.data_ptr(), dt, shape[0], shape[1], ld,
                None if h is None else residual.data_ptr(), hdt, rld, None if h is None else h.data_ptr(), hld,
                weight.data_ptr(), float(eps), rstd.data_ptr(), y.data_ptr(), ydt, yld, None, None, None, None)
@@ -1171,8 +1199,11 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual=None, out=None, dweight=Non
     rld = 0
     if dresidual is not None:
         _, rld = _rows("dresidual", dresidual, dev, shape, h.dtype)
-    dh = torch.empty(shape, dtype=h.dtype, device=dev) if out is None else out
-    _, old = _rows("out", dh, dev, shape, h.dtype)
+    if out is None:
+        dh, old = torch.empty(shape, dtype=h.dtype, device=dev), max(cols, 1)
+    else:
+        dh = out
+        _, old = _rows("out", dh, dev, shape, h.dtype)
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate=True needs dweight")
@@ -1209,8 +1240,10 @@ def _by_token(name: str, t, ids, cols: int):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if tuple(t.shape) != (*ids.shape, cols):
+    if t.shape != (*ids.shape, cols):
         raise ValueError(f"{name} must have shape {(*ids.shape, cols)}, got {tuple(t.shape)}")
+    if t.dim() == 2:
+        return t
     try:
         return t.view(ids.numel(), cols)
     except RuntimeError:
@@ -1232,11 +1265,13 @@ def embedding(ids, table, scale: float = 1.0, out=None, out_dtype=None, first: i
     dev = table.device
     nbytes = _ids(ids, dev)
     rows, cols = table.shape
-    y = out
-    if y is None:
-        y = torch.empty((*ids.shape, cols), dtype=table.dtype if out_dtype is None else out_dtype, device=dev)
-    flat = _by_token("out", y, ids, cols)
-    odt, old = _rows("out", flat, dev, None, out_dtype)
+    if out is None:
+        odt = dt if out_dtype is None else _fp8_dt(torch, out_dtype)
+        y = flat = torch.empty((*ids.shape, cols), dtype=table.dtype if out_dtype is None else out_dtype, device=dev)
+        old = max(cols, 1)
+    else:
+        y, flat = out, _by_token("out", out, ids, cols)
+        odt, old = _rows("out", flat, dev, None, out_dtype)
     _on_device(torch, dev, get_lib().muonh_embedding, ids.data_ptr(), nbytes, ids.numel(), int(first), table.data_ptr(),
                dt, rows, cols, ld, float(scale), flat.data_ptr(), odt, old)
     if out is not None:

@@ -77,6 +77,27 @@ __device__ __forceinline__ void put_scales(uint8_t* s, int64_t row, int64_t cols
     for (uint32_t j = tiles_c; j < ld / 4; ++j) p[j] = 0;
 }
 
+// Lane t of a quad holds dword t of rows 0 .. 3, in q[0] .. q[3]: afterwards all 4 of row t, by two
+// exchanges of halves.
+template <int CTRL>
+__device__ __forceinline__ uint32_t from(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint4 quad_rows(const uint32_t* q, int t) {
+  const bool odd = t & 1, high = t & 2;
+  uint32_t u[2][2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const uint32_t got = from<0xB1>(odd ? q[2 * p] : q[2 * p + 1]);  // quad [1,0,3,2]
+    u[p][0] = odd ? got : q[2 * p];
+    u[p][1] = odd ? q[2 * p + 1] : got;
+  }
+  uint32_t got[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) got[e] = from<0x4E>(high ? u[0][e] : u[1][e]);  // quad [2,3,0,1]
+  return high ? make_uint4(got[0], got[1], u[1][0], u[1][1]) : make_uint4(u[0][0], u[0][1], got[0], got[1]);
+}
+
 // Thread (ty, tx) = (tid / 16, tid % 16) holds rows 8 ty .. +7, columns
 // 8 tx .. +7 of the tile. PLAIN, TRANS: the forms written. Tiles are dealt to
 // the XCDs as in the 8-bit kernel.
@@ -133,6 +154,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
 
   if constexpr (PLAIN) {
     const int64_t ld = code_ld(cols);
+    uint32_t rows8[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       // the 4 lanes of a group
@@ -141,12 +163,18 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
       for (int h = 0; h < 2; ++h) {
         const int i = 2 * k + h;
         const uint32_t byte = h ? b >> 16 : b & 0xffu;
-        uint32_t q;
-        if constexpr (BF) q = codes8(w[i][0], w[i][1], w[i][2], w[i][3], byte);
-        else q = codes8(v[i], byte);
-        if (r0 + i < rows) *reinterpret_cast<uint32_t*>(a.codes + (r0 + i) * ld + c0 / 2) = q;
+        if constexpr (BF) rows8[i] = codes8(w[i][0], w[i][1], w[i][2], w[i][3], byte);
+        else rows8[i] = codes8(v[i], byte);
         if ((tx & 3) == 0) reinterpret_cast<uint8_t*>(&bytes_of[0][8 * ty + i])[tx >> 2] = (uint8_t)byte;
       }
+    }
+    // 16 bytes a lane, a quad's group of a row each (8192 x 2048 bf16 in both forms 13.4 -> 12.5
+    // us against 4-byte stores)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 q = quad_rows(rows8 + 4 * h, tx & 3);
+      const int64_t r = r0 + 4 * h + (tx & 3);
+      if (r < rows) *reinterpret_cast<uint4*>(a.codes + r * ld + (int64_t)tc * (kTile / 2) + (tx >> 2) * 16) = q;
     }
   }
 

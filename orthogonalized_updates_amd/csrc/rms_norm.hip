@@ -566,24 +566,29 @@ int muonh_rms_norm(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, i
   if (off(codes, 16) || off(codes_t, 16) || off(scales, 4) || off(scales_t, 4))
     return fail(MUONH_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
   if (codes_t && !fp8::tiles_fit(rows, cols)) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more");
-  const Span read[3] = {span_of(in, rows, cols), span_of(res, rows, cols), span("weight", weight, cols * 4)};
-  const Span written[7] = {span_of(sum, rows, cols),
-                           span_of(out, rows, cols),
-                           span("rstd", rstd, rows * 4),
-                           span("codes", codes, rows * code_ld(cols)),
-                           span("scales", scales, rows * fp8::scale_ld(cols)),
-                           span("codes_t", codes_t, cols * code_ld(rows)),
-                           span("scales_t", scales_t, cols * fp8::scale_ld(rows))};
-  for (int i = 0; i < 7; ++i) {
-    for (int j = 0; j < 3; ++j) {
-      // h may take the place of x or of the residual, entry by entry
-      if (i == 0 && ((j == 0 && same(sum, in)) || (j == 1 && same(sum, res)))) continue;
-      if (overlap(written[i], read[j])) return fail(MUONH_EALIAS, "%s overlaps %s", written[i].name, read[j].name);
+  // h may take the place of x or of the residual, entry by entry
+  const Mat* const mats[4] = {&in, &res, &sum, &out};
+  for (int i = 2; i < 4; ++i)
+    for (int j = 0; j < i; ++j) {
+      if (!mats[i]->p || !mats[j]->p || (i == 2 && same(*mats[i], *mats[j]))) continue;
+      if (meet(*mats[i], *mats[j], rows, cols)) return fail(MUONH_EALIAS, "%s overlaps %s", mats[i]->name, mats[j]->name);
     }
-    for (int j = i + 1; j < 7; ++j)
-      if (overlap(written[i], written[j]))
-        return fail(MUONH_EALIAS, "%s overlaps %s", written[j].name, written[i].name);
-  }
+  const Span spans[10] = {span_of(in, rows, cols),
+                          span_of(res, rows, cols),
+                          span("weight", weight, cols * 4),
+                          span_of(sum, rows, cols),
+                          span_of(out, rows, cols),
+                          span("rstd", rstd, rows * 4),
+                          span("codes", codes, rows * code_ld(cols)),
+                          span("scales", scales, rows * fp8::scale_ld(cols)),
+                          span("codes_t", codes_t, cols * code_ld(rows)),
+                          span("scales_t", scales_t, cols * fp8::scale_ld(rows))};
+  for (int i = 3; i < 10; ++i)
+    for (int j = 0; j < i; ++j) {
+      const bool both_mats = i < 5 && j != 2;  // done above
+      if (!both_mats && overlap(spans[i], spans[j]))
+        return fail(MUONH_EALIAS, "%s overlaps %s", spans[i].name, spans[j].name);
+    }
 
   FwdArgs a{};
   a.x = x;
@@ -661,20 +666,19 @@ int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, con
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MUONH_EWORKSPACE, "workspace must be 256-byte aligned");
   if (workspace_bytes < need)
     return fail(MUONH_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
-  const Span read[5] = {span_of(d, rows, cols), span_of(x, rows, cols), span_of(res, rows, cols),
-                        span("weight", weight, cols * 4), span("rstd", rstd, rows * 4)};
-  const Span written[3] = {span_of(out, rows, cols), span("dweight", dweight, cols * 4),
-                           span("workspace", workspace, (int64_t)need)};
-  for (int i = 0; i < 3; ++i) {
-    for (int j = 0; j < 5; ++j) {
-      // dh may take the place of dy or of dresidual, entry by entry
-      if (i == 0 && ((j == 0 && same(out, d)) || (j == 2 && same(out, res)))) continue;
-      if (overlap(written[i], read[j])) return fail(MUONH_EALIAS, "%s overlaps %s", written[i].name, read[j].name);
-    }
-    for (int j = i + 1; j < 3; ++j)
-      if (overlap(written[i], written[j]))
-        return fail(MUONH_EALIAS, "%s overlaps %s", written[j].name, written[i].name);
+  // dh may take the place of dy or of dresidual, entry by entry
+  const Mat* const mats[3] = {&d, &x, &res};
+  for (int j = 0; j < 3; ++j) {
+    if (!mats[j]->p || (j != 1 && same(out, *mats[j]))) continue;
+    if (meet(out, *mats[j], rows, cols)) return fail(MUONH_EALIAS, "dh overlaps %s", mats[j]->name);
   }
+  const Span spans[8] = {span_of(d, rows, cols),          span_of(x, rows, cols),
+                         span_of(res, rows, cols),        span("weight", weight, cols * 4),
+                         span("rstd", rstd, rows * 4),    span_of(out, rows, cols),
+                         span("dweight", dweight, cols * 4), span("workspace", workspace, (int64_t)need)};
+  for (int i = 5; i < 8; ++i)
+    for (int j = i == 5 ? 3 : 0; j < i; ++j)
+      if (overlap(spans[i], spans[j])) return fail(MUONH_EALIAS, "%s overlaps %s", spans[i].name, spans[j].name);
 
   BwdArgs a{};
   a.dy = dy;

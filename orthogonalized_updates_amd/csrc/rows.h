@@ -96,6 +96,16 @@ inline int check_mat(const Mat& m, int64_t cols) {
 inline Span span_of(const Mat& m, int64_t rows, int64_t cols) {
   return span(m.name, m.p, m.p ? ((rows - 1) * m.ld + cols) * size_of(m.dtype) : 0);
 }
+// Whether two matrices of `rows` x `cols` entries have memory in common. Rows of one pitch may lie
+// between each other's, as columns of a wider matrix.
+inline bool meet(const Mat& a, const Mat& b, int64_t rows, int64_t cols) {
+  if (!fp8::overlap(span_of(a, rows, cols), span_of(b, rows, cols))) return false;
+  const int64_t pitch = a.ld * size_of(a.dtype);
+  if (rows < 2 || pitch != b.ld * size_of(b.dtype)) return true;
+  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % pitch;
+  const int64_t d = apart < 0 ? apart + pitch : apart;  // b's first column after a's
+  return d < cols * size_of(a.dtype) || d + cols * size_of(b.dtype) > pitch;
+}
 inline bool same(const Mat& a, const Mat& b) { return a.p == b.p && a.ld == b.ld && a.dtype == b.dtype; }
 
 inline int launched(const char* what) {

@@ -314,6 +314,25 @@ def test_codes_past_32_bits():
     assert torch.equal(m.fp4_matmul(big, a, out_dtype=torch.float32), out.t())
 
 
+def test_quantization_past_32_bits():
+    """The last rows and columns of a source of more than 2^32 bytes, codes past 2^31."""
+    rows, k = 70000, 66000
+    x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = values(3, k, 1, "bf16")
+    x[:, -2:] = values(rows, 2, 2, "bf16")
+    q, qt = mh().fp4_quantize(x, forms="both")
+    last = x[-3:].double().cpu().numpy()
+    codes, scales = fo.quantize(last)
+    assert np.array_equal(fo.unpack(q.codes.view(torch.uint8)[-3:].cpu().numpy()), codes)
+    assert np.array_equal(q.scales.view(torch.uint8)[-3:].cpu().numpy(), scales)
+    codes, scales = fo.quantize(x[:, -2:].double().cpu().numpy().T)
+    assert np.array_equal(fo.unpack(qt.codes.view(torch.uint8)[-2:].cpu().numpy()), codes)
+    assert np.array_equal(qt.scales.view(torch.uint8)[-2:].cpu().numpy(), scales)
+    v = q.dequantize(torch.bfloat16)
+    assert np.array_equal(v[-3:].double().cpu().numpy(), fo.values(*(t.view(torch.uint8)[-3:].cpu().numpy() for t in (q.codes, q.scales)), (3, k)))
+    assert not v[:-3, :-32].any()
+
+
 def test_python_refuses():
     m = mh()
     a, b = m.Fp4Matrix.empty(3, 100), m.Fp4Matrix.empty(4, 100)

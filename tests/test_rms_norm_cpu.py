@@ -68,6 +68,18 @@ def test_forward_refuses(kw, code):
     assert mh.lib.muonh_last_error()
 
 
+@pytest.mark.parametrize("apart,meets", [(800, False), (4000, False), (8800, False), (796, True), (4, True), (9600, True), (8804, True),
+                                         (-800, False), (-796, True), (-8800, False), (-9600, True)])
+def test_rows_may_lie_between_each_other(apart, meets):
+    """dh's 200 floats per row in the same rows of 2400 floats as dy's, `apart` bytes on."""
+    f = mh.lib.muonh_rms_norm_backward
+    dh = A + (1 << 20) + apart
+    got = f(A + (1 << 20), 0, 2400, 9 * A, 0, 100, 200, 200, 3 * A, 4 * A, None, 0, dh, 2400, 7 * A if meets else 4 * A + 4, 0, 8 * A, 1 << 40, None)
+    # the accepted ones go on to the next check, which refuses dweight for overlapping rstd
+    assert got == mh.MUONH_EALIAS
+    assert (b"dh overlaps dy" in mh.lib.muonh_last_error()) == meets
+
+
 def test_forward_of_no_rows_is_a_no_op():
     assert _forward(rows=0, x=None, res=None, h=None, y=None, w=None, rstd=None) == mh.MUONH_OK
 

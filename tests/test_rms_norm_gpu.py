@@ -223,6 +223,23 @@ def test_strides_and_untouched_neighbours(cols, ld, first, dtype):
         assert (base[keep] == 7.0).all()
 
 
+def test_columns_of_one_wide_buffer():
+    """Inputs and outputs side by side in the same rows."""
+    rows, cols = 70, 256
+    buf = values(rows, 5 * cols, 1, "bf16")
+    x, res, h, y, dh = (buf[:, i * cols:(i + 1) * cols] for i in range(5))
+    w = weights(cols)
+    want = mh().rms_norm(x.contiguous(), w, residual=res.contiguous())
+    got = mh().rms_norm(x, w, residual=res, residual_out=h, out=y)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    back = mh().rms_norm_backward(y, h, w, got[2], dresidual=res, out=dh)
+    again = mh().rms_norm_backward(want[0], want[1], w, want[2], dresidual=res.contiguous())
+    assert torch.equal(dh, again[0]) and torch.equal(back[1], again[1])
+    with pytest.raises(mh().MuonHError) as e:
+        mh().rms_norm(x, w, residual=res, residual_out=buf[:, cols - 1:2 * cols - 1])
+    assert e.value.status == mh().MUONH_EALIAS
+
+
 @pytest.mark.parametrize("rows,cols", [(5, 2048), (300, 128), (400, 1001), (3, 40000)])
 def test_in_place(rows, cols):
     x, res, w = values(rows, cols, 1, "bf16"), values(rows, cols, 2, "bf16"), weights(cols)
