@@ -106,7 +106,8 @@ __global__ __launch_bounds__(256) void k_lookup(LookArgs a) {
 }
 
 // ---- the gradient of few tokens ------------------------------------------------------
-// Up to kFewMax tokens, in one launch: a workgroup to each token and 512 columns,
+// Up to kFewMax tokens, in one launch (777 tokens into 5003 x 1001 from zero: 9 us, of which the
+// clearing is 5; sorted, summed and joined in three launches 28): a workgroup to each token and 512 columns,
 // which does nothing unless its token is the first of its row, and else sums the row's tokens in their order:
 // up to 8 of them by one wave, more by 4, a quarter each, joined in order. Where G starts
 // at zero, the first `clearing` workgroups clear the rows that do not occur.
@@ -264,7 +265,7 @@ struct Sorted {
 // workgroup counts for token x of its kTok the tokens of slice y of all; waves read
 // the slice's rows from LDS as broadcasts. The workgroups past the first `sorting` fill G with zeros.
 //
-// (To be measured against the passes below.)
+// 4096, 8192, 16384 tokens of 151936 rows: 6.8, 10.4, 27.8 us; the passes below take 52, 62, 64, launches apart.
 constexpr int kCountMax = 16384, kTok = 32, kSlices = 1024 / kTok;
 __global__ __launch_bounds__(1024) void k_count(Ids ids, int n, Sorted out, int sorting, FillArgs f) {
   // n rounded up to 4 kSlices, then the counts
@@ -419,7 +420,8 @@ __global__ __launch_bounds__(256) void k_move(PassArgs a) {
 // tokens begin sums them to the end of the next chunk and, if that is all of them,
 // stores the row; what lies in later chunks is summed there (`head`) and joined to
 // the first sum (`tail`) by k_join. So most rows are stored at once, and a frequent token's
-// sum is shared out.
+// sum is shared out. 8192 tokens added to 151936 x 2048 from bf16: 21.7 us for about 86 MB (chunks of 4 and
+// 16: 21.4 and 22.5), k_join 5.3 (7.2 and 4.7).
 struct SumArgs {
   Sorted s;
   const void* dy;

@@ -115,7 +115,8 @@ def test_backward_workspace():
     assert f(100, 200) == 25 * 200 * 4              # 4 rows at a time
     assert f(1, 2048) == 2048 * 4
     assert f(1 << 20, 2048) == 512 * 2048 * 4
-    assert f(10, 8193) == (10 * 8193 + 10) * 4      # and the rows' means
+    assert f(10, 16384) == 10 * 16384 * 4
+    assert f(10, 16385) == (10 * 16385 + 10) * 4    # and the rows' means
     assert f(5, 1 << 24) == (5 * (1 << 24) + 5) * 4
 
 

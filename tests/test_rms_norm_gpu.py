@@ -94,7 +94,7 @@ def add(x, res):
 
 
 SIZES = [(1, 1), (1, 2048), (3, 7), (2, 128), (17, 129), (300, 128), (5, 512), (257, 520), (64, 1000), (300, 1001), (300, 1536),
-         (129, 2048), (258, 2048), (7, 2056), (300, 4096), (33, 8192), (3, 8200), (5, 20000), (2, 32768), (3, 40001)]
+         (129, 2048), (258, 2048), (7, 2056), (300, 4096), (33, 8192), (3, 8200), (40, 16384), (5, 20000), (2, 32768), (3, 40001)]
 
 
 @pytest.mark.parametrize("types", [("bf16", None), ("fp32", None), ("bf16", "bf16"), ("fp32", "fp32"), ("bf16", "fp32"), ("fp32", "bf16")])
@@ -135,7 +135,7 @@ def test_norm_in_8_bits(rows, cols, types):
             assert torch.equal(q.scales.view(torch.uint8), first.scales.view(torch.uint8))
 
 
-def check_back(dh, dw, dy, h, w, r, res, groups=512):
+def check_back(dh, dw, dy, h, w, r, res):
     rows, cols = h.shape
     d64, h64, w64, r64 = f64(dy), f64(h), f64(w), f64(r)[:, None]
     want, wdw = no.backward(d64, h64, w64, f64(r), None if res is None else f64(res))
@@ -147,8 +147,8 @@ def check_back(dh, dw, dy, h, w, r, res, groups=512):
     err = np.abs(f64(dh) - want)
     assert (err <= tol + 1e-44).all(), (err / (tol + 1e-44)).max()
     per = 16 if cols <= 128 else 4 if cols <= 2048 else 1
-    blocks = min(rows, 64) if cols > 8192 else min(-(-rows // per), 512)
-    terms = 3 + math.ceil(rows / (blocks * (per if cols <= 8192 else 1))) + 16 + blocks / 32 + 32
+    blocks = min(rows, 64) if cols > 16384 else min(-(-rows // per), 2048 if cols <= 128 else 1024 if 2048 < cols <= 8192 else 512)
+    terms = 3 + math.ceil(rows / (blocks * (per if cols <= 16384 else 1))) + 16 + blocks / 32 + 32
     assert (np.abs(f64(dw) - wdw) <= U * terms * np.sum(np.abs(d64) * n, axis=0) + 1e-44).all()
 
 
