@@ -68,12 +68,12 @@ __device__ __forceinline__ uint32_t quad_off(int row, int quad, int i, int lane,
   const int dw = (((lane & 7) >> 1) ^ (i & 1)) * 2 + (lane & 1);
   return (uint32_t)row * (uint32_t)sld + (uint32_t)min(quad * kQuadRow + dw * 4, sld - 4);
 }
-// The lane's two of row `first` + l%16's for block s, first a multiple of 16, as bytes: a shift after
-// wider reads would stand between a phase's barrier and its first matrix instruction.
-__device__ __forceinline__ Scales row_scales(const char* quad, int first, int lane, int s) {
+// Row `first` + l%16's 8 bytes of block s, first a multiple of 16. The lane's two of them (scales_of) are
+// shifted out where they were read, before the phase's barrier. (Reads of single bytes: lanes that want
+// different bytes of one word wait for each other, 2 cycles each.)
+__device__ __forceinline__ u32x2 row_scales(const char* quad, int first, int lane, int s) {
   const int r = lane & 15;
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(quad) + (first + r) * kQuadRow + (((s & 3) ^ (r >> 3)) << 3) + (lane >> 4);
-  return Scales{p[0], p[4]};
+  return *reinterpret_cast<const u32x2*>(quad + (first + r) * kQuadRow + (((s & 3) ^ (r >> 3)) << 3));
 }
 
 // ---- 128 x 128 tiles: two groups of 4 waves that take the blocks in turn, a ring of 4 stages ----
@@ -149,14 +149,20 @@ __global__ __launch_bounds__(512, 2) void k_matmul4_tile(MatArgs a) {
       return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
     };
     Frag fa[4], fb[4];
-    Scales sa[4], sb[4];
+    u32x2 ba[4], bb[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(st + (64 * wm + 16 * f) * kRow);
       fb[f] = frag(st + kOpStage + (64 * wn + 16 * f) * kRow);
-      sa[f] = row_scales(ss, 64 * wm + 16 * f, lane, s);
-      sb[f] = row_scales(ss, kT + 64 * wn + 16 * f, lane, s);
+      ba[f] = row_scales(ss, 64 * wm + 16 * f, lane, s);
+      bb[f] = row_scales(ss, kT + 64 * wn + 16 * f, lane, s);
       if constexpr (kMore) fetch_part(s + 3, f);
+    }
+    Scales sa[4], sb[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      sa[f] = scales_of(ba[f], 8 * g);
+      sb[f] = scales_of(bb[f], 8 * g);
     }
     stage_barrier<(kMore ? kOps : 0)>();
     mma_block<4, 4>(fb, fa, sb, sa, acc);
@@ -217,6 +223,7 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
   const int w4 = wave & 3, r16 = lane & 15, g = lane >> 4;
   const int foff = r16 * kRow + ((g ^ (r16 & 7)) << 4);
   Frag fa[FA], fb[4];
+  u32x2 ba[FA], bb[4];
   Scales sa[FA], sb[4];
   auto frag = [&](const char* p) {
     return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
@@ -258,7 +265,7 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
 #pragma unroll
     for (int f = 0; f < FA; ++f) {
       fa[f] = frag(p + 16 * f * kRow);
-      sa[f] = bytes(s, (2 * G + half) * 16 * FA + 16 * f);
+      ba[f] = bytes(s, (2 * G + half) * 16 * FA + 16 * f);
       if constexpr (decltype(dma)::value)
 #pragma unroll
         for (int q = kOps[0] * f / FA; q < kOps[0] * (f + 1) / FA; ++q) fetch(t, 0, q);
@@ -269,11 +276,19 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       fb[f] = frag(p + 16 * f * kRow);
-      sb[f] = bytes(s, kB + 64 * w4 + 16 * f);
+      bb[f] = bytes(s, kB + 64 * w4 + 16 * f);
       if constexpr (decltype(dma)::value)
 #pragma unroll
         for (int q = kOps[1] * f / 4; q < kOps[1] * (f + 1) / 4; ++q) fetch(t, 1, q);
     }
+  };
+  auto shift_a = [&] {
+#pragma unroll
+    for (int f = 0; f < FA; ++f) sa[f] = scales_of(ba[f], 8 * g);
+  };
+  auto shift_b = [&] {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sb[q] = scales_of(bb[q], 8 * g);
   };
   auto mul = [&](int half) {
 #pragma unroll
@@ -309,10 +324,13 @@ __device__ __forceinline__ void big_loop(const char* lds, uint32_t base, const u
     constexpr std::false_type none{};
     load_b(s, std::bool_constant<G == 0 && kLeft >= 1>{}, s + 1);
     load_a(s, 0, none, 0);
+    shift_b();
+    shift_a();
     stage_barrier<63>();
     mul(0);
     stage_barrier<63>();
     load_a(s, 1, std::bool_constant<kLeft >= 2>{}, s + 2);
+    shift_a();
     constexpr int kLand = kLeft >= 2 ? kOps[0] : 0;
     stage_barrier<(G == 1 ? kLand : 63)>();
     mul(1);
@@ -477,7 +495,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
     __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xF << 8));  // vmcnt(0)
     asm volatile("" ::: "memory");
     Frag fa[4], fb[4];
-    Scales ea[4], eb[4];
+    u32x2 ba[4], bb[4];
     auto frag = [&](const char* p) {
       return Frag{*reinterpret_cast<const i32x4*>(p + foff), *reinterpret_cast<const i32x4*>(p + (foff ^ 64))};
     };
@@ -486,8 +504,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
     for (int f = 0; f < 4; ++f) {
       fa[f] = frag(st + 16 * f * kRow);
       fb[f] = frag(st + kSmallOp + 16 * f * kRow);
-      ea[f] = row_scales(ss, 16 * f, lane, kb);
-      eb[f] = row_scales(ss, kS + 16 * f, lane, kb);
+      ba[f] = row_scales(ss, 16 * f, lane, kb);
+      bb[f] = row_scales(ss, kS + 16 * f, lane, kb);
     }
     if (kb + 1 < end) {
       // the reads have retired before the stage is refilled
@@ -495,6 +513,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_matmul4_small(MatArgs a) {
       __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4) | (0 << 8));  // lgkmcnt(0)
       asm volatile("" ::: "memory");
       fetch(kb + 1, false);
+    }
+    Scales ea[4], eb[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      ea[f] = scales_of(ba[f], 8 * g);
+      eb[f] = scales_of(bb[f], 8 * g);
     }
     mma_block<4, 4>(fb, fa, eb, ea, acc);
   }
