@@ -103,7 +103,8 @@ __device__ __forceinline__ uint4 quad_rows(const uint32_t* q, int t) {
 // the XCDs as in the 8-bit kernel.
 template <bool BF, bool PLAIN, bool TRANS>
 __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
-  __shared__ __attribute__((aligned(16))) uint32_t bytes_of[2][kTile];                // 4 scale bytes of each row, column
+  __shared__ __attribute__((aligned(16))) uint32_t row_bytes[kTile];      // 4 scale bytes of each row
+  __shared__ __attribute__((aligned(16))) uint8_t col_bytes[4][kTile];    // one of each column for each wave's 32 rows
   __shared__ __attribute__((aligned(16))) uint8_t stage[TRANS ? kTile * kTile / 2 : 16];  // transposed codes
   const uint32_t x = blockIdx.x & 7;
   const uint32_t lo = (uint32_t)(((uint64_t)x * a.tiles) >> 3);
@@ -112,7 +113,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
   uint32_t index = (blockIdx.x >> 3) + ((x * count) >> 3);
   if (index >= count) index -= count;
   index += lo;
-  const uint32_t tr = index / a.tiles_c, tc = index - tr * a.tiles_c;
+  // two tile rows at a time: neighbours in both directions, whose codes share cache lines (64 bytes of either
+  // form a row and tile), come one after the other
+  const uint32_t tiles_r = a.tiles / a.tiles_c, band = index / (2 * a.tiles_c), in = index - band * (2 * a.tiles_c);
+  const uint32_t high = min(2u, tiles_r - 2 * band);
+  const uint32_t tc = high == 2 ? in >> 1 : in, tr = 2 * band + (high == 2 ? in & 1 : 0);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int64_t rows = a.rows, cols = a.cols;
   const int64_t r0 = (int64_t)tr * kTile + 8 * ty, c0 = (int64_t)tc * kTile + 8 * tx;
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
 
   if constexpr (PLAIN) {
     const int64_t ld = code_ld(cols);
-    uint32_t rows8[8];
+    uint32_t rows8[8], mine = 0;  // mine: the 4 bytes of row tx, in the lanes tx < 8
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       // the 4 lanes of a group
@@ -165,9 +170,14 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
         const uint32_t byte = h ? b >> 16 : b & 0xffu;
         if constexpr (BF) rows8[i] = codes8(w[i][0], w[i][1], w[i][2], w[i][3], byte);
         else rows8[i] = codes8(v[i], byte);
-        if ((tx & 3) == 0) reinterpret_cast<uint8_t*>(&bytes_of[0][8 * ty + i])[tx >> 2] = (uint8_t)byte;
+        // the 4 quads' bytes together (a byte's store by each quad: lanes that write to one word wait for each other)
+        uint32_t all = byte << (8 * (tx >> 2));
+        all |= from<0x124>(all);  // row rotated by 4
+        all |= from<0x128>(all);  // and by 8
+        mine = tx == i ? all : mine;
       }
     }
+    if (tx < 8) row_bytes[8 * ty + tx] = mine;
     // 16 bytes a lane, a quad's group of a row each (8192 x 2048 bf16 in both forms 13.4 -> 12.5
     // us against 4-byte stores)
 #pragma unroll
@@ -179,6 +189,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
   }
 
   if constexpr (TRANS) {
+    uint32_t bytes8[2] = {0, 0};  // of the lane's 8 columns
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       // the 4 thread rows of the wave
@@ -201,16 +212,16 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
         // Column 8 tx + j is the stage's row 16 j + tx (64 bytes), and its piece ty lies at ty ^ (tx & 12): the
         // 64 lanes of a store, 4 pieces of 16 columns, fall on 64 banks.
         *reinterpret_cast<uint32_t*>(stage + ((16 * j + tx) * 16 + (ty ^ (tx & 12))) * 4) = q;
-        if ((ty & 3) == 0) reinterpret_cast<uint8_t*>(&bytes_of[1][8 * tx + j])[ty >> 2] = (uint8_t)byte;
+        bytes8[j >> 2] |= byte << (8 * (j & 3));
       }
     }
+    if ((ty & 3) == 0) *reinterpret_cast<uint2*>(&col_bytes[ty >> 2][8 * tx]) = make_uint2(bytes8[0], bytes8[1]);
   }
   __syncthreads();
-  const uint32_t tiles_r = a.tiles / a.tiles_c;
   if constexpr (PLAIN) {
     const int64_t r = (int64_t)tr * kTile + tid;
     if (tid < kTile && r < rows) {
-      put_scales(a.scales, r, cols, tc, a.tiles_c, bytes_of[0][tid]);
+      put_scales(a.scales, r, cols, tc, a.tiles_c, row_bytes[tid]);
       // codes to a multiple of 256: an odd last tile's other half
       if (tc == a.tiles_c - 1 && (tc & 1) == 0) {
         uint4* p = reinterpret_cast<uint4*>(a.codes + r * code_ld(cols) + (int64_t)(tc + 1) * (kTile / 2));
@@ -235,7 +246,9 @@ __global__ __launch_bounds__(kThreads, 4) void k_quantize4(Args a) {
     }
     const int c = tid - (kThreads - kTile);
     if (c >= 0 && (int64_t)tc * kTile + c < cols)
-      put_scales(a.scales_t, (int64_t)tc * kTile + c, rows, tr, tiles_r, bytes_of[1][c]);
+      put_scales(a.scales_t, (int64_t)tc * kTile + c, rows, tr, tiles_r,
+                 (uint32_t)col_bytes[0][c] | (uint32_t)col_bytes[1][c] << 8 | (uint32_t)col_bytes[2][c] << 16 |
+                     (uint32_t)col_bytes[3][c] << 24);
   }
 }
 
