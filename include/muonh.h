@@ -511,7 +511,7 @@ int muonh_embedding(const void* ids, int32_t id_bytes, int64_t n, int64_t first,
  * where there is none, or added to grad's old values if `accumulate`, which then reads and
  * writes the rows that occur only. Ids that are no row have no part in it. grad: DEVICE, rows x cols
  * fp32, pitch grad_ld (the gradient that muonh_adamw_step reads); dy: n x cols of dy_dtype.
- * The tokens are sorted by their rows, stably, and each row's sum is taken in
+ * A row's tokens are brought together, in their order, and its sum is taken in
  * fp32 in an order that n, cols and the ids fix: deterministic, no atomics.
  * workspace: DEVICE, 256-byte aligned, at least
  * muonh_embedding_backward_workspace_bytes(n, cols) bytes (NULL if that is 0); calls in flight

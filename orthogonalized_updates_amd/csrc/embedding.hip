@@ -4,7 +4,7 @@
 //
 //   out[t] = scale * table[ids[t]];   G[v] (+)= scale * sum of dy[t] over ids[t] = v
 //
-// Both are bound by memory. The gradient sorts the tokens by id, stably, so
+// Both are bound by memory. The gradient brings a row's tokens together, in their order, so
 // that a row of G is read and written once, by whom is known, and its sum has a fixed
 // order: no atomics, the same bits every time.
 #include <algorithm>
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256) void k_lookup(LookArgs a) {
 
 // ---- the gradient of few tokens ------------------------------------------------------
 // Up to kFewMax tokens, in one launch (777 tokens into 5003 x 1001 from zero: 9 us, of which the
-// clearing is 5; sorted, summed and joined in three launches 28): a workgroup to each token and 512 columns,
+// clearing is 5; ordered, summed and joined in three launches 19 and the time between them): a workgroup to each token and 512 columns,
 // which does nothing unless its token is the first of its row, and else sums the row's tokens in their order:
 // up to 8 of them by one wave, more by 4, a quarter each, joined in order. Where G starts
 // at zero, the first `clearing` workgroups clear the rows that do not occur.
@@ -257,59 +257,160 @@ __device__ __forceinline__ void fill(const FillArgs& f, int64_t block, int64_t b
 __global__ __launch_bounds__(1024) void k_fill(FillArgs f) { fill(f, blockIdx.x, gridDim.x); }
 
 struct Sorted {
-  uint32_t *key, *tok;  // rows in ascending order, and whose they are
+  uint32_t *key, *tok;  // rows, equal ones together, and whose they are, ascending for each
 };
 
-// Up to kCountMax tokens: a token's place is the number of tokens before it,
-// counted over all of them, n^2 comparisons in one launch. Thread (x, y) of a
-// workgroup counts for token x of its kTok the tokens of slice y of all; waves read
-// the slice's rows from LDS as broadcasts. The workgroups past the first `sorting` fill G with zeros.
+// Up to kOrderMax tokens, in one launch: a workgroup to each of 256 buckets of rows reads all ids, takes
+// its own and counts those of the buckets before, which is where its part of the order begins. A row's
+// bucket is the high byte of row * kMul mod 2^24, which spreads neighbouring and evenly spaced rows over all of
+// them, and the product's other 16 bits name the row in its bucket. Entries of these 16 bits and
+// the token are all different, and their order is the tokens' within a row. The workgroups past the first
+// 256 fill G with zeros.
 //
-// 4096, 8192, 16384 tokens of 151936 rows: 6.8, 10.4, 27.8 us; the passes below take 52, 62, 64, launches apart.
-constexpr int kCountMax = 16384, kTok = 32, kSlices = 1024 / kTok;
-__global__ __launch_bounds__(1024) void k_count(Ids ids, int n, Sorted out, int sorting, FillArgs f) {
-  // n rounded up to 4 kSlices, then the counts
-  __shared__ __attribute__((aligned(16))) uint32_t keys[kCountMax + 1024];
-  if ((int)blockIdx.x >= sorting) {
-    fill(f, blockIdx.x - sorting, gridDim.x - sorting);
+// A frequent row may leave more entries than the kCounted that are sorted by counting the smaller ones: up to kFrequent
+// times the row of the first entry is set apart. What then is still too much is sorted bit by bit.
+//
+// 4096, 8192, 16384, 32768 tokens of 151936 rows: 5.3, 7.0, 12, 18.5 us, most of it the ids' way to
+// all workgroups (n^2 comparisons 6.8, 10.4, 27.8 up to 16384; the passes below 52, 62, 64, launches apart).
+// 8192 tokens of different rows in one bucket, the worst there is: 54 us, 32768 of them 210.
+constexpr int kOrderMax = 32768, kBuckets = 256, kCounted = 256, kFrequent = 4;
+constexpr uint32_t kMul = 0x9e3779, kInv = 0xb382c9, kNoRow = 1u << 24;
+static_assert((kMul * kInv & 0xffffffu) == 1, "rows from their products");
+static_assert(MUONH_MAX_FP8_DIM <= 1 << 24 && kOrderMax <= 1 << 16, "rows of 24 bits, tokens of 16");
+
+// K: tokens per thread.
+template <int K>
+__global__ __launch_bounds__(1024) void k_order(Ids ids, int n, Sorted out, FillArgs f) {
+  __shared__ __attribute__((aligned(16))) uint32_t list[1024 * K], sums[2][16];
+  if ((int)blockIdx.x >= kBuckets) {
+    fill(f, (int64_t)blockIdx.x - kBuckets, (int64_t)gridDim.x - kBuckets);
     return;
   }
-  const int per = (int)ceil_div(n, 4 * kSlices) * 4, all = per * kSlices;
-  for (int t = threadIdx.x; t < all; t += 8 * 1024) {
-    uint32_t r[8];
-    rows_of<8>(ids, t, 1024, n, r);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t bucket = blockIdx.x;
+  const uint64_t lower = (1ull << lane) - 1;
+  auto total = [&](int which) {  // over the waves
+    uint32_t s = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (t + k * 1024 < all) keys[t + k * 1024] = t + k * 1024 < n ? r[k] : 0xffffffffu;
+    for (int w = 0; w < 16; ++w) s += sums[which][w];
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)s);
+  };
+  auto before = [&](int which) {  // over the waves before this one
+    uint32_t s = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += w < wave ? sums[which][w] : 0;
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)s);
+  };
+
+  int m, begin;
+  {
+    const int per = (int)ceil_div(n, 1024) * 64, t0 = wave * per, end = min(t0 + per, n);
+    uint32_t h[K];
+    int own = 0, below = 0;
+    constexpr int kStep = K < 8 ? K : 8;
+#pragma unroll
+    for (int k0 = 0; k0 < K; k0 += kStep) {
+      uint32_t r[kStep];
+      rows_of<kStep>(ids, t0 + k0 * 64 + lane, 64, end, r);
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        const uint32_t v = r[k] < (uint32_t)ids.rows ? r[k] * kMul & (kNoRow - 1) : kNoRow;
+        h[k0 + k] = v;
+        own += __popcll(__ballot(v >> 16 == bucket));
+        below += __popcll(__ballot(v >> 16 < bucket));
+      }
+    }
+    if (lane == 0) {
+      sums[0][wave] = (uint32_t)own;
+      sums[1][wave] = (uint32_t)below;
+    }
+    __syncthreads();
+    m = (int)total(0);
+    begin = (int)total(1);
+    int at = (int)before(0);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const bool is = h[k] >> 16 == bucket;
+      const uint64_t mask = __ballot(is);
+      if (is) list[at + __popcll(mask & lower)] = h[k] << 16 | (uint32_t)(t0 + k * 64 + lane);
+      at += __popcll(mask);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int x = threadIdx.x & (kTok - 1), y = threadIdx.x / kTok;
-  const int t = (int)blockIdx.x * kTok + x;
-  const uint32_t mine = t < n ? keys[t] : 0u;
-  // rows equal to mine count where their token comes first: all of the 4 before t's own 4, and of those some
-  int count = 0;
-  const int end = (y + 1) * per, own = t & ~3;
+
+  // The first `count` entries in two parts, each in its old order; returns how many the first has.
+  auto split = [&](int count, auto second) -> int {
+    const int per = (int)ceil_div(count, 1024) * 64, i0 = wave * per + lane;
+    uint32_t e[K];
+    uint64_t masks[2];
+    uint32_t firsts = 0, seconds = 0;
+    auto part = [&](int k) {
+      const bool live = i0 + k * 64 < count, b = second(e[k]);
+      masks[0] = __ballot(live && !b);
+      masks[1] = __ballot(live && b);
+      return b;
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * 64 >= per) continue;
+      e[k] = list[min(i0 + k * 64, count - 1)];
+      part(k);
+      firsts += __popcll(masks[0]);
+      seconds += __popcll(masks[1]);
+    }
+    if (lane == 0) {
+      sums[0][wave] = firsts;
+      sums[1][wave] = seconds;
+    }
+    __syncthreads();
+    const int middle = (int)total(0);
+    int at[2] = {(int)before(0), middle + (int)before(1)};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * 64 >= per) continue;
+      const bool b = part(k);
+      if (i0 + k * 64 < count) list[b ? at[1] + __popcll(masks[1] & lower) : at[0] + __popcll(masks[0] & lower)] = e[k];
+      at[0] += __popcll(masks[0]);
+      at[1] += __popcll(masks[1]);
+    }
+    __syncthreads();
+    return middle;
+  };
+  int rest = m;
+  for (int i = 0; i < kFrequent && rest > kCounted; ++i) {
+    const uint32_t frequent = list[0] >> 16;
+    rest = split(rest, [&](uint32_t e) { return e >> 16 == frequent; });
+  }
+  if (rest > kCounted) {
+    for (int b = 16; b < 32; ++b) split(rest, [&](uint32_t e) { return (e >> b & 1) != 0; });
+  } else {  // 4 lanes an entry, each a quarter of the others
+    static_assert(4 * kCounted == 1024, "a turn");
+    const int mine = tid >> 2;
+    const uint32_t e = list[min(mine, max(rest - 1, 0))];
+    int place = 0;
 #pragma unroll 4
-  for (int i = y * per; i < end; i += 4) {
-    const u32x4 k = *reinterpret_cast<const u32x4*>(keys + i);
-    const uint32_t below = mine + (i < own ? 1u : 0u);
+    for (int i = 4 * (tid & 3); i < rest; i += 16) {
+      const u32x4 other = *reinterpret_cast<const u32x4*>(list + i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) count += k[j] < below ? 1 : 0;
+      for (int j = 0; j < 4; ++j) place += other[j] < e && i + j < rest ? 1 : 0;
+    }
+    place += __builtin_amdgcn_mov_dpp(place, 0xB1, 0xF, 0xF, false);  // quad [1,0,3,2]
+    place += __builtin_amdgcn_mov_dpp(place, 0x4E, 0xF, 0xF, false);  // quad [2,3,0,1]
+    __syncthreads();
+    if ((tid & 3) == 0 && mine < rest) list[place] = e;
+    __syncthreads();
   }
-  if (y * per <= own && own < end)
-    for (int i = own; i < t; ++i) count += keys[i] == mine ? 1 : 0;
-  uint32_t* sums = keys + all;
-  sums[y * kTok + x] = (uint32_t)count;
-  __syncthreads();
-  if (threadIdx.x < kTok && t < n) {
-    uint32_t place = 0;
-#pragma unroll
-    for (int s = 0; s < kSlices; ++s) place += sums[s * kTok + x];
-    out.key[place] = mine;
-    out.tok[place] = (uint32_t)t;
+  for (int i = tid; i < m; i += 1024) {
+    const uint32_t e = list[i];
+    out.key[begin + i] = (bucket << 16 | e >> 16) * kInv & (kNoRow - 1);
+    out.tok[begin + i] = e & 0xffffu;
   }
+  if (bucket == kBuckets - 1)  // ids that are no row
+    for (int i = begin + m + tid; i < n; i += 1024) {
+      out.key[i] = (uint32_t)ids.rows;
+      out.tok[i] = 0;
+    }
 }
-static_assert(kCountMax % (4 * kSlices) == 0, "rounded up, n fits keys");
 
 // More tokens: by 8 bits of the row at a time, from the lowest. A pass counts
 // each tile's digits, sums the counts up over digits and tiles, and moves the tokens.
@@ -416,12 +517,12 @@ __global__ __launch_bounds__(256) void k_move(PassArgs a) {
 }
 
 // ---- the sums -----------------------------------------------------------------------
-// The sorted tokens are cut into chunks of `chunk`. The chunk in which a row's
+// The ordered tokens are cut into chunks of `chunk`. The chunk in which a row's
 // tokens begin sums them to the end of the next chunk and, if that is all of them,
 // stores the row; what lies in later chunks is summed there (`head`) and joined to
 // the first sum (`tail`) by k_join. So most rows are stored at once, and a frequent token's
-// sum is shared out. 8192 tokens added to 151936 x 2048 from bf16: 21.7 us for about 86 MB (chunks of 4 and
-// 16: 21.4 and 22.5), k_join 5.3 (7.2 and 4.7).
+// sum is shared out. 8192 tokens added to 151936 x 2048 from bf16: 22.7 us for about 86 MB, k_join 4.8 (chunks of
+// 16: 23.9 and 5.2).
 struct SumArgs {
   Sorted s;
   const void* dy;
@@ -522,11 +623,16 @@ __global__ __launch_bounds__(256, 4) void k_sums(SumArgs a) {
 }
 
 // Rows whose tokens go on past the chunk after the one they begin in: the tail
-// and the heads, each of 4 waves a quarter of them, then the quarters in order. A
+// and the heads, each of the waves a part of them, then the parts in order. A
 // workgroup to each chunk and slab; most of them have nothing to do.
-template <int LPR>
-__global__ __launch_bounds__(256) void k_join(SumArgs a) {
-  __shared__ float sums[4][64 * 8 + 8];
+//
+// Waves that start only to stop cost as much as the sums do, so where chunks and slabs are many a row
+// has 4 of them, else 8 (us with 4, 8: 4088 workgroups 4.8, 7; 10782 tokens of 1208 rows, 2694 workgroups, 15.3, 10.7).
+constexpr unsigned kJoinWide = 3072;
+template <int LPR, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_join(SumArgs a) {
+  __shared__ float sums[WAVES][64 * 8 + 8];
+  constexpr int kFlight = 8;  // sums whose loads run together
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = (int)(blockIdx.x / a.slabs), slab = (int)(blockIdx.x % a.slabs);
   const int col = (slab * LPR + (lane & (LPR - 1))) * 8, left = lane < LPR ? a.cols - col : 0;
@@ -534,69 +640,56 @@ __global__ __launch_bounds__(256) void k_join(SumArgs a) {
   auto key_of = [&](int64_t chunk) { return key[chunk * a.chunk]; };
   const uint32_t k = key[(int64_t)(c + 1) * a.chunk - 1];
   if (k >= a.rows || key_of((int64_t)c + 2) != k || (c > 0 && key[(int64_t)c * a.chunk - 1] == k)) return;
-  {
-    int heads = 0;  // chunks c + 2 .. c + 1 + heads
-    for (;;) {
-      const int64_t q = (int64_t)c + 2 + heads + lane;
-      const uint64_t eq = __ballot(q < a.chunks && key_of(q) == k);
-      const int run = ~eq ? __builtin_ctzll(~eq) : 64;
-      heads += run;
-      if (run < 64) break;
-    }
-    const int lo = (int)((int64_t)wave * heads >> 2), hi = (int)((int64_t)(wave + 1) * heads >> 2);
-    float acc[8] = {};
-    if (left > 0) {
-      const float* p = a.head + ((int64_t)c + 2) * a.cols + col;
-      if (wave == 0) {
-        Raw<float> t;
-        const float* q = a.tail + (int64_t)c * a.cols + col;
-        if (left >= 8) t.load(q);
-        else t.load(q, left);
+  auto load = [&](Raw<float>& t, const float* p) {
+    if (left >= 8) t.load(p);
+    else t.load(p, left);
+  };
+  float* o = a.g + (int64_t)k * a.g_ld + col;
+  float acc[8] = {};
+  Raw<float> old, tail;
+  if (wave == 0 && left > 0) {
+    load(tail, a.tail + (int64_t)c * a.cols + col);
+    if (a.accumulate) load(old, o);
+  }
+  int heads = 0;  // chunks c + 2 .. c + 1 + heads
+  for (;;) {
+    const int64_t q = (int64_t)c + 2 + heads + lane;
+    const uint64_t eq = __ballot(q < a.chunks && key_of(q) == k);
+    const int run = ~eq ? __builtin_ctzll(~eq) : 64;
+    heads += run;
+    if (run < 64) break;
+  }
+  const int lo = (int)((int64_t)wave * heads / WAVES), hi = (int)((int64_t)(wave + 1) * heads / WAVES);
+  if (left > 0) {
+    const float* p = a.head + ((int64_t)c + 2) * a.cols + col;
+    if (wave == 0)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = t.at(j);
-      }
-      int h = lo;
-      for (; h + 4 <= hi; h += 4) {
-        Raw<float> t[4];
+      for (int j = 0; j < 8; ++j) acc[j] = tail.at(j);
+    for (int h = lo; h < hi; h += kFlight) {
+      Raw<float> t[kFlight];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float* q = p + (int64_t)(h + i) * a.cols;
-          if (left >= 8) t[i].load(q);
-          else t[i].load(q, left);
-        }
+      for (int i = 0; i < kFlight; ++i)
+        if (h + i < hi) load(t[i], p + (int64_t)(h + i) * a.cols);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kFlight; ++i)
+        if (h + i < hi)
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] += t[i].at(j);
-      }
-      for (; h < hi; ++h) {
-        Raw<float> t;
-        const float* q = p + (int64_t)h * a.cols;
-        if (left >= 8) t.load(q);
-        else t.load(q, left);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += t.at(j);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = acc[j];
-    __syncthreads();
-    if (wave == 0 && left > 0) {
-      float v[8];
-      float* o = a.g + (int64_t)k * a.g_ld + col;
-      Raw<float> old;
-      if (a.accumulate) {
-        if (left >= 8) old.load(o);
-        else old.load(o, left);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = acc[j] + sums[1][lane * 8 + j] + sums[2][lane * 8 + j] + sums[3][lane * 8 + j];
-        v[j] = a.accumulate ? __builtin_fmaf(s, a.scale, old.at(j)) : s * a.scale;
-      }
-      store8(o, v, left);
     }
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = acc[j];
+  __syncthreads();
+  if (wave || left <= 0) return;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float s = acc[j];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += sums[w][lane * 8 + j];
+    v[j] = a.accumulate ? __builtin_fmaf(s, a.scale, old.at(j)) : s * a.scale;
+  }
+  store8(o, v, left);
 }
 
 // ---- host side ----------------------------------------------------------------------
@@ -620,18 +713,18 @@ Plan plan_of(int64_t n, int64_t cols) {
   while (p.chunk < 256 && n * p.slabs * (p.lpr / 16) > (int64_t)p.chunk * 16384) p.chunk *= 2;
   p.chunks = (int)ceil_div(n, p.chunk);
   p.tiles = (int)ceil_div(n, kTile);
-  const bool count = n <= kCountMax;
+  const bool ordered = n <= kOrderMax;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = up256(at + bytes);
     return here;
   };
-  for (int i = 0; i < (count ? 1 : 2); ++i) {
+  for (int i = 0; i < (ordered ? 1 : 2); ++i) {
     p.key[i] = take((size_t)n * 4);
     p.tok[i] = take((size_t)n * 4);
   }
-  p.counts = count ? 0 : take((size_t)kDigits * p.tiles * 4);
+  p.counts = ordered ? 0 : take((size_t)kDigits * p.tiles * 4);
   p.tail = take((size_t)p.chunks * cols * 4);
   p.head = take((size_t)p.chunks * cols * 4);
   p.bytes = at;
@@ -767,10 +860,13 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
     return Sorted{reinterpret_cast<uint32_t*>(ws + p.key[i]), reinterpret_cast<uint32_t*>(ws + p.tok[i])};
   };
   SumArgs a{};
-  if (n <= kCountMax) {
-    const int sorting = (int)ceil_div(n, kTok);
-    hipLaunchKernelGGL(k_count, dim3((unsigned)(sorting + fills)), dim3(1024), 0, s, which, (int)n,
-                       sorted(0), sorting, f);
+  if (n <= kOrderMax) {
+    const dim3 grid((unsigned)(kBuckets + fills));
+    auto order = [&](auto per) { hipLaunchKernelGGL((k_order<decltype(per)::value>), grid, dim3(1024), 0, s, which, (int)n, sorted(0), f); };
+    if (n <= 4096) order(std::integral_constant<int, 4>{});
+    else if (n <= 8192) order(std::integral_constant<int, 8>{});
+    else if (n <= 16384) order(std::integral_constant<int, 16>{});
+    else order(std::integral_constant<int, 32>{});
     a.s = sorted(0);
   } else {
     if (fills) hipLaunchKernelGGL(k_fill, dim3((unsigned)fills), dim3(1024), 0, s, f);
@@ -805,7 +901,7 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
   a.rows = (uint32_t)rows;
   a.scale = scale;
   const int64_t groups = (int64_t)p.chunks * p.slabs;
-  const dim3 sums((unsigned)ceil_div(groups, 256 / p.lpr)), join((unsigned)((int64_t)(p.chunks - 2) * p.slabs));
+  const dim3 sums((unsigned)ceil_div(groups, 256 / p.lpr));
   auto run = [&](auto type) {
     using T = decltype(type);
     if (p.lpr == 16) hipLaunchKernelGGL((k_sums<T, 16>), sums, dim3(256), 0, s, a);
@@ -814,8 +910,10 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
   if (dy_dtype == MUONH_DT_BF16) run(__bf16{});
   else run(float{});
   if (p.chunks > 2) {
-    if (p.lpr == 16) hipLaunchKernelGGL((k_join<16>), join, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_join<64>), join, dim3(256), 0, s, a);
+    const dim3 join((unsigned)((p.chunks - 2) * p.slabs));
+    if (p.lpr == 16) hipLaunchKernelGGL((k_join<16, 8>), join, dim3(512), 0, s, a);
+    else if (join.x <= kJoinWide) hipLaunchKernelGGL((k_join<64, 8>), join, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_join<64, 4>), join, dim3(256), 0, s, a);
   }
   return launched("embedding backward");
 }

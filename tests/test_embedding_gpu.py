@@ -104,10 +104,12 @@ def test_values_pass_through():
     assert torch.equal(mh().embedding(torch.tensor([0, 5], device="cuda"), t).view(torch.int32), torch.stack([t[0], torch.zeros(6, device="cuda")]).view(torch.int32))
 
 
-# up to 1024 tokens in one launch; else chunks of 4 to 64 tokens, the counting sort up to 16384 tokens, then passes of 8 bits
+# up to 1024 tokens in one launch; else chunks of 4 to 64 tokens, in the order of one launch up to 32768 tokens (4, 8, 16 or 32 a
+# thread), then of passes of 8 bits
 SIZES = [(1, 1, 1), (1, 300, 2048), (2, 3, 5), (4, 4, 64), (5, 7, 128), (9, 2, 129), (13, 300, 520), (100, 257, 1001), (777, 5003, 1001),
          (1000, 256, 2048), (1024, 300, 520), (1025, 300, 520), (1024, 40000, 6), (4099, 1000, 100), (3000, 90, 4096), (16384, 3000, 64), (16385, 3000, 64), (20000, 255, 40), (20000, 256, 40),
-         (20000, 257, 40), (50001, 70000, 24), (140000, 66000, 136), (70000, 1 << 24, 1), (9000, 151936, 8)]
+         (20000, 257, 40), (50001, 70000, 24), (140000, 66000, 136), (70000, 1 << 24, 1), (9000, 151936, 8),
+         (4096, 700, 16), (4097, 700, 16), (8192, 90000, 9), (8193, 500, 24), (32768, 40000, 8), (32769, 40000, 8)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -124,6 +126,26 @@ def test_gradient_of_whole_numbers_is_exact(n, rows, cols, kind):
     assert torch.equal(got.double(), want)
     got = mh().embedding_backward(ids, dy, old.clone(), scale=0.5, accumulate=True)
     assert torch.equal(got.double(), want + old.double())
+
+
+@pytest.mark.parametrize("kind", ["distinct", "frequent", "many frequent", "one of them"])
+@pytest.mark.parametrize("n", [1025, 4096, 5000, 16384, 32768])
+def test_gradient_of_rows_that_share_a_bucket(n, kind):
+    """The worst ids for the order of the tokens: products with its multiplier that differ in their low 16 bits only."""
+    rows, rng = 1 << 24, np.random.default_rng((n, 9))
+    inverse = pow(0x9E3779, -1, 1 << 24)
+    here = (77 << 16 | rng.permutation(1 << 16)) * inverse % rows
+    v = here[:n].copy()
+    if kind == "frequent":  # one row's for the most part
+        v = np.where(rng.random(n) < 0.9, here[0], v)
+    elif kind == "many frequent":
+        v = np.where(rng.random(n) < 0.8, here[rng.integers(0, 9, n)], v)
+    elif kind == "one of them":  # and other buckets' in between, few of this one's rows
+        v = np.where(rng.random(n) < 0.5, here[rng.integers(0, 40, n)], rng.integers(0, rows, n))
+    ids, dy = torch.from_numpy(v.astype(np.int64)).cuda(), whole(n, 2, 2)
+    want = torch.zeros(rows, 2, dtype=torch.float64, device="cuda").index_add_(0, ids, dy.double())
+    got = mh().embedding_backward(ids, dy, torch.full((rows, 2), float("nan"), device="cuda"))
+    assert torch.equal(got.double(), want)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -216,7 +238,7 @@ def test_python_refuses():
             call()
 
 
-@pytest.mark.parametrize("n", [700, 17000])
+@pytest.mark.parametrize("n", [700, 17000, 33000])
 def test_captured_graph_and_other_stream(n):
     ids, dy = ids_of("frequent", n, 900, 1), normal(n, 520, 2, "bf16")
     table, g = normal(900, 520, 3), torch.zeros(900, 520, device="cuda")
