@@ -629,7 +629,7 @@ __global__ __launch_bounds__(256, 4) void k_sums(SumArgs a) {
 //
 // Waves that start only to stop cost as much as the sums do, so where chunks and slabs are many a row
 // has 4 of them, else 8 (us with 4, 8: 4088 workgroups 4.8, 7; 10782 tokens of 1208 rows, 2694 workgroups, 15.3, 10.7).
-constexpr unsigned kJoinWide = 3072;
+constexpr unsigned kJoinWide = 3500;
 template <int LPR, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_join(SumArgs a) {
   __shared__ float sums[WAVES][64 * 8 + 8];
