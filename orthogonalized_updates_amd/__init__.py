@@ -1225,13 +1225,15 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual=None, out=None, dweight=Non
 
 
 # -- embedding -------------------------------------------------------------------
-def _ids(ids, dev) -> int:
-    """Bytes per id of a contiguous int32 or int64 tensor."""
+def _ids(ids, dev, first) -> int:
+    """Bytes per id of a contiguous int32 or int64 tensor; first: a whole number that an id can be."""
     import torch
     if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be an int32 or int64 torch tensor")
     if ids.device != dev or not ids.is_contiguous():
         raise ValueError(f"ids must be contiguous and on {dev}")
+    if first != int(first) or first >= 1 << 63:
+        raise ValueError(f"first must be a whole number below 2^63, got {first}")
     return ids.element_size()
 
 
@@ -1263,7 +1265,7 @@ def embedding(ids, table, scale: float = 1.0, out=None, out_dtype=None, first: i
     import torch
     dt, ld = _rows("table", table, getattr(table, "device", None))
     dev = table.device
-    nbytes = _ids(ids, dev)
+    nbytes = _ids(ids, dev, first)
     rows, cols = table.shape
     if out is None:
         odt = dt if out_dtype is None else _fp8_dt(torch, out_dtype)
@@ -1291,7 +1293,7 @@ def embedding_backward(ids, dy, out, scale: float = 1.0, accumulate: bool = Fals
     import torch
     _, ld = _rows("out", out, getattr(out, "device", None), None, torch.float32)
     dev = out.device
-    nbytes = _ids(ids, dev)
+    nbytes = _ids(ids, dev, first)
     rows, cols = out.shape
     flat = _by_token("dy", dy, ids, cols)
     ddt, dld = _rows("dy", flat, dev)

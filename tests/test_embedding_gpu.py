@@ -225,6 +225,7 @@ def test_python_refuses():
     ids, t, dy = torch.zeros(3, dtype=torch.int64, device="cuda"), normal(4, 8, 1), normal(3, 8, 2)
     for call in (lambda: m.embedding(ids.cpu(), t), lambda: m.embedding(ids, t.t()), lambda: m.embedding(ids, t, out=torch.empty(3, 7, device="cuda")),
                  lambda: m.embedding(torch.zeros(6, dtype=torch.int64, device="cuda")[::2], t), lambda: m.embedding_backward(ids, dy[:2], t),
+                 lambda: m.embedding(ids, t, first=1 << 64), lambda: m.embedding(ids, t, first=0.5), lambda: m.embedding_backward(ids, dy, t.clone(), first=1 << 63),
                  lambda: m.embedding(ids.view(3, 1), t, out=torch.empty(1, 3, 8, device="cuda").transpose(0, 1)[:, :, :7])):
         with pytest.raises(ValueError):
             call()
