@@ -1232,8 +1232,9 @@ def _ids(ids, dev, first) -> int:
         raise TypeError("ids must be an int32 or int64 torch tensor")
     if ids.device != dev or not ids.is_contiguous():
         raise ValueError(f"ids must be contiguous and on {dev}")
-    if first != int(first) or first >= 1 << 63:
-        raise ValueError(f"first must be a whole number below 2^63, got {first}")
+    # ctypes would take it modulo 2^64; the call refuses what is below zero
+    if not -(1 << 63) <= first < 1 << 63 or first != int(first):
+        raise ValueError(f"first must be a whole number of 64 bits, got {first}")
     return ids.element_size()
 
 
@@ -1254,7 +1255,8 @@ def _by_token(name: str, t, ids, cols: int):
 
 def embedding(ids, table, scale: float = 1.0, out=None, out_dtype=None, first: int = 0):
     """out[...] = scale * table[ids[...] - first] (muonh_embedding); an id that is
-    no row of the table (padding, or a row of another part of it) gives zeros.
+    no row of the table (padding, or a row of another part of it) gives zeros. first >= 0: the
+    id of the table's first row.
 
     ids: a contiguous int32 or int64 tensor of any shape; table: a 2-d fp32 or
     bf16 tensor whose rows are contiguous; out: a tensor of shape ids.shape +

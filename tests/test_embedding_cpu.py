@@ -98,3 +98,21 @@ def test_python_refuses():
         mh.embedding(ids, t.double())
     with pytest.raises(TypeError):
         mh.embedding_backward(ids, torch.zeros(3, 8), t.bfloat16())
+
+
+@pytest.mark.parametrize("first", [-(1 << 64), -(1 << 64) + 5, -(1 << 63) - 1, 1 << 63, 1 << 64, float("inf"), float("-inf"), float("nan"), 0.5])
+def test_first_that_the_call_could_not_hold(first):
+    """64 bits signed: the call would take the value modulo 2^64, -2^64 as 0."""
+    torch = pytest.importorskip("torch")
+    ids = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="first"):
+        mh._ids(ids, ids.device, first)
+
+
+@pytest.mark.parametrize("first", [0, 5, (1 << 63) - 1, -1, -(1 << 63), 3.0, np.int64(7)])
+def test_first_that_it_holds(first):
+    """Those below zero are refused by the call itself."""
+    torch = pytest.importorskip("torch")
+    ids = torch.zeros(3, dtype=torch.int32)
+    assert mh._ids(ids, ids.device, first) == 4
+    assert _look(first=int(first), n=0) == (mh.MUONH_OK if first >= 0 else mh.MUONH_EINVAL)
