@@ -32,9 +32,10 @@ struct Ids {
 // The row of token t's id; `rows` for an id that is no row.
 __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t t) {
   const int64_t id = ids.wide ? static_cast<const int64_t*>(ids.p)[t] : (int64_t) static_cast<const int32_t*>(ids.p)[t];
-  // as unsigned, so that ids below `first`, and differences past 2^63, are past the end too
+  // as unsigned, so that ids below `first` are past the end too; first >= 0, so only from a negative id may
+  // the difference pass 2^64
   const uint64_t r = (uint64_t)id - (uint64_t)ids.first;
-  return r < (uint64_t)ids.rows ? (uint32_t)r : (uint32_t)ids.rows;
+  return id >= 0 && r < (uint64_t)ids.rows ? (uint32_t)r : (uint32_t)ids.rows;
 }
 
 // The rows of tokens t, t + step, ... (N of them; `rows` from n on), whose loads run together.
@@ -51,7 +52,7 @@ __device__ __forceinline__ void rows_of(const Ids& ids, int t, int step, int n, 
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const uint64_t v = (uint64_t)id[k] - (uint64_t)ids.first;
-    r[k] = t + k * step < n && v < (uint64_t)ids.rows ? (uint32_t)v : (uint32_t)ids.rows;
+    r[k] = t + k * step < n && id[k] >= 0 && v < (uint64_t)ids.rows ? (uint32_t)v : (uint32_t)ids.rows;
   }
 }
 

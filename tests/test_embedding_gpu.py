@@ -239,6 +239,23 @@ def test_python_refuses():
             call()
 
 
+@pytest.mark.parametrize("n", [4, 1000, 1500, 30000, 33000])
+@pytest.mark.parametrize("back", [1, 3, 5, 6, 4000])
+def test_ids_at_both_ends_of_64_bits(n, back):
+    """The lowest ids minus a `first` near 2^63 pass 2^64: they are below `first` all the same."""
+    first, rows, cols = (1 << 63) - back, 5, 40
+    rng = np.random.default_rng((n, back))
+    v = np.where(rng.random(n) < 0.5, rng.integers(-(1 << 63), -(1 << 63) + 8, n), (1 << 63) - 1 - rng.integers(0, 8, n))
+    row = torch.from_numpy(np.where(v >= first, v - np.where(v >= first, first, 0), rows)).cuda()
+    row = torch.where(row < rows, row, rows)
+    ids, t, dy = torch.from_numpy(v).cuda(), whole(rows, cols, 1), whole(n, cols, 2)
+    assert torch.equal(mh().embedding(ids, t, first=first), torch.cat([t, torch.zeros(1, cols, device="cuda")])[row])
+    want = torch.zeros(rows + 1, cols, device="cuda").index_add_(0, row, dy)[:rows]
+    got = mh().embedding_backward(ids, dy, torch.full((rows, cols), float("nan"), device="cuda"), first=first)
+    assert torch.equal(got, want)
+    assert torch.equal(mh().embedding_backward(ids, dy, t.clone(), first=first, accumulate=True), t + want)
+
+
 @pytest.mark.parametrize("n", [700, 17000, 33000])
 def test_captured_graph_and_other_stream(n):
     ids, dy = ids_of("frequent", n, 900, 1), normal(n, 520, 2, "bf16")
