@@ -9,20 +9,17 @@
 // order: no atomics, the same bits every time.
 #include <algorithm>
 
-#include "fp8_internal.h"
+#include "embedding_plan.h"
 #include "rows.h"
 
 namespace muonh {
 namespace embed {
 namespace {
 
-using fp8::ceil_div;
 using fp8::overlap;
 using namespace rows;
 
 constexpr int kMaxGrid = 1 << 20;
-// of dy: the launches of k_sums and k_few stay below 2^32 threads
-constexpr int64_t kMaxEntries = 1LL << 38;
 
 struct Ids {
   const void* p;
@@ -112,7 +109,6 @@ __global__ __launch_bounds__(256) void k_lookup(LookArgs a) {
 // which does nothing unless its token is the first of its row, and else sums the row's tokens in their order:
 // up to 8 of them by one wave, more by 4, a quarter each, joined in order. Where G starts
 // at zero, the first `clearing` workgroups clear the rows that do not occur.
-constexpr int kFewMax = 1024;
 struct FewArgs {
   Ids ids;
   const void* dy;
@@ -275,7 +271,7 @@ struct Sorted {
 // all workgroups (n^2 comparisons 6.8, 10.4, 27.8 up to 16384; the passes below 52, 62, 64, launches apart).
 // 8192 tokens of different rows in one bucket, the worst there is: 54 us, 32768 of them 210. Rows in ascending order
 // would save the sums 1 us of 22.7 (pages of neighbours), and buckets of neighbours fill unevenly.
-constexpr int kOrderMax = 32768, kBuckets = 256, kCounted = 256, kFrequent = 4;
+constexpr int kBuckets = 256, kCounted = 256, kFrequent = 4;
 constexpr uint32_t kMul = 0x9e3779, kInv = 0xb382c9, kNoRow = 1u << 24;
 static_assert((kMul * kInv & 0xffffffu) == 1, "rows from their products");
 static_assert(MUONH_MAX_FP8_DIM <= 1 << 24 && kOrderMax <= 1 << 16, "rows of 24 bits, tokens of 16");
@@ -416,7 +412,6 @@ __global__ __launch_bounds__(1024) void k_order(Ids ids, int n, Sorted out, Fill
 
 // More tokens: by 8 bits of the row at a time, from the lowest. A pass counts
 // each tile's digits, sums the counts up over digits and tiles, and moves the tokens.
-constexpr int kTile = 4096, kDigits = 256;
 struct PassArgs {
   Ids ids;
   Sorted in, out;  // in.key == nullptr: the ids themselves
@@ -627,10 +622,6 @@ __global__ __launch_bounds__(256, 4) void k_sums(SumArgs a) {
 // Rows whose tokens go on past the chunk after the one they begin in: the tail
 // and the heads, each of the waves a part of them, then the parts in order. A
 // workgroup to each chunk and slab; most of them have nothing to do.
-//
-// Waves that start only to stop cost as much as the sums do, so where chunks and slabs are many a row
-// has 4 of them, else 8 (us with 4, 8: 4088 workgroups 4.8, 7; 10782 tokens of 1208 rows, 2694 workgroups, 15.3, 10.7).
-constexpr unsigned kJoinWide = 3500;
 template <int LPR, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_join(SumArgs a) {
   __shared__ float sums[WAVES][64 * 8 + 8];
@@ -695,44 +686,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_join(SumArgs a) {
 }
 
 // ---- host side ----------------------------------------------------------------------
-// Where things are in the workspace, and how the tokens are cut.
-struct Plan {
-  int64_t n;
-  int lpr, slabs, chunk, chunks, tiles;
-  size_t key[2], tok[2], counts, tail, head, bytes;
-};
-// Whether k_few takes the call: a launch has fewer than 2^32 threads.
-bool few(int64_t n, int64_t cols) { return n <= kFewMax && n * ceil_div(cols, 512) < (1 << 23); }
-size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
-Plan plan_of(int64_t n, int64_t cols) {
-  Plan p{};
-  p.n = n;
-  if (few(n, cols)) return p;
-  p.lpr = cols <= 128 ? 16 : 64;
-  p.slabs = (int)ceil_div(cols, p.lpr * 8);
-  // about 4096 waves, 16 a CU; each chunk pays for its ends
-  p.chunk = 4;
-  while (p.chunk < 256 && n * p.slabs * (p.lpr / 16) > (int64_t)p.chunk * 16384) p.chunk *= 2;
-  p.chunks = (int)ceil_div(n, p.chunk);
-  p.tiles = (int)ceil_div(n, kTile);
-  const bool ordered = n <= kOrderMax;
-  size_t at = 0;
-  auto take = [&](size_t bytes) {
-    const size_t here = at;
-    at = up256(at + bytes);
-    return here;
-  };
-  for (int i = 0; i < (ordered ? 1 : 2); ++i) {
-    p.key[i] = take((size_t)n * 4);
-    p.tok[i] = take((size_t)n * 4);
-  }
-  p.counts = ordered ? 0 : take((size_t)kDigits * p.tiles * 4);
-  p.tail = take((size_t)p.chunks * cols * 4);
-  p.head = take((size_t)p.chunks * cols * 4);
-  p.bytes = at;
-  return p;
-}
-
 int check_ids(const void* ids, int32_t id_bytes, int64_t n, int64_t rows, int64_t cols, int64_t first) {
   if (id_bytes != 4 && id_bytes != 8) return fail(MUONH_EINVAL, "id_bytes=%d is neither 4 nor 8", id_bytes);
   if (fp8::bad_dim(n)) return fail(MUONH_ESHAPE, "%lld ids out of [0, %d]", (long long)n, MUONH_MAX_FP8_DIM);
@@ -914,7 +867,7 @@ int muonh_embedding_backward(const void* ids, int32_t id_bytes, int64_t n, int64
   if (p.chunks > 2) {
     const dim3 join((unsigned)((p.chunks - 2) * p.slabs));
     if (p.lpr == 16) hipLaunchKernelGGL((k_join<16, 8>), join, dim3(512), 0, s, a);
-    else if (join.x <= kJoinWide) hipLaunchKernelGGL((k_join<64, 8>), join, dim3(512), 0, s, a);
+    else if (join_waves(p) == 8) hipLaunchKernelGGL((k_join<64, 8>), join, dim3(512), 0, s, a);
     else hipLaunchKernelGGL((k_join<64, 4>), join, dim3(256), 0, s, a);
   }
   return launched("embedding backward");

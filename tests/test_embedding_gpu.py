@@ -128,6 +128,17 @@ def test_gradient_of_whole_numbers_is_exact(n, rows, cols, kind):
     assert torch.equal(got.double(), want + old.double())
 
 
+# several slabs of columns, where 4 waves join a row's sums, up to the most workgroups that do; one slab with as many
+MORE_SIZES = [(8192, 3000, 2048), (30000, 400, 601), (4000, 150000, 2047), (33000, 500, 520), (70000, 300, 1030), (16000, 900, 500),
+              (32768, 700, 300), (40000, 900, 130), (140000, 60, 20)]
+
+
+@pytest.mark.parametrize("kind", ["same", "frequent", "runs", "mixed"])
+@pytest.mark.parametrize("n,rows,cols", MORE_SIZES)
+def test_gradient_of_many_chunks_is_exact(n, rows, cols, kind):
+    test_gradient_of_whole_numbers_is_exact(n, rows, cols, kind)
+
+
 @pytest.mark.parametrize("kind", ["distinct", "frequent", "many frequent", "one of them"])
 @pytest.mark.parametrize("n", [1025, 4096, 5000, 16384, 32768])
 def test_gradient_of_rows_that_share_a_bucket(n, kind):
