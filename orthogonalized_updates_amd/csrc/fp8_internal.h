@@ -42,7 +42,7 @@ inline bool bad_dim(int64_t v) { return v < 0 || v > MUONH_MAX_FP8_DIM; }
 constexpr int64_t kMaxBlocks = (1 << 24) - 8;
 bool tiles_fit(int64_t rows, int64_t cols);
 
-// codes, scales, codes_t, scales_t (MUONH_FP8_ROWS; codes and scales may be
+// codes, scales, codes_t, scales_t (MUONH_FP8_ROWS; codes and scales, not codes_t and scales_t, may be
 // nullptr) of the matrix (src[r][c] * rstd[r]) * weight[c]. Arguments are the
 // caller's to check.
 int quantize_normed(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t src_ld, const float* rstd,

@@ -282,10 +282,10 @@ void launch_forms(const Args& a, bool plain, bool trans, hipStream_t s) {
   const dim3 grid((unsigned)(8 * ceil_div(a.tiles, 8))), thr(kThreads);
   if (plain && trans)
     hipLaunchKernelGGL((k_quantize<BF, TILES, true, true, NORM>), grid, thr, 0, s, a);
-  else if (plain)
-    hipLaunchKernelGGL((k_quantize<BF, TILES, true, false, NORM>), grid, thr, 0, s, a);
-  else
+  else if (trans)
     hipLaunchKernelGGL((k_quantize<BF, TILES, false, true, NORM>), grid, thr, 0, s, a);
+  else if constexpr (!NORM)  // the norm's own kernel writes a plain form alone
+    hipLaunchKernelGGL((k_quantize<BF, TILES, true, false, false>), grid, thr, 0, s, a);
 }
 
 int launched(const char* what) {
@@ -314,8 +314,8 @@ int quantize_normed(const void* src, int32_t dtype, int64_t rows, int64_t cols, 
   a.scales_t = scales_t;
   a.rstd = rstd;
   a.weight = weight;
-  if (dtype == MUONH_DT_BF16) launch_forms<true, false, true>(a, codes != nullptr, codes_t != nullptr, s);
-  else launch_forms<false, false, true>(a, codes != nullptr, codes_t != nullptr, s);
+  if (dtype == MUONH_DT_BF16) launch_forms<true, false, true>(a, codes != nullptr, true, s);
+  else launch_forms<false, false, true>(a, codes != nullptr, true, s);
   return launched("rms norm in 8 bits");
 }
 
