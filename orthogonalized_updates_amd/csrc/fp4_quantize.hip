@@ -11,7 +11,6 @@
 // it, rounds once (to nearest, ties to even).
 #include "fp4_internal.h"
 #include "fp8_codes.h"
-#include "rows.h"
 
 namespace muonh {
 namespace fp4 {
@@ -22,6 +21,7 @@ using fp8::u16x2;
 using fp8::umax;
 using rows::bad_dtype;
 using rows::launched;
+using rows::misaligned;
 
 constexpr int kThreads = 256;
 constexpr int kTile = 128;
@@ -306,8 +306,6 @@ void launch_forms(const Args& a, hipStream_t s) {
   else if (a.codes) hipLaunchKernelGGL((k_quantize4<BF, true, false>), grid, thr, 0, s, a);
   else hipLaunchKernelGGL((k_quantize4<BF, false, true>), grid, thr, 0, s, a);
 }
-
-bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 }  // namespace
 }  // namespace fp4

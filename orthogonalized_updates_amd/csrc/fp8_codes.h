@@ -5,10 +5,13 @@
 
 #include <type_traits>
 
-#include "fp8_internal.h"
+#include "rows.h"
 
 namespace muonh {
 namespace fp8 {
+
+using rows::f32x4_a4;
+using rows::u32x4_a2;
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
@@ -79,11 +82,6 @@ __device__ __forceinline__ uint2 codes8(uint32_t a, uint32_t b, uint32_t c, uint
   const s16x2 y = two(two(s16x2{0, 0}, c, std::false_type{}), d, std::true_type{});
   return make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
 }
-
-// 8 consecutive entries from i, at any multiple of the entry's size (gfx950
-// takes vector accesses at any address).
-typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // A thread's 8 x 8 entries: zeros past the matrix.
 __device__ __forceinline__ void load_patch(const float* p, int64_t ld, int64_t r0, int64_t c0, int64_t rows,

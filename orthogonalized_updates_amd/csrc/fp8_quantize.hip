@@ -19,6 +19,9 @@ namespace muonh {
 namespace fp8 {
 namespace {
 
+using rows::launched;
+using rows::misaligned;
+
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 16;
 
@@ -287,14 +290,6 @@ void launch_forms(const Args& a, bool plain, bool trans, hipStream_t s) {
   else if constexpr (!NORM)  // the norm's own kernel writes a plain form alone
     hipLaunchKernelGGL((k_quantize<BF, TILES, true, false, false>), grid, thr, 0, s, a);
 }
-
-int launched(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(MUONH_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
-  return MUONH_OK;
-}
-
-bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 }  // namespace
 

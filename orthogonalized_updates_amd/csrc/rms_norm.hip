@@ -568,10 +568,9 @@ int muonh_rms_norm(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, i
   }
   if (y)
     if (const int err = check_mat(out, cols)) return err;
-  auto off = [](const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; };
-  if (!weight || off(weight, 4)) return fail(MUONH_EINVAL, "weight must be a 4-byte aligned array of cols floats");
-  if (!rstd || off(rstd, 4)) return fail(MUONH_EINVAL, "rstd must be a 4-byte aligned array of rows floats");
-  if (off(codes, 16) || off(codes_t, 16) || off(scales, 4) || off(scales_t, 4))
+  if (!weight || misaligned(weight, 4)) return fail(MUONH_EINVAL, "weight must be a 4-byte aligned array of cols floats");
+  if (!rstd || misaligned(rstd, 4)) return fail(MUONH_EINVAL, "rstd must be a 4-byte aligned array of rows floats");
+  if (misaligned(codes, 16) || misaligned(codes_t, 16) || misaligned(scales, 4) || misaligned(scales_t, 4))
     return fail(MUONH_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
   if (codes_t && !fp8::tiles_fit(rows, cols)) return fail(MUONH_ESHAPE, "2^24 tiles of 128 x 128 or more");
   // h may take the place of x or of the residual, entry by entry
@@ -651,8 +650,7 @@ int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, con
   if (bad_dtype(dy_dtype)) return fail(MUONH_EINVAL, "dy_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", dy_dtype);
   if (bad_dtype(h_dtype)) return fail(MUONH_EINVAL, "h_dtype=%d is neither MUONH_DT_FP32 nor MUONH_DT_BF16", h_dtype);
   if (const int err = check_shape(rows, cols)) return err;
-  auto off = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; };
-  if (!dweight || off(dweight)) return fail(MUONH_EINVAL, "dweight must be a 4-byte aligned array of cols floats");
+  if (!dweight || misaligned(dweight, 4)) return fail(MUONH_EINVAL, "dweight must be a 4-byte aligned array of cols floats");
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 join((unsigned)ceil_div(cols, 16));
   if (rows == 0) {  // the sum over no rows
@@ -667,8 +665,8 @@ int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, con
   if (dresidual)
     if (const int err = check_mat(res, cols)) return err;
   if (const int err = check_mat(out, cols)) return err;
-  if (!weight || off(weight)) return fail(MUONH_EINVAL, "weight must be a 4-byte aligned array of cols floats");
-  if (!rstd || off(rstd)) return fail(MUONH_EINVAL, "rstd must be a 4-byte aligned array of rows floats");
+  if (!weight || misaligned(weight, 4)) return fail(MUONH_EINVAL, "weight must be a 4-byte aligned array of cols floats");
+  if (!rstd || misaligned(rstd, 4)) return fail(MUONH_EINVAL, "rstd must be a 4-byte aligned array of rows floats");
   const size_t need = back_bytes(rows, cols);
   if (!workspace) return fail(MUONH_EWORKSPACE, "workspace is NULL, the call needs %zu bytes", need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MUONH_EWORKSPACE, "workspace must be 256-byte aligned");

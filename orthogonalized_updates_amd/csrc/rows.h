@@ -1,5 +1,5 @@
 // Rows of fp32 or bf16 entries: what the operators that go through them in
-// vectors of 8 share (rms_norm.hip, embedding.hip), device side and argument checks.
+// vectors of 8 share (rms_norm.hip, embedding.hip, the quantizers), device side and argument checks.
 #pragma once
 
 #include "fp8_internal.h"
@@ -76,6 +76,7 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8], int n) {
 
 // ---- host side ----------------------------------------------------------------
 inline bool bad_dtype(int32_t d) { return d != MUONH_DT_FP32 && d != MUONH_DT_BF16; }
+inline bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 inline int size_of(int32_t d) { return d == MUONH_DT_BF16 ? 2 : 4; }
 
 // A 2-d argument: rows of `cols` entries, ld apart.
@@ -87,7 +88,7 @@ struct Mat {
 };
 inline int check_mat(const Mat& m, int64_t cols) {
   if (!m.p) return fail(MUONH_EINVAL, "%s is NULL", m.name);
-  if (reinterpret_cast<uintptr_t>(m.p) & (uintptr_t)(size_of(m.dtype) - 1))
+  if (misaligned(m.p, (uintptr_t)size_of(m.dtype)))
     return fail(MUONH_EINVAL, "%s is not aligned to its type", m.name);
   if (m.ld < cols || m.ld > (1LL << 36))
     return fail(MUONH_EINVAL, "%s's row pitch %lld out of [cols=%lld, 2^36]", m.name, (long long)m.ld, (long long)cols);
