@@ -12,13 +12,13 @@
 #include <algorithm>
 
 #include "fp8_codes.h"
+#include "norm_choice.h"
 #include "rows.h"
 
 namespace muonh {
 namespace norm {
 namespace {
 
-using fp8::ceil_div;
 using fp8::code_ld;
 using fp8::fail;
 using fp8::kBlock;
@@ -142,7 +142,8 @@ __device__ __forceinline__ void emit(const FwdArgs& a, int64_t row, int c, bool 
 }
 
 // LPR lanes share a row, NV vectors of 8 each: a row is read once and stays in
-// registers. A workgroup goes on to further rows with the weights it holds.
+// registers. A workgroup takes one set of rows, and further ones only in a call that would have more than
+// kMaxGrid workgroups.
 template <typename TX, typename TH, int LPR, int NV, int OUT>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void k_norm(FwdArgs a) {
   constexpr int kRows = LPR < 256 ? 256 / LPR : 1;
@@ -258,30 +259,26 @@ __global__ __launch_bounds__(1024) void k_norm_long(FwdArgs a) {
   }
 }
 
-constexpr int kMaxGrid = 1 << 20;  // workgroups of up to 1024 threads: below 2^32 threads
-
-// The lanes of a row: a wave where that holds it, four for the longest such rows and where rows are
-// few. bf16 with a residual into 8-bit rows of 2048, a wave and four: 1 row 4.1, 2.3 us; 256 rows 5.2, 3.4;
-// 4096 rows 13.5, 12.2; 8192 rows 22.3, 20.6; 16384 rows 41.7, 42.7. 8192 rows of 600 fp32 entries: 8.7, 10.5.
-// 131072 rows of 128 (16 lanes each) 13.0, at 5.2 TB/s.
 template <typename TX, typename TH, int OUT>
 void launch_norm(const FwdArgs& a, hipStream_t s) {
-  auto grid = [&](int per) { return dim3((unsigned)std::min<int64_t>(ceil_div(a.rows, per), kMaxGrid)); };
-  const int vecs = (int)ceil_div(a.cols, 8);
-#define MUONH_NORM(LPR, NV)                                                                              \
-  hipLaunchKernelGGL((k_norm<TX, TH, LPR, NV, OUT>), grid(LPR < 256 ? 256 / LPR : 1), dim3(LPR < 256 ? 256 : LPR), \
-                     0, s, a)
-  if (vecs <= 16) MUONH_NORM(16, 1);
-  else if (vecs <= 256 && (a.rows <= 256 || vecs > 192)) MUONH_NORM(256, 1);
-  else if (vecs <= 64) MUONH_NORM(64, 1);
-  else if (vecs <= 128) MUONH_NORM(64, 2);
-  else if (vecs <= 192) MUONH_NORM(64, 3);
-  else if (vecs <= 512) MUONH_NORM(256, 2);
-  else if (vecs <= 1024) MUONH_NORM(256, 4);
-  else if (vecs <= 2048) MUONH_NORM(1024, 2);
-  else if (vecs <= 4096) MUONH_NORM(1024, 4);
-  else hipLaunchKernelGGL((k_norm_long<TX, TH, OUT>), grid(1), dim3(1024), 0, s, a);
+  const Form f = forward_form(a.rows, a.cols);
+  const dim3 grid((unsigned)forward_groups(a.rows, f));
+#define MUONH_NORM(LPR, NV)             \
+  if (f.lanes == LPR && f.vecs == NV) { \
+    hipLaunchKernelGGL((k_norm<TX, TH, LPR, NV, OUT>), grid, dim3(LPR < 256 ? 256 : LPR), 0, s, a); \
+    return;                             \
+  }
+  MUONH_NORM(16, 1)
+  MUONH_NORM(64, 1)
+  MUONH_NORM(64, 2)
+  MUONH_NORM(64, 3)
+  MUONH_NORM(256, 1)
+  MUONH_NORM(256, 2)
+  MUONH_NORM(256, 4)
+  MUONH_NORM(1024, 2)
+  MUONH_NORM(1024, 4)
 #undef MUONH_NORM
+  hipLaunchKernelGGL((k_norm_long<TX, TH, OUT>), grid, dim3(1024), 0, s, a);
 }
 template <typename TX, typename TH>
 void launch_norm(const FwdArgs& a, Out out, hipStream_t s) {
@@ -491,41 +488,32 @@ __global__ __launch_bounds__(256) void k_norm_join(const float* part, int groups
   }
 }
 
-constexpr int kBackCols = 16384;  // longer rows go through k_norm_dots
-// Workgroups, and so partial sums of dw: as many as a chip holds, or fewer where joining the sums
-// costs more than that gains (main kernel and join, us: 131072 x 128 512 groups 22.2 + 4.7, 2048 18.5 + 4.6; 8192 x
-// 2048 512 27.6 + 3.9, 1024 30.5 + 4.2; 8192 x 4096 512 62 + 4.9, 1024 48.8 + 6.6, 2048 54.8 + 11.5).
-int back_groups(int64_t rows, int64_t cols) {
-  if (cols > kBackCols) return (int)std::min<int64_t>(rows, 64);
-  const int per = cols <= 128 ? 16 : cols <= 2048 ? 4 : 1;  // rows at a time
-  const int most = cols <= 128 ? 2048 : cols > 2048 && cols <= 8192 ? 1024 : 512;
-  return (int)std::min<int64_t>(ceil_div(rows, per), most);
-}
 size_t back_bytes(int64_t rows, int64_t cols) {
   const size_t part = (size_t)back_groups(rows, cols) * (size_t)cols * sizeof(float);
   return part + (cols > kBackCols ? (size_t)rows * sizeof(float) : 0);
 }
 
 template <typename TD, typename TH>
-void launch_back(BwdArgs a, hipStream_t s) {
-  const int vecs = (int)ceil_div(a.cols, 8);
+void launch_back(const BwdArgs& a, hipStream_t s) {
+  const Form f = backward_form(a.cols);
   const dim3 grid((unsigned)a.groups);
-#define MUONH_NORM(LPR, NV) \
-  hipLaunchKernelGGL((k_norm_back<TD, TH, LPR, NV>), grid, dim3(LPR < 256 ? 256 : LPR), 0, s, a)
-  if (vecs <= 16) MUONH_NORM(16, 1);
-  else if (vecs <= 64) MUONH_NORM(64, 1);
-  else if (vecs <= 128) MUONH_NORM(64, 2);
-  else if (vecs <= 192) MUONH_NORM(64, 3);
-  else if (vecs <= 256) MUONH_NORM(64, 4);
-  else if (vecs <= 512) MUONH_NORM(256, 2);
-  else if (vecs <= 1024) MUONH_NORM(256, 4);
-  else if (vecs <= 2048) MUONH_NORM(1024, 2);
-  else {
-    hipLaunchKernelGGL((k_norm_dots<TD, TH>), dim3((unsigned)std::min<int64_t>(a.rows, kMaxGrid)), dim3(1024), 0, s, a);
-    hipLaunchKernelGGL((k_norm_back_long<TD, TH>), dim3((unsigned)ceil_div(vecs, 256), (unsigned)a.groups), dim3(256),
-                       0, s, a);
+#define MUONH_NORM(LPR, NV)             \
+  if (f.lanes == LPR && f.vecs == NV) { \
+    hipLaunchKernelGGL((k_norm_back<TD, TH, LPR, NV>), grid, dim3(LPR < 256 ? 256 : LPR), 0, s, a); \
+    return;                             \
   }
+  MUONH_NORM(16, 1)
+  MUONH_NORM(64, 1)
+  MUONH_NORM(64, 2)
+  MUONH_NORM(64, 3)
+  MUONH_NORM(64, 4)
+  MUONH_NORM(256, 2)
+  MUONH_NORM(256, 4)
+  MUONH_NORM(1024, 2)
 #undef MUONH_NORM
+  hipLaunchKernelGGL((k_norm_dots<TD, TH>), dim3((unsigned)std::min<int64_t>(a.rows, kMaxGrid)), dim3(1024), 0, s, a);
+  hipLaunchKernelGGL((k_norm_back_long<TD, TH>), dim3((unsigned)ceil_div(ceil_div(a.cols, 8), 256), (unsigned)a.groups),
+                     dim3(256), 0, s, a);
 }
 
 // A mean over no columns is no number: refused.

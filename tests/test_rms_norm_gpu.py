@@ -135,6 +135,77 @@ def test_norm_in_8_bits(rows, cols, types):
             assert torch.equal(q.scales.view(torch.uint8), first.scales.view(torch.uint8))
 
 
+# 64 lanes with a vector each: more than 256 rows of 129 to 512 columns
+LANES_64 = [(300, 129), (300, 500), (257, 512), (261, 385)]
+
+
+@pytest.mark.parametrize("types", [("bf16", None), ("fp32", None), ("bf16", "bf16"), ("fp32", "fp32"), ("bf16", "fp32"), ("fp32", "bf16")])
+@pytest.mark.parametrize("rows,cols", LANES_64)
+def test_norm_by_64_lanes(rows, cols, types):
+    test_norm(rows, cols, types)
+    test_norm_in_8_bits(rows, cols, types)
+
+
+# more rows than a launch's workgroups take at once, by less than ENDS
+ENDS = 12
+TALL = [((4 << 20) + 9, 130), ((4 << 20) + 9, 515), ((4 << 20) + 9, 1025), ((1 << 20) + 5, 1537), ((1 << 20) + 5, 2049), ((1 << 20) + 5, 4097),
+        ((1 << 20) + 5, 8193), ((1 << 20) + 5, 16385), ((1 << 20) + 5, 32769)]
+
+
+def tall(rows, cols, seed, rest, scale=1.0):
+    """A bf16 matrix with values in its first and last ENDS rows, and these."""
+    if torch.cuda.mem_get_info()[0] < 4 * rows * cols + rest:
+        torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 4 * rows * cols + rest:
+        pytest.skip("not enough free memory")
+    x, ends = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda"), values(2 * ENDS, cols, seed, "bf16", scale)
+    x[:ENDS], x[-ENDS:] = ends[:ENDS], ends[ENDS:]
+    return x, ends
+
+
+def both_ends(t):
+    return torch.cat([t[:ENDS], t[-ENDS:]])
+
+
+@pytest.mark.parametrize("rows,cols", TALL)
+def test_rows_past_the_most_workgroups(rows, cols):
+    x, ends = tall(rows, cols, 1, 8 << 30)
+    w = weights(cols).abs()  # so that zeros have no sign
+    want = no.forward(f64(ends), f64(w), EPS)[0]
+    q, _, _, r = mh().rms_norm_fp8(x, w, eps=EPS)
+    assert float((r[ENDS:-ENDS] - 1e3).abs().max()) <= tol_r(cols) * 1e3
+    codes, scales = (both_ends(t.view(torch.uint8)) for t in (q.codes, q.scales))
+    check_codes(mh().Fp8Matrix(codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu), (2 * ENDS, cols)), want, tol_r(cols) + 2 * U)
+    rest = q.codes.view(torch.uint8)[ENDS:-ENDS]
+    assert int(rest.amax()) == 0
+    del q, rest
+    y, _, r = mh().rms_norm(x, w, eps=EPS)
+    check_y(both_ends(y), both_ends(r), ends, w)
+    assert float(y[ENDS:-ENDS].amax()) == float(y[ENDS:-ENDS].amin()) == 0
+
+
+# more rows than the gradient's workgroups take at once: dw is summed over a workgroup's sets of rows
+TURNS = [(33000, 128), (32800, 77), (2100, 300), (2100, 1001), (2100, 1500), (2100, 2047), (1030, 4095), (1030, 8190), (520, 16384), (515, 12001),
+         (70, 20000), (67, 16391)]
+
+
+@pytest.mark.parametrize("types", [("bf16", "fp32"), ("fp32", "bf16")])
+@pytest.mark.parametrize("rows,cols", TURNS)
+def test_gradient_over_further_rows(rows, cols, types):
+    test_gradient(rows, cols, types)
+
+
+def test_gradient_of_long_rows_past_the_most_workgroups():
+    rows, cols = (1 << 20) + 5, 16387
+    (h, hends), (dy, dends) = tall(rows, cols, 1, 48 << 30), tall(rows, cols, 2, 8 << 30, 1e-3)
+    w, r = weights(cols), torch.full((rows,), 1e3, device="cuda")
+    rends = torch.from_numpy(no.forward(f64(hends), f64(w), EPS)[1].astype(np.float32)).cuda()
+    r[:ENDS], r[-ENDS:] = rends[:ENDS], rends[ENDS:]
+    dh, dw = mh().rms_norm_backward(dy, h, w, r, out=dy)
+    check_back(both_ends(dh), dw, dends, hends, w, rends, None)
+    assert float(dh[ENDS:-ENDS].amax()) == float(dh[ENDS:-ENDS].amin()) == 0
+
+
 def check_back(dh, dw, dy, h, w, r, res):
     rows, cols = h.shape
     d64, h64, w64, r64 = f64(dy), f64(h), f64(w), f64(r)[:, None]
