@@ -491,7 +491,7 @@ int muonh_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t dy_ld, con
                             int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Embedding lookup: out[t] = scale * table[ids[t] - first], rounded once, for
+ * Embedding lookup: out[t] = scale * table[ids[t] - first] in fp32, then rounded to out's type, for
  * t < n; an id that is no row (below `first`, or first + rows or above: padding,
  * or a row of another part of a table split by rows) gives zeros.
  * ids: DEVICE, n integers of id_bytes (4 or 8) bytes, signed; n in [0,

@@ -1129,7 +1129,8 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, out_dtype=No
     rstd (rows, fp32) and h are what rms_norm_backward takes.
 
     x, residual: 2-d fp32 or bf16 tensors whose rows are contiguous, any row
-    stride, each of its own type; h has the residual's, and y is the norm of h as
+    stride, each of its own type (heads that lie in wider rows of tokens have no one
+    stride: copy them out first); h has the residual's, and y is the norm of h as
     stored. weight: fp32 vector. residual_out: a tensor for h, which may be
     `residual` or `x` itself. out: a tensor for y; otherwise a new one of out_dtype
     (default: h's type). Runs on the current stream of x's device, outside

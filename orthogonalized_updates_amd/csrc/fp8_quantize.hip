@@ -56,7 +56,8 @@ struct Args {
 // 103 (91).
 //
 // NORM: entry (r, c) is src's times rstd[r] times weight[c], in that order, in
-// fp32: RMS norm's output, whose row sums are there already (rms_norm.hip).
+// fp32: RMS norm's output, whose row sums are there already (rms_norm.hip). From bf16 the products take 64
+// registers beside the 32 of the pairs, 7 or 8 more than there are: 8192 x 2048 into both forms 17.3 us, 67 MB at 3.9 TB/s.
 template <bool BF, bool TILES, bool PLAIN, bool TRANS, bool NORM>
 __global__ __launch_bounds__(kThreads, 4) void k_quantize(Args a) {
   __shared__ __attribute__((aligned(16))) uint32_t red[4][kBlock / 2];  // maxima by wave

@@ -30,7 +30,7 @@ inline Form forward_form(int64_t rows, int64_t cols) {
   if (vecs <= 512) return {256, 2};
   if (vecs <= 1024) return {256, 4};
   if (vecs <= 2048) return {1024, 2};
-  if (vecs <= 4096) return {1024, 4};
+  if (vecs <= 4096) return {1024, 4};  // up to 45 registers more than there are
   return {0, 0};
 }
 // Of up to 1024 threads: below 2^32. Rows past these go to the same workgroups again.
